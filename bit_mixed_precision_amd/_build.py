@@ -14,7 +14,8 @@ LIB = os.path.join(_HERE, "libbq.so")
 # measurement kernels for the benchmark's achievable ceilings (not the library)
 CALIB_SRC = os.path.join(CSRC, "calib", "calib.hip")
 CALIB_LIB = os.path.join(_HERE, "libbq_calib.so")
-SOURCES = ["api.hip", "quantize.hip", "pack.hip", "gemv.hip", "gemv_nf4.hip", "gemm_stream.hip", "gemm_tiled.hip"]
+SOURCES = ["api.hip", "quantize.hip", "pack.hip", "gemv.hip", "gemv_nf4.hip", "gemm_stream.hip", "gemm_tiled.hip",
+           "api_layer.hip", "gemm_w4g.hip", "qk_rope.hip", "attn_kv4.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -48,7 +48,23 @@ SIGNATURES = {
     "bq_gemm_splitk": [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I64, _P],
     "bq_gemm_splitk_static": [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P],
 }
-_RESTYPES = {"bq_status_string": ctypes.c_char_p, "bq_gemm_splitk_workspace_bytes": ctypes.c_int64}
+_F32, _F64 = ctypes.c_float, ctypes.c_double
+# the same for include/bq_layer.h
+LAYER_SIGNATURES = {
+    "bq_gemm_w4g_a16": [_P, _I, _P, _P, _P, _I, _P, _I64, _I64, _I64, _P, _I64, _P],
+    "bq_gemm_w4g_workspace_bytes": [_I64, _I64, _I64],
+    "bq_qk_norm_rope": [_P, _I64, _P, _I64, _I, _I64, _I, _I, _I, _P, _P, _F64, _P, _P, _I64, _I, _I, _P, _P, _P, _P],
+    "bq_kv4_page_bytes": [_I, _I, _I],
+    "bq_qk_norm_rope_kv4": [_P, _I64, _P, _I64, _P, _I64, _I, _I64, _I, _I, _I, _P, _P, _F64, _P, _P, _I64, _I, _I, _P,
+                            _P, _P, _I64, _I, _P, _P],
+    "bq_kv4_read": [_P, _I64, _I, _I, _I, _P, _I64, _I, _P, _P, _P],
+    "bq_attn_kv4": [_P, _I64, _I, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _I, _I64, _F32, _I64, _P, _P, _P,
+                    _I64, _P],
+    "bq_attn_kv4_workspace_bytes": [_I64, _I64, _I, _I, _I, _I64],
+}
+_RESTYPES = {"bq_status_string": ctypes.c_char_p, "bq_gemm_splitk_workspace_bytes": ctypes.c_int64,
+             "bq_gemm_w4g_workspace_bytes": ctypes.c_int64, "bq_kv4_page_bytes": ctypes.c_int64,
+             "bq_attn_kv4_workspace_bytes": ctypes.c_int64}
 
 
 class BQError(RuntimeError):
@@ -69,7 +85,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build the HIP library first "
                 "(python -c 'import __graft_entry__ as g; g.build()')")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, args in SIGNATURES.items():
+        for name, args in {**SIGNATURES, **LAYER_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = _RESTYPES.get(name, ctypes.c_int)
@@ -420,3 +436,261 @@ def gemm_nf4_a16(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
     _check_tensor(out, "out", torch.float16, (M, N), dev)
     _call("bq_gemm_nf4_a16", dev, _ptr(A), _ptr(B), _ptr(scale), _ptr(zero), _ptr(out), M, N, K)
     return out
+
+
+# --------------------------------------------------------------------------
+# decoder-layer operators (include/bq_layer.h)
+# --------------------------------------------------------------------------
+
+_DTYPES16 = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _dtype16(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES16:
+        raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    return _DTYPES16[t.dtype]
+
+
+def _check_rows(t: torch.Tensor, name: str, dtype, tokens, heads, dim, device) -> int:
+    """A [tokens, heads, dim] tensor, dense within a token; the elements
+    between its tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name} must have shape {(tokens, heads, dim)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if (s[2] != 1 and dim > 1) or (s[1] != dim and heads > 1):
+        raise ValueError(f"{name} must be dense within a token")
+    return s[0] if tokens > 1 else heads * dim
+
+
+def _workspace(t: Optional[torch.Tensor], nbytes: int, device) -> Optional[torch.Tensor]:
+    if t is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes else None
+    _check_tensor(t, "workspace", torch.uint8, None, device)
+    return t
+
+
+def gemm_w4g_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Device workspace bytes with which gemm_w4g_a16 splits K for this shape
+    (0: it does not)."""
+    n = lib().bq_gemm_w4g_workspace_bytes(M, N, K)
+    if n < 0:
+        raise BQError(-n, "bq_gemm_w4g_workspace_bytes")
+    return n
+
+
+def gemm_w4g_a16(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """4-bit weights with group scales: C = sum_k A[m,k] (c[n,k] - zero[n,g])
+    scale[n,g], g = k // group, with fp32 accumulation, of A's type.
+
+    A fp16 or bf16 [M, K]; B uint8 [N, K/2] (pack_int4's layout, codes
+    -8..7); scale, zero fp16 [N, K/group], group 32, 64 or 128 (quantize_pack
+    of the weight viewed as [N * K/group, group] gives B and scale).  A
+    workspace is allocated for the call when it needs one and none is given."""
+    dt = _dtype16(A, "A")
+    if A.dim() != 2 or B.dim() != 2 or scale.dim() != 2:
+        raise ValueError("A, B and scale must be 2-D")
+    M, K = A.shape
+    N = B.shape[0]
+    dev = A.device
+    _check_tensor(A, "A", A.dtype)
+    _check_tensor(B, "B", torch.uint8, (N, K // 2), dev)
+    groups = scale.shape[1]
+    if K and (groups == 0 or K % groups):
+        raise ValueError("scale must have K/group columns")
+    group = K // groups if K else 32
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    _check_tensor(scale, "scale", torch.float16, (N, groups), dev)
+    if zero is not None:
+        _check_tensor(zero, "zero", torch.float16, (N, groups), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=A.dtype, device=dev)
+    _check_tensor(out, "out", A.dtype, (M, N), dev)
+    ws = _workspace(workspace, gemm_w4g_workspace_bytes(M, N, K), dev)
+    _call("bq_gemm_w4g_a16", dev, _ptr(A), dt, _ptr(B), _ptr(scale), _ptr(zero), group, _ptr(out), M, N, K, _ptr(ws),
+          ws.numel() if ws is not None else 0)
+    return out
+
+
+def _rope_args(q, k, cos, sin, positions, q_weight, k_weight):
+    dt = _dtype16(k, "k")
+    if k.dim() != 3:
+        raise ValueError("k must be 3-D [tokens, heads, head_dim]")
+    tokens, hkv, dim = k.shape
+    dev, dtype = k.device, k.dtype
+    ks = _check_rows(k, "k", dtype, tokens, hkv, dim, dev)
+    hq, qs = 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be 3-D [tokens, heads, head_dim]")
+        hq = q.shape[1]
+        qs = _check_rows(q, "q", dtype, tokens, hq, dim, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _check_tensor(w, name, dtype, (dim,), dev)
+    rot, max_pos = 0, 0
+    if cos is not None:
+        if sin is None or positions is None:
+            raise ValueError("cos needs sin and positions")
+        if cos.dim() != 2:
+            raise ValueError("cos must be 2-D [max_pos, rot_dim/2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _check_tensor(cos, "cos", torch.float32, None, dev)
+        _check_tensor(sin, "sin", torch.float32, cos.shape, dev)
+        _check_tensor(positions, "positions", torch.int32, (tokens,), dev)
+    return dt, dtype, dev, tokens, hq, hkv, dim, qs, ks, rot, max_pos
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch.Tensor],
+                 positions: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """The norm of each head of q [tokens, q_heads, head_dim] and k [tokens,
+    kv_heads, head_dim] (fp16 or bf16, dense within a token) with weights
+    [head_dim] (None: no norm), and the rotation of the first rot_dim channels
+    by cos / sin fp32 [max_pos, rot_dim/2] at positions int32 [tokens] (None:
+    no rotation), in one pass -> (q_out, k_out).  A token whose position is
+    outside the table is left out: its outputs are not written."""
+    dt, dtype, dev, tokens, hq, hkv, dim, qs, ks, rot, max_pos = _rope_args(q, k, cos, sin, positions, q_weight, k_weight)
+    if q_out is None:
+        q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty((tokens, hkv, dim), dtype=dtype, device=dev)
+    _check_tensor(q_out, "q_out", dtype, (tokens, hq, dim), dev)
+    _check_tensor(k_out, "k_out", dtype, (tokens, hkv, dim), dev)
+    _call("bq_qk_norm_rope", dev, _ptr(q), qs, _ptr(k), ks, dt, tokens, hq, hkv, dim, _ptr(q_weight), _ptr(k_weight), eps,
+          _ptr(cos), _ptr(sin), max_pos, rot, int(interleaved), _ptr(positions), _ptr(q_out), _ptr(k_out))
+    return q_out, k_out
+
+
+def kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of a page of the 4-bit cache; a cache is a uint8 tensor
+    [num_pages, kv4_page_bytes(...)] (its layout: include/bq_layer.h)."""
+    n = lib().bq_kv4_page_bytes(kv_heads, head_dim, page_size)
+    if n < 0:
+        raise BQError(-n, "bq_kv4_page_bytes")
+    return n
+
+
+def _check_cache(cache, kv_heads, head_dim, page_size, dev):
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 2:
+        raise ValueError("cache must be a 2-D tensor [num_pages, page bytes]")
+    _check_tensor(cache, "cache", torch.uint8, (cache.shape[0], kv4_page_bytes(kv_heads, head_dim, page_size)), dev)
+    return cache.shape[0]
+
+
+def qk_norm_rope_kv4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor],
+                     sin: Optional[torch.Tensor], positions: Optional[torch.Tensor], cache: torch.Tensor,
+                     slots: torch.Tensor, page_size: int, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                     q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """qk_norm_rope with the keys (rounded to their type) and the values v
+    written to the 4-bit cache at slots int64 [tokens] (page * page_size +
+    offset, each at most once; outside the cache: not written) -> q_out.  q
+    None: keys and values only."""
+    dt, dtype, dev, tokens, hq, hkv, dim, qs, ks, rot, max_pos = _rope_args(q, k, cos, sin, positions, q_weight, k_weight)
+    vs = _check_rows(v, "v", dtype, tokens, hkv, dim, dev)
+    pages = _check_cache(cache, hkv, dim, page_size, dev)
+    _check_tensor(slots, "slots", torch.int64, (tokens,), dev)
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=dev)
+        _check_tensor(q_out, "q_out", dtype, (tokens, hq, dim), dev)
+    _call("bq_qk_norm_rope_kv4", dev, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, dt, tokens, hq, hkv, dim, _ptr(q_weight),
+          _ptr(k_weight), eps, _ptr(cos), _ptr(sin), max_pos, rot, int(interleaved), _ptr(positions), _ptr(q_out),
+          _ptr(cache), pages, page_size, _ptr(slots))
+    return q_out
+
+
+def kv4_read(cache: torch.Tensor, slots: torch.Tensor, page_size: int, kv_heads: int, head_dim: int,
+             dtype: torch.dtype = torch.float16, k_out: Optional[torch.Tensor] = None,
+             v_out: Optional[torch.Tensor] = None):
+    """The keys and values at slots int64 [tokens] of the 4-bit cache, dense
+    [tokens, kv_heads, head_dim] of dtype -> (k, v).  A slot outside the cache
+    leaves its rows as they were."""
+    if dtype not in _DTYPES16:
+        raise ValueError("dtype must be float16 or bfloat16")
+    dev = cache.device
+    pages = _check_cache(cache, kv_heads, head_dim, page_size, dev)
+    if slots.dim() != 1:
+        raise ValueError("slots must be 1-D")
+    _check_tensor(slots, "slots", torch.int64, None, dev)
+    shape = (slots.shape[0], kv_heads, head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    _check_tensor(k_out, "k_out", dtype, shape, dev)
+    _check_tensor(v_out, "v_out", dtype, shape, dev)
+    _call("bq_kv4_read", dev, _ptr(cache), pages, page_size, kv_heads, head_dim, _ptr(slots), shape[0], _DTYPES16[dtype],
+          _ptr(k_out), _ptr(v_out))
+    return k_out, v_out
+
+
+def attn_kv4_workspace_bytes(batch: int, max_q_len: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
+    """Device workspace bytes with which attn_kv4 splits sequences of up to
+    max_len keys (0: it does not)."""
+    n = lib().bq_attn_kv4_workspace_bytes(batch, max_q_len, q_heads, kv_heads, head_dim, max_len)
+    if n < 0:
+        raise BQError(-n, "bq_attn_kv4_workspace_bytes")
+    return n
+
+
+def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int,
+             kv_heads: int, scale: Optional[float] = None, q_start: Optional[torch.Tensor] = None,
+             max_q_len: Optional[int] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None, return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Attention of q [total_q, q_heads, head_dim] (fp16 or bf16, dense within
+    a token) over the 4-bit cache: sequence b's queries stand at the end of
+    its seq_lens[b] cached keys (int32 [batch]), found through block_table
+    int32 [batch, max_blocks]; causal, within the last `window` keys if
+    window > 0.  q_start int32 [batch + 1] gives each sequence's queries, at
+    most max_q_len; None: total_q / batch each.  scale None: head_dim ** -0.5.
+
+    -> out, of q's shape and type; (out, lse) with return_lse or lse given:
+    lse fp32 [total_q, q_heads].  A row with no keys gives zeros (lse -inf).
+    A workspace is allocated for the call when it needs one and none is
+    given."""
+    dt = _dtype16(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [total_q, q_heads, head_dim]")
+    total, hq, dim = q.shape
+    dev, dtype = q.device, q.dtype
+    qs = _check_rows(q, "q", dtype, total, hq, dim, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [batch, max_blocks]")
+    batch, blocks = block_table.shape
+    _check_tensor(block_table, "block_table", torch.int32, None, dev)
+    _check_tensor(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    pages = _check_cache(cache, kv_heads, dim, page_size, dev)
+    if q_start is None:
+        if batch == 0 or total % batch:
+            raise ValueError("without q_start every sequence has total_q / batch queries")
+        if max_q_len is not None and max_q_len != total // batch:
+            raise ValueError("max_q_len must be total_q / batch without q_start")
+        max_q_len = total // batch
+    else:
+        if max_q_len is None:
+            raise ValueError("q_start needs max_q_len")
+        _check_tensor(q_start, "q_start", torch.int32, (batch + 1,), dev)
+    if out is None:
+        out = torch.empty((total, hq, dim), dtype=dtype, device=dev)
+    _check_tensor(out, "out", dtype, (total, hq, dim), dev)
+    if lse is None and return_lse:
+        lse = torch.empty((total, hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _check_tensor(lse, "lse", torch.float32, (total, hq), dev)
+    ws = _workspace(workspace, attn_kv4_workspace_bytes(batch, max_q_len, hq, kv_heads, dim, blocks * page_size), dev)
+    _call("bq_attn_kv4", dev, _ptr(q), qs, dt, _ptr(q_start), _ptr(seq_lens), _ptr(block_table), batch, total, max_q_len, hq,
+          kv_heads, dim, _ptr(cache), pages, page_size, blocks, dim ** -0.5 if scale is None else scale, window, _ptr(out),
+          _ptr(lse), _ptr(ws), ws.numel() if ws is not None else 0)
+    return (out, lse) if lse is not None else out

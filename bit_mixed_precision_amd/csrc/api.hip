@@ -40,14 +40,7 @@ int check_device()
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
-// A launcher's grid check (kGridTooLarge) is a shape error; nothing was
-// launched.  Any other failure is the runtime's.
-int launch_status(hipError_t e)
-{
-    if (e == hipSuccess)
-        return BQ_OK;
-    return e == bq::kGridTooLarge ? BQ_ERR_SHAPE : BQ_ERR_HIP;
-}
+using bq::launch_status;
 
 // Largest M handled by the streaming kernel (when asked for), and the largest
 // M for which automatic dispatch takes it.  Below the MI355X ridge point
@@ -95,6 +88,21 @@ int validate_gemm(const int8_t *A, const void *B, int bits, const void *scale, v
 }
 
 }  // namespace
+
+namespace bq {
+
+int device_status() { return check_device(); }
+
+// A launcher's grid check (kGridTooLarge) is a shape error; nothing was
+// launched.  Any other failure is the runtime's.
+int launch_status(hipError_t e)
+{
+    if (e == hipSuccess)
+        return BQ_OK;
+    return e == kGridTooLarge ? BQ_ERR_SHAPE : BQ_ERR_HIP;
+}
+
+}  // namespace bq
 
 extern "C" {
 

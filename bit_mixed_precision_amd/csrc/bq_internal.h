@@ -115,4 +115,59 @@ hipError_t launch_gemm_nf4(const uint16_t *A, const uint8_t *B, const uint16_t *
 hipError_t launch_gemv_nf4(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero,
                            uint16_t *C, int M, int N, int K, hipStream_t s);
 
+// Checks that the current device is gfx950 (a bq_status), once per device.
+int device_status();
+// The bq_status of a launcher's result.
+int launch_status(hipError_t e);
+
+// Query/key norm and rotation (decoder-layer operators, include/bq_layer.h).
+// cache == nullptr: keys go to k_out, else keys and values to the cache.
+struct QkRopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const uint16_t *q_weight, *k_weight;
+    double eps;
+    const float *cos, *sin;
+    const int32_t *positions;
+    int64_t max_pos;
+    int rot, inter;
+    int64_t tokens;
+    int hq, hkv, D;
+    uint16_t *q_out, *k_out;
+    uint8_t *cache;
+    int64_t num_pages;
+    int page_size;
+    const int64_t *slots;
+};
+hipError_t launch_qk_norm_rope(const QkRopeArgs &p, bool bf16, hipStream_t s);
+hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_size, int hkv, int D, const int64_t *slots,
+                           int64_t tokens, uint16_t *k, uint16_t *v, bool bf16, hipStream_t s);
+
+// Attention over the 4-bit paged cache.
+struct AttnKv4Args {
+    const void *q;
+    int64_t q_stride;
+    const int32_t *q_start, *seq_lens, *block_table;
+    int batch, total_q, max_q_len;
+    int hq, hkv, group;
+    const uint8_t *cache;
+    int64_t num_pages;
+    int page_shift, max_blocks;
+    float scale;
+    int window;
+    void *out;
+    float *lse;
+    int row_tiles, nsplit;
+    float *part, *part_ml;
+};
+// Splits of the keys for this many (sequence, kv head, 16-row tile) items.
+int attn_kv4_splits(int64_t items, int64_t max_len);
+hipError_t launch_attn_kv4(const AttnKv4Args &p, int D, bool bf16, hipStream_t s);
+
+// 4-bit weights with group scales times 16-bit activations.  A call whose
+// outputs are few splits K over workgroups through `ws` when it is given.
+int64_t gemm_w4g_workspace_bytes(int M, int N, int K);
+hipError_t launch_gemm_w4g(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int group,
+                           uint16_t *C, int M, int N, int K, bool bf16, float *ws, int64_t wsBytes, hipStream_t s);
+
 }  // namespace bq

@@ -1,0 +1,307 @@
+// The step between the QKV product and attention, one pass over its rows:
+//   y = x * rsqrt(mean(x^2) + eps) * w       per head (w absent: y = x)
+//   (a, b) -> (a cos - b sin, b cos + a sin) on the first rot_dim channels,
+// pairs (i, i + rot_dim/2) or (2i, 2i + 1), one rounding to the 16-bit type;
+// and, with a cache, keys and values quantized to 4 bits per token and head:
+//   min = fp16(min y), scale = fp16((max y - min) / 15),
+//   code = rint((y - min) / scale) in 0..15     (fp32, correctly rounded).
+//
+// Layout: D/8 lanes per head row, eight channels (16 bytes) a lane, so a
+// wavefront covers 512 channels with one load instruction; the norm's sum and
+// the quantizer's range are butterfly reductions inside the row's lanes, and
+// a rotation pair in halves is a lane rot_dim/16 away.  Bound by moving the
+// rows (and by launch latency at decode sizes).
+//
+// Keys that go to the cache are normalized and rotated in fp64 (fp64 runs at
+// the fp32 rate on this chip): a code turns over at a border between two
+// values, and with 53 bits the rounded key, hence the code, is the
+// definition's.  Queries (and keys without a cache) take fp32.
+#include "bq_internal.h"
+#include "dtype16.h"
+
+namespace bq {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename F, int LPR>
+__device__ __forceinline__ F row_sum(F v)
+{
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1)
+        v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+__device__ __forceinline__ float inv_rms(float ms) { return __builtin_amdgcn_rsqf(ms); }
+__device__ __forceinline__ double inv_rms(double ms) { return 1.0 / sqrt(ms); }
+
+// Norm and rotation of one lane's eight channels in type F; the result in
+// the 16-bit type's bits (through fp32, as a conversion from fp64 goes).
+template <typename T, typename F, int LPR>
+__device__ __forceinline__ void norm_rope(const uint4 raw, const uint16_t *w, double eps, const float *cs, const float *sn,
+                                          int rot, int inter, int sub, uint16_t out[8])
+{
+    F y[8];
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = (F)T::to_f32(r[i] & 0xffffu);
+        y[2 * i + 1] = (F)T::to_f32(r[i] >> 16);
+    }
+    if (w) {
+        F ss = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            ss += y[i] * y[i];
+        const F inv = inv_rms(row_sum<F, LPR>(ss) * (F)(1.0 / (8 * LPR)) + (F)eps);
+        const uint4 wr = *(const uint4 *)(w + 8 * sub);
+        const uint32_t wv[4] = {wr.x, wr.y, wr.z, wr.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = y[2 * i] * inv * (F)T::to_f32(wv[i] & 0xffffu);
+            y[2 * i + 1] = y[2 * i + 1] * inv * (F)T::to_f32(wv[i] >> 16);
+        }
+    }
+    const bool in = 8 * sub < rot;  // rot is a multiple of 16: whole lanes
+    if (inter) {
+        if (in) {
+            const float4 c = *(const float4 *)(cs + 4 * sub), s = *(const float4 *)(sn + 4 * sub);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F a = y[2 * i], b = y[2 * i + 1];
+                y[2 * i] = a * (F)cc[i] - b * (F)ss[i];
+                y[2 * i + 1] = b * (F)cc[i] + a * (F)ss[i];
+            }
+        }
+    } else if (rot) {
+        const int hl = rot / 16;  // lanes of one half
+        const bool first = sub < hl;
+        const int lane = threadIdx.x & 63;
+        const int partner = in ? lane + (first ? hl : -hl) : lane;
+        F o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = __shfl(y[i], partner, 64);
+        if (in) {
+            const int at = 8 * (first ? sub : sub - hl);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 c = *(const float4 *)(cs + at + 4 * h), s = *(const float4 *)(sn + at + 4 * h);
+                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 4 * h + i;
+                    y[j] = first ? y[j] * (F)cc[i] - o[j] * (F)ss[i] : y[j] * (F)cc[i] + o[j] * (F)ss[i];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        out[i] = T::from_f32((float)y[i]);
+}
+
+__device__ __forceinline__ uint4 pack8(const uint16_t o[8])
+{
+    return make_uint4(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16, o[4] | (uint32_t)o[5] << 16,
+                      o[6] | (uint32_t)o[7] << 16);
+}
+
+// Bytes of one head of one page: K codes, V codes, K and V parameters.
+__device__ __forceinline__ int64_t head_base(int64_t page, int head, int hkv, int page_size, int D)
+{
+    return (page * hkv + head) * (int64_t)page_size * (D + 8);
+}
+
+template <typename T, int LPR>
+__device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8_t *base, int tok, int page_size, int sub)
+{
+    constexpr int D = 8 * LPR;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = T::to_f32(x16[i]);
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) {
+        lo = fminf(lo, __shfl_xor(lo, off, 64));
+        hi = fmaxf(hi, __shfl_xor(hi, off, 64));
+    }
+    // the stored parameters are fp16: bf16 values past its range are held at its ends
+    const float mn = (float)(_Float16)fminf(fmaxf(lo, -65504.0f), 65504.0f);
+    const float sc = (float)(_Float16)fminf((hi - mn) / 15.0f, 65504.0f);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = sc > 0.0f ? fminf(fmaxf(rintf((x[i] - mn) / sc), 0.0f), 15.0f) : 0.0f;
+        w |= (uint32_t)q << (4 * i);
+    }
+    if (!isV) {
+        *(uint32_t *)(base + tok * (D / 2) + 4 * sub) = w;
+    } else {
+        uint8_t *v = base + page_size * (D / 2) + (tok >> 2) * (2 * D);
+        if constexpr (D >= 128) {
+            *(uint32_t *)(v + 16 * sub + 4 * (tok & 3)) = w;
+        } else {
+            *(uint16_t *)(v + 16 * sub + 2 * (tok & 3)) = (uint16_t)w;
+            *(uint16_t *)(v + 16 * sub + 8 + 2 * (tok & 3)) = (uint16_t)(w >> 16);
+        }
+    }
+    if (sub == 0)
+        *(uint32_t *)(base + page_size * D + (isV ? 4 * page_size : 0) + 4 * tok) =
+            F16::from_f32(sc) | (uint32_t)F16::from_f32(mn) << 16;
+}
+
+template <typename T, int LPR, bool CACHE>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs p)
+{
+    constexpr int D = 8 * LPR;
+    const int heads = p.hq + p.hkv * (CACHE ? 2 : 1);
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const int sub = threadIdx.x % LPR;
+    const int64_t tok = row / heads;
+    const int head = (int)(row - tok * heads);
+    if (tok >= p.tokens)
+        return;
+    // a row's lanes take one path together: every shuffle stays inside a row
+    int64_t pos = 0;
+    if (p.rot) {
+        pos = p.positions[tok];
+        if (pos < 0 || pos >= p.max_pos)
+            return;
+    }
+    const float *cs = p.cos + pos * (p.rot / 2), *sn = p.sin + pos * (p.rot / 2);
+    uint16_t o[8];
+    if (head < p.hq) {
+        const uint4 raw = *(const uint4 *)(p.q + tok * p.q_stride + head * D + 8 * sub);
+        norm_rope<T, float, LPR>(raw, p.q_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
+        *(uint4 *)(p.q_out + (tok * p.hq + head) * D + 8 * sub) = pack8(o);
+    } else if constexpr (!CACHE) {
+        const int h = head - p.hq;
+        const uint4 raw = *(const uint4 *)(p.k + tok * p.k_stride + h * D + 8 * sub);
+        norm_rope<T, float, LPR>(raw, p.k_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
+        *(uint4 *)(p.k_out + (tok * p.hkv + h) * D + 8 * sub) = pack8(o);
+    } else {
+        const bool isV = head >= p.hq + p.hkv;
+        const int h = head - p.hq - (isV ? p.hkv : 0);
+        const int64_t slot = p.slots[tok];
+        if (slot < 0 || slot >= p.num_pages * p.page_size)
+            return;
+        const uint16_t *src = isV ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
+        const uint4 raw = *(const uint4 *)(src + h * D + 8 * sub);
+        if (isV) {
+            const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = (uint16_t)r[i];
+                o[2 * i + 1] = (uint16_t)(r[i] >> 16);
+            }
+        } else {
+            norm_rope<T, double, LPR>(raw, p.k_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
+        }
+        const int64_t page = slot / p.page_size;
+        store_kv4<T, LPR>(o, isV, p.cache + head_base(page, h, p.hkv, p.page_size, D), (int)(slot - page * p.page_size),
+                          p.page_size, sub);
+    }
+}
+
+// Eight channels a lane of K or V of one token: codes and parameters to the
+// 16-bit type, T(fp32(code * scale) + min): the product is exact.
+template <typename T, int LPR>
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(const uint8_t *cache, int64_t num_pages, int page_size, int hkv,
+                                                            const int64_t *slots, int64_t tokens, uint16_t *k, uint16_t *v)
+{
+    constexpr int D = 8 * LPR;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const int sub = threadIdx.x % LPR;
+    const int64_t tok = row / (2 * hkv);
+    if (tok >= tokens)
+        return;
+    const int head = (int)(row - tok * 2 * hkv);
+    const bool isV = head >= hkv;
+    const int h = isV ? head - hkv : head;
+    const int64_t slot = slots[tok];
+    if (slot < 0 || slot >= num_pages * page_size)
+        return;
+    const int64_t page = slot / page_size;
+    const int t = (int)(slot - page * page_size);
+    const uint8_t *base = cache + head_base(page, h, hkv, page_size, D);
+    uint32_t w;
+    if (!isV) {
+        w = *(const uint32_t *)(base + t * (D / 2) + 4 * sub);
+    } else {
+        const uint8_t *b = base + page_size * (D / 2) + (t >> 2) * (2 * D) + 16 * sub;
+        if constexpr (D >= 128)
+            w = *(const uint32_t *)(b + 4 * (t & 3));
+        else
+            w = *(const uint16_t *)(b + 2 * (t & 3)) | (uint32_t)*(const uint16_t *)(b + 8 + 2 * (t & 3)) << 16;
+    }
+    const uint32_t par = *(const uint32_t *)(base + page_size * D + (isV ? 4 * page_size : 0) + 4 * t);
+    const float sc = half_bits(par & 0xffffu), mn = half_bits(par >> 16);
+    uint16_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] = T::from_f32((float)((w >> (4 * i)) & 15u) * sc + mn);
+    *(uint4 *)((isV ? v : k) + (tok * hkv + h) * D + 8 * sub) = pack8(o);
+}
+
+template <typename T, bool CACHE>
+hipError_t launch_rope_t(const QkRopeArgs &p, int64_t rows, hipStream_t s)
+{
+    const int per = kThreads / (p.D / 8);
+    const int64_t wgs = (rows + per - 1) / per;
+    if (!grid_fits(wgs, kThreads))
+        return kGridTooLarge;
+    const dim3 grid((unsigned)wgs);
+    if (p.D == 64)
+        qk_norm_rope_kernel<T, 8, CACHE><<<grid, kThreads, 0, s>>>(p);
+    else if (p.D == 128)
+        qk_norm_rope_kernel<T, 16, CACHE><<<grid, kThreads, 0, s>>>(p);
+    else
+        qk_norm_rope_kernel<T, 32, CACHE><<<grid, kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_read_t(const uint8_t *cache, int64_t num_pages, int page_size, int hkv, int D, const int64_t *slots,
+                         int64_t tokens, uint16_t *k, uint16_t *v, hipStream_t s)
+{
+    const int per = kThreads / (D / 8);
+    const int64_t wgs = (tokens * 2 * hkv + per - 1) / per;
+    if (!grid_fits(wgs, kThreads))
+        return kGridTooLarge;
+    const dim3 grid((unsigned)wgs);
+    if (D == 64)
+        kv4_read_kernel<T, 8><<<grid, kThreads, 0, s>>>(cache, num_pages, page_size, hkv, slots, tokens, k, v);
+    else if (D == 128)
+        kv4_read_kernel<T, 16><<<grid, kThreads, 0, s>>>(cache, num_pages, page_size, hkv, slots, tokens, k, v);
+    else
+        kv4_read_kernel<T, 32><<<grid, kThreads, 0, s>>>(cache, num_pages, page_size, hkv, slots, tokens, k, v);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const QkRopeArgs &p, bool bf16, hipStream_t s)
+{
+    const int64_t rows = p.tokens * (p.hq + (int64_t)p.hkv * (p.cache ? 2 : 1));
+    if (p.cache)
+        return bf16 ? launch_rope_t<BF16, true>(p, rows, s) : launch_rope_t<F16, true>(p, rows, s);
+    return bf16 ? launch_rope_t<BF16, false>(p, rows, s) : launch_rope_t<F16, false>(p, rows, s);
+}
+
+hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_size, int hkv, int D, const int64_t *slots,
+                           int64_t tokens, uint16_t *k, uint16_t *v, bool bf16, hipStream_t s)
+{
+    return bf16 ? launch_read_t<BF16>(cache, num_pages, page_size, hkv, D, slots, tokens, k, v, s)
+                : launch_read_t<F16>(cache, num_pages, page_size, hkv, D, slots, tokens, k, v, s);
+}
+
+}  // namespace bq

@@ -383,4 +383,7 @@ int bq_gemm_select_path(int64_t M, int64_t N, int64_t K, int bits);
 }
 #endif
 
+/* The operators of a low-bit decoder layer around these products. */
+#include "bq_layer.h"
+
 #endif /* BQ_H */
