@@ -9,6 +9,7 @@ library is missing or the device is not gfx950 the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -442,6 +443,10 @@ def gemm_nf4_a16(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
 # decoder-layer operators (include/bq_layer.h)
 # --------------------------------------------------------------------------
 
+# These calls are made many times per token, so their marshalling is kept
+# short: one combined test per tensor (the named checks only say what failed),
+# plain integers for pointers, sizes that depend on integers alone remembered.
+
 _DTYPES16 = {torch.float16: 0, torch.bfloat16: 1}
 
 
@@ -453,37 +458,67 @@ def _dtype16(t: torch.Tensor, name: str) -> int:
     return _DTYPES16[t.dtype]
 
 
-def _check_rows(t: torch.Tensor, name: str, dtype, tokens, heads, dim, device) -> int:
+def _dense(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """The address of a dense GPU tensor of this type, shape (None: any) and
+    device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_cuda and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        _check_tensor(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """A [tokens, heads, dim] tensor, dense within a token; the elements
     between its tokens."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != (tokens, heads, dim):
-        raise ValueError(f"{name} must have shape {(tokens, heads, dim)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    tokens, heads, dim = shape
     s = t.stride()
-    if (s[2] != 1 and dim > 1) or (s[1] != dim and heads > 1):
+    if s[2] != 1 or (s[1] != dim and heads > 1):
         raise ValueError(f"{name} must be dense within a token")
     return s[0] if tokens > 1 else heads * dim
 
 
-def _workspace(t: Optional[torch.Tensor], nbytes: int, device) -> Optional[torch.Tensor]:
+def _enqueue(name: str, device: torch.device, *args):
+    """The C call of this name on the device's current torch stream."""
+    if torch.cuda.current_device() != device.index:
+        _call(name, device, *args)
+        return
+    st = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if st != BQ_OK:
+        raise BQError(st, name)
+
+
+@functools.lru_cache(maxsize=4096)
+def _host_bytes(name: str, *args) -> int:
+    """A size that the library computes from integers alone."""
+    n = getattr(lib(), name)(*args)
+    if n < 0:
+        raise BQError(-n, name)
+    return n
+
+
+def _workspace(t: Optional[torch.Tensor], nbytes: int, device):
+    """(tensor, address, bytes) of the workspace given or allocated; the
+    tensor is held until the call is enqueued."""
     if t is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes else None
-    _check_tensor(t, "workspace", torch.uint8, None, device)
-    return t
+        if not nbytes:
+            return None, None, 0
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return t, t.data_ptr(), nbytes
+    return t, _dense(t, "workspace", torch.uint8, None, device), t.numel()
 
 
 def gemm_w4g_workspace_bytes(M: int, N: int, K: int) -> int:
     """Device workspace bytes with which gemm_w4g_a16 splits K for this shape
     (0: it does not)."""
-    n = lib().bq_gemm_w4g_workspace_bytes(M, N, K)
-    if n < 0:
-        raise BQError(-n, "bq_gemm_w4g_workspace_bytes")
-    return n
+    return _host_bytes("bq_gemm_w4g_workspace_bytes", M, N, K)
 
 
 def gemm_w4g_a16(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
@@ -499,55 +534,50 @@ def gemm_w4g_a16(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, zero: Op
     if A.dim() != 2 or B.dim() != 2 or scale.dim() != 2:
         raise ValueError("A, B and scale must be 2-D")
     M, K = A.shape
-    N = B.shape[0]
-    dev = A.device
-    _check_tensor(A, "A", A.dtype)
-    _check_tensor(B, "B", torch.uint8, (N, K // 2), dev)
-    groups = scale.shape[1]
+    N, groups = scale.shape
+    dev, dtype = A.device, A.dtype
+    a = _dense(A, "A", dtype, None, dev)
+    b = _dense(B, "B", torch.uint8, (N, K // 2), dev)
     if K and (groups == 0 or K % groups):
         raise ValueError("scale must have K/group columns")
     group = K // groups if K else 32
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
-    _check_tensor(scale, "scale", torch.float16, (N, groups), dev)
-    if zero is not None:
-        _check_tensor(zero, "zero", torch.float16, (N, groups), dev)
+    s = _dense(scale, "scale", torch.float16, None, dev)
+    z = None if zero is None else _dense(zero, "zero", torch.float16, (N, groups), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=dev)
-    _check_tensor(out, "out", A.dtype, (M, N), dev)
-    ws = _workspace(workspace, gemm_w4g_workspace_bytes(M, N, K), dev)
-    _call("bq_gemm_w4g_a16", dev, _ptr(A), dt, _ptr(B), _ptr(scale), _ptr(zero), group, _ptr(out), M, N, K, _ptr(ws),
-          ws.numel() if ws is not None else 0)
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+    c = _dense(out, "out", dtype, (M, N), dev)
+    ws, wp, wn = _workspace(workspace, gemm_w4g_workspace_bytes(M, N, K), dev)
+    _enqueue("bq_gemm_w4g_a16", dev, a, dt, b, s, z, group, c, M, N, K, wp, wn)
     return out
 
 
 def _rope_args(q, k, cos, sin, positions, q_weight, k_weight):
     dt = _dtype16(k, "k")
-    if k.dim() != 3:
-        raise ValueError("k must be 3-D [tokens, heads, head_dim]")
-    tokens, hkv, dim = k.shape
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q and k must be 3-D [tokens, heads, head_dim]")
+    shape = tokens, hkv, dim = k.shape
     dev, dtype = k.device, k.dtype
-    ks = _check_rows(k, "k", dtype, tokens, hkv, dim, dev)
-    hq, qs = 0, 0
+    ks = _rows(k, "k", dtype, shape, dev)
+    hq, qs, qp = 0, 0, None
     if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be 3-D [tokens, heads, head_dim]")
-        hq = q.shape[1]
-        qs = _check_rows(q, "q", dtype, tokens, hq, dim, dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _check_tensor(w, name, dtype, (dim,), dev)
-    rot, max_pos = 0, 0
+        hq, qp = q.shape[1], q.data_ptr()
+        qs = _rows(q, "q", dtype, (tokens, hq, dim), dev)
+    wq = None if q_weight is None else _dense(q_weight, "q_weight", dtype, (dim,), dev)
+    wk = None if k_weight is None else _dense(k_weight, "k_weight", dtype, (dim,), dev)
+    rot, max_pos, c, s, at = 0, 0, None, None, None
     if cos is not None:
         if sin is None or positions is None:
             raise ValueError("cos needs sin and positions")
         if cos.dim() != 2:
             raise ValueError("cos must be 2-D [max_pos, rot_dim/2]")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        _check_tensor(cos, "cos", torch.float32, None, dev)
-        _check_tensor(sin, "sin", torch.float32, cos.shape, dev)
-        _check_tensor(positions, "positions", torch.int32, (tokens,), dev)
-    return dt, dtype, dev, tokens, hq, hkv, dim, qs, ks, rot, max_pos
+        max_pos, half = cos.shape
+        rot = 2 * half
+        c = _dense(cos, "cos", torch.float32, None, dev)
+        s = _dense(sin, "sin", torch.float32, (max_pos, half), dev)
+        at = _dense(positions, "positions", torch.int32, (tokens,), dev)
+    return dt, dtype, dev, tokens, hq, hkv, dim, qp, qs, k.data_ptr(), ks, wq, wk, c, s, max_pos, rot, at
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch.Tensor],
@@ -560,32 +590,29 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: Optional[torch.Tensor], 
     by cos / sin fp32 [max_pos, rot_dim/2] at positions int32 [tokens] (None:
     no rotation), in one pass -> (q_out, k_out).  A token whose position is
     outside the table is left out: its outputs are not written."""
-    dt, dtype, dev, tokens, hq, hkv, dim, qs, ks, rot, max_pos = _rope_args(q, k, cos, sin, positions, q_weight, k_weight)
+    dt, dtype, dev, tokens, hq, hkv, dim, qp, qs, kp, ks, wq, wk, c, s, max_pos, rot, at = _rope_args(
+        q, k, cos, sin, positions, q_weight, k_weight)
     if q_out is None:
         q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=dev)
     if k_out is None:
         k_out = torch.empty((tokens, hkv, dim), dtype=dtype, device=dev)
-    _check_tensor(q_out, "q_out", dtype, (tokens, hq, dim), dev)
-    _check_tensor(k_out, "k_out", dtype, (tokens, hkv, dim), dev)
-    _call("bq_qk_norm_rope", dev, _ptr(q), qs, _ptr(k), ks, dt, tokens, hq, hkv, dim, _ptr(q_weight), _ptr(k_weight), eps,
-          _ptr(cos), _ptr(sin), max_pos, rot, int(interleaved), _ptr(positions), _ptr(q_out), _ptr(k_out))
+    qo = _dense(q_out, "q_out", dtype, (tokens, hq, dim), dev)
+    ko = _dense(k_out, "k_out", dtype, (tokens, hkv, dim), dev)
+    _enqueue("bq_qk_norm_rope", dev, qp, qs, kp, ks, dt, tokens, hq, hkv, dim, wq, wk, eps, c, s, max_pos, rot, interleaved, at,
+             qo, ko)
     return q_out, k_out
 
 
 def kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
     """Bytes of a page of the 4-bit cache; a cache is a uint8 tensor
     [num_pages, kv4_page_bytes(...)] (its layout: include/bq_layer.h)."""
-    n = lib().bq_kv4_page_bytes(kv_heads, head_dim, page_size)
-    if n < 0:
-        raise BQError(-n, "bq_kv4_page_bytes")
-    return n
+    return _host_bytes("bq_kv4_page_bytes", kv_heads, head_dim, page_size)
 
 
-def _check_cache(cache, kv_heads, head_dim, page_size, dev):
+def _cache_ptr(cache, kv_heads, head_dim, page_size, dev) -> int:
     if not isinstance(cache, torch.Tensor) or cache.dim() != 2:
         raise ValueError("cache must be a 2-D tensor [num_pages, page bytes]")
-    _check_tensor(cache, "cache", torch.uint8, (cache.shape[0], kv4_page_bytes(kv_heads, head_dim, page_size)), dev)
-    return cache.shape[0]
+    return _dense(cache, "cache", torch.uint8, (cache.shape[0], kv4_page_bytes(kv_heads, head_dim, page_size)), dev)
 
 
 def qk_norm_rope_kv4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor],
@@ -597,17 +624,18 @@ def qk_norm_rope_kv4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor
     written to the 4-bit cache at slots int64 [tokens] (page * page_size +
     offset, each at most once; outside the cache: not written) -> q_out.  q
     None: keys and values only."""
-    dt, dtype, dev, tokens, hq, hkv, dim, qs, ks, rot, max_pos = _rope_args(q, k, cos, sin, positions, q_weight, k_weight)
-    vs = _check_rows(v, "v", dtype, tokens, hkv, dim, dev)
-    pages = _check_cache(cache, hkv, dim, page_size, dev)
-    _check_tensor(slots, "slots", torch.int64, (tokens,), dev)
+    dt, dtype, dev, tokens, hq, hkv, dim, qp, qs, kp, ks, wq, wk, c, s, max_pos, rot, at = _rope_args(
+        q, k, cos, sin, positions, q_weight, k_weight)
+    vs = _rows(v, "v", dtype, (tokens, hkv, dim), dev)
+    pages = _cache_ptr(cache, hkv, dim, page_size, dev)
+    sl = _dense(slots, "slots", torch.int64, (tokens,), dev)
+    qo = None
     if q is not None:
         if q_out is None:
             q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=dev)
-        _check_tensor(q_out, "q_out", dtype, (tokens, hq, dim), dev)
-    _call("bq_qk_norm_rope_kv4", dev, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, dt, tokens, hq, hkv, dim, _ptr(q_weight),
-          _ptr(k_weight), eps, _ptr(cos), _ptr(sin), max_pos, rot, int(interleaved), _ptr(positions), _ptr(q_out),
-          _ptr(cache), pages, page_size, _ptr(slots))
+        qo = _dense(q_out, "q_out", dtype, (tokens, hq, dim), dev)
+    _enqueue("bq_qk_norm_rope_kv4", dev, qp, qs, kp, ks, v.data_ptr(), vs, dt, tokens, hq, hkv, dim, wq, wk, eps, c, s, max_pos,
+             rot, interleaved, at, qo, pages, cache.shape[0], page_size, sl)
     return q_out
 
 
@@ -620,29 +648,24 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, page_size: int, kv_heads:
     if dtype not in _DTYPES16:
         raise ValueError("dtype must be float16 or bfloat16")
     dev = cache.device
-    pages = _check_cache(cache, kv_heads, head_dim, page_size, dev)
+    pages = _cache_ptr(cache, kv_heads, head_dim, page_size, dev)
     if slots.dim() != 1:
         raise ValueError("slots must be 1-D")
-    _check_tensor(slots, "slots", torch.int64, None, dev)
+    sl = _dense(slots, "slots", torch.int64, None, dev)
     shape = (slots.shape[0], kv_heads, head_dim)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=dev)
-    _check_tensor(k_out, "k_out", dtype, shape, dev)
-    _check_tensor(v_out, "v_out", dtype, shape, dev)
-    _call("bq_kv4_read", dev, _ptr(cache), pages, page_size, kv_heads, head_dim, _ptr(slots), shape[0], _DTYPES16[dtype],
-          _ptr(k_out), _ptr(v_out))
+    ko, vo = _dense(k_out, "k_out", dtype, shape, dev), _dense(v_out, "v_out", dtype, shape, dev)
+    _enqueue("bq_kv4_read", dev, pages, cache.shape[0], page_size, kv_heads, head_dim, sl, shape[0], _DTYPES16[dtype], ko, vo)
     return k_out, v_out
 
 
 def attn_kv4_workspace_bytes(batch: int, max_q_len: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
     """Device workspace bytes with which attn_kv4 splits sequences of up to
     max_len keys (0: it does not)."""
-    n = lib().bq_attn_kv4_workspace_bytes(batch, max_q_len, q_heads, kv_heads, head_dim, max_len)
-    if n < 0:
-        raise BQError(-n, "bq_attn_kv4_workspace_bytes")
-    return n
+    return _host_bytes("bq_attn_kv4_workspace_bytes", batch, max_q_len, q_heads, kv_heads, head_dim, max_len)
 
 
 def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int,
@@ -663,15 +686,16 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
     dt = _dtype16(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be 3-D [total_q, q_heads, head_dim]")
-    total, hq, dim = q.shape
+    shape = total, hq, dim = q.shape
     dev, dtype = q.device, q.dtype
-    qs = _check_rows(q, "q", dtype, total, hq, dim, dev)
+    qs = _rows(q, "q", dtype, shape, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be 2-D [batch, max_blocks]")
     batch, blocks = block_table.shape
-    _check_tensor(block_table, "block_table", torch.int32, None, dev)
-    _check_tensor(seq_lens, "seq_lens", torch.int32, (batch,), dev)
-    pages = _check_cache(cache, kv_heads, dim, page_size, dev)
+    tab = _dense(block_table, "block_table", torch.int32, None, dev)
+    lens = _dense(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    pages = _cache_ptr(cache, kv_heads, dim, page_size, dev)
+    starts = None
     if q_start is None:
         if batch == 0 or total % batch:
             raise ValueError("without q_start every sequence has total_q / batch queries")
@@ -681,16 +705,14 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
     else:
         if max_q_len is None:
             raise ValueError("q_start needs max_q_len")
-        _check_tensor(q_start, "q_start", torch.int32, (batch + 1,), dev)
+        starts = _dense(q_start, "q_start", torch.int32, (batch + 1,), dev)
     if out is None:
-        out = torch.empty((total, hq, dim), dtype=dtype, device=dev)
-    _check_tensor(out, "out", dtype, (total, hq, dim), dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
     if lse is None and return_lse:
         lse = torch.empty((total, hq), dtype=torch.float32, device=dev)
-    if lse is not None:
-        _check_tensor(lse, "lse", torch.float32, (total, hq), dev)
-    ws = _workspace(workspace, attn_kv4_workspace_bytes(batch, max_q_len, hq, kv_heads, dim, blocks * page_size), dev)
-    _call("bq_attn_kv4", dev, _ptr(q), qs, dt, _ptr(q_start), _ptr(seq_lens), _ptr(block_table), batch, total, max_q_len, hq,
-          kv_heads, dim, _ptr(cache), pages, page_size, blocks, dim ** -0.5 if scale is None else scale, window, _ptr(out),
-          _ptr(lse), _ptr(ws), ws.numel() if ws is not None else 0)
-    return (out, lse) if lse is not None else out
+    o = _dense(out, "out", dtype, shape, dev)
+    e = None if lse is None else _dense(lse, "lse", torch.float32, (total, hq), dev)
+    ws, wp, wn = _workspace(workspace, attn_kv4_workspace_bytes(batch, max_q_len, hq, kv_heads, dim, blocks * page_size), dev)
+    _enqueue("bq_attn_kv4", dev, q.data_ptr(), qs, dt, starts, lens, tab, batch, total, max_q_len, hq, kv_heads, dim, pages,
+             cache.shape[0], page_size, blocks, dim ** -0.5 if scale is None else scale, window, o, e, wp, wn)
+    return out if lse is None else (out, lse)

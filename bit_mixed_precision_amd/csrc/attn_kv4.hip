@@ -5,10 +5,12 @@
 //
 // The scale and min stay outside the products:
 //   q . K[t]  = sk (sum_d q uk) + mk (sum_d q)
-//   sum_t p V = sum_t (p sv) uv + sum_t p mv
-// so the matrix instructions multiply by the bare codes, which enter them
-// as the bits of subnormal fp16 numbers (dtype16.h): one shift and four
-// masks for eight codes, no conversion.
+//   sum_t p V = sum_t (p sv) (uv - 8) + sum_t p (mv + 8 sv)
+// so the matrix instructions multiply by the bare codes.  K's enter them as
+// the bits of subnormal fp16 numbers (dtype16.h): one shift and four masks
+// for eight codes.  V's are made the fp16 integers u - 8 (nine operations):
+// an average over many tokens is far smaller than its terms, and summed
+// uncentred (0..15) its fp32 accumulator would carry their mean.
 //
 // One wavefront takes 32 tokens a step for a tile of 16 query rows (the
 // queries of one kv head: q_len x heads per kv head).  It computes
@@ -22,9 +24,9 @@
 // lane four tokens of the same channels; a byte permute per pair of tokens
 // makes the operand.
 //
-// p sv is split in two fp16 values (high part and remainder): the sum
-// runs over codes 0..15, not centred, so a single fp16 rounding would be
-// felt at twice the output's own; with a bf16 output the high part is enough.
+// p sv is split in two fp16 values (high part and remainder) for an fp16
+// output: one rounding of it alone would weigh as much as the output's own;
+// with a bf16 output the high part is enough.
 // The reference maximum is raised only when a score passes it by 2^8, and
 // then for all lanes of the row; sums and accumulators are fp32.
 //
@@ -140,6 +142,16 @@ __device__ __forceinline__ void load_tile(Tile<D> &x, const AttnKv4Args &p, cons
 
 constexpr uint32_t kM0 = 0x000f000fu, kM4 = 0x00f000f0u;
 
+// Codes at bits 0..3 (or, high, 4..7) of each half as the fp16 integers u - 8:
+// 0x6400 | u = 1024 + u, and (1024 + 16 u) / 16 - 72, both exact.
+__device__ __forceinline__ uint32_t centred(bool high, uint32_t w)
+{
+    const h2 x = __builtin_bit_cast(h2, (w & (high ? kM4 : kM0)) | 0x64006400u);
+    const h2 s = {(_Float16)0.0625f, (_Float16)0.0625f}, c = {(_Float16)-72.0f, (_Float16)-72.0f};
+    const h2 b = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+    return __builtin_bit_cast(uint32_t, high ? __builtin_elementwise_fma(x, s, c) : x + b);
+}
+
 template <typename T, int D>
 struct Wave {
     static constexpr int kQ = D / 64;   // operand pairs of the queries
@@ -226,7 +238,7 @@ struct Wave {
                 const int j = 4 * h + i;
                 s[j] = (s0[i] * 16.0f + s4[i]) * sk * a1 + mk * b1;
                 sv[j] = half_bits(x.vp[h][i] & 0xffffu);
-                mv[j] = half_bits(x.vp[h][i] >> 16);
+                mv[j] = half_bits(x.vp[h][i] >> 16) + 8.0f * sv[j];
                 if constexpr (MASK) {
                     const int tok = t + 16 * h + 4 * g + i;
                     const bool on = tok < x.lim[h] && tok <= pos && (window <= 0 || tok > pos - window);
@@ -274,10 +286,10 @@ struct Wave {
             z += p0 * mv[j];
             z += p1 * mv[j + 1];
             const float v0 = p0 * sv[j], v1 = p1 * sv[j + 1];
-            const auto hi = __builtin_amdgcn_cvt_pkrtz(v0, v1);
+            const h2 hi = {(_Float16)v0, (_Float16)v1};
             ph[j / 2] = __builtin_bit_cast(uint32_t, hi);
             if constexpr (kLow)
-                pl[j / 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v0 - (float)hi[0], v1 - (float)hi[1]));
+                pl[j / 2] = __builtin_bit_cast(uint32_t, (h2){(_Float16)(v0 - (float)hi[0]), (_Float16)(v1 - (float)hi[1])});
         }
 #pragma unroll
         for (int c = 0; c < (D == 256 ? 2 : 1); ++c) {
@@ -296,7 +308,10 @@ struct Wave {
 #pragma unroll
             for (int j = 0; j < (D == 64 ? 4 : 8); ++j) {
                 const u4 w = j < 4 ? lo : hi;
-                const u4 a = ((j & 2) ? w >> 8 : w) & ((j & 1) ? kM4 : kM0);
+                u4 a;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a[i] = centred(j & 1, (j & 2) ? w[i] >> 8 : w[i]);
                 f4 &acc = o[8 * c + j];
                 acc = F16::mma(a, ph, acc);
                 if constexpr (kLow)
@@ -305,7 +320,7 @@ struct Wave {
         }
     }
 
-    // Sums of the row over its four lanes, and the accumulators brought to one scale.
+    // Sums of the row over its four lanes; the accumulators take in z.
     __device__ __forceinline__ void finish()
     {
 #pragma unroll
@@ -315,7 +330,7 @@ struct Wave {
         }
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
-            o[i] = o[i] * ((i & 1) ? 0x1p20f : 0x1p24f) + z;
+            o[i] += z;
     }
 };
 
@@ -347,14 +362,25 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
     Wave<T, D> w;
     w.init((const uint16_t *)p.q + (int64_t)(r.q0 + qi) * p.q_stride + (head * p.group + hg) * D, ok, p.scale, lane);
     const int *table = p.block_table + (int64_t)b * p.max_blocks;
-    for (int t = start + wave * kTile; t < end; t += kWaves * kTile) {
-        Tile<D> x;
-        load_tile<D>(x, p, table, head, t, end, lane);
+    const auto one = [&](const Tile<D> &x, int t) {
         const int whole = min(min(x.lim[0], x.lim[1]), r.pos_min + 1);
         if (t + kTile <= whole && (p.window <= 0 || t > r.pos_max - p.window))
             w.template step<false>(x, t, pos, p.window, lane);
         else
             w.template step<true>(x, t, pos, p.window, lane);
+    };
+    int t = start + wave * kTile;
+    if (t < end) {
+        // the next tile's loads are in flight during a tile's arithmetic
+        Tile<D> x;
+        load_tile<D>(x, p, table, head, t, end, lane);
+        for (; t + kWaves * kTile < end; t += kWaves * kTile) {
+            Tile<D> y;
+            load_tile<D>(y, p, table, head, t + kWaves * kTile, end, lane);
+            one(x, t);
+            x = y;
+        }
+        one(x, t);
     }
     w.finish();
 

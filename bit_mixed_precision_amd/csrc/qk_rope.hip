@@ -99,8 +99,13 @@ __device__ __forceinline__ void norm_rope(const uint4 raw, const uint16_t *w, do
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        out[i] = T::from_f32((float)y[i]);
+    for (int i = 0; i < 8; ++i) {
+        // fp32 first, then the 16-bit type: the empty asm keeps the compiler
+        // from rounding an fp64 value straight to 16 bits
+        float f = (float)y[i];
+        asm volatile("" : "+v"(f));
+        out[i] = T::from_f32(f);
+    }
 }
 
 __device__ __forceinline__ uint4 pack8(const uint16_t o[8])
