@@ -17,6 +17,24 @@ namespace {
 
 constexpr uint32_t kFlip = 0x88888888u;  // two's complement nibble -> c + 8
 
+// Loads through a buffer descriptor: an offset at or past its size gives
+// zeros, so rows and columns past the ends need no branch.
+typedef __amdgpu_buffer_rsrc_t Buf;
+
+__device__ __forceinline__ Buf buffer(const void *base, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)min(bytes, (int64_t)0x7fffffff), 0x00020000);
+}
+__device__ __forceinline__ u4 load16(Buf b, uint32_t off)
+{
+    return __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+}
+__device__ __forceinline__ uint16_t load2(Buf b, uint32_t off)
+{
+    return __builtin_bit_cast(uint16_t, __builtin_amdgcn_raw_buffer_load_b16(b, off, 0, 0));
+}
+constexpr uint32_t kOut = 0x80000000u;  // past every buffer
+
 // ---------------------------------------------------------------------------
 // gemv
 // ---------------------------------------------------------------------------
@@ -41,79 +59,118 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t p[4])
     }
 }
 
-// A wavefront takes ROWS rows of B; its lanes walk them in chunks of 32 codes
-// (16 bytes, inside one group), lane l taking chunks l, l + 64, ...
-template <typename T, int MR, int ROWS, int U>
+// A wavefront takes ROWS rows of B and walks them 2048 codes a pass, lane l
+// the 32 codes (16 bytes, inside one group) from 32 l on, so a row is read in
+// whole kilobytes.  The workgroup puts the pass of A into LDS once, already in
+// the codes' pair order and with the sum of every 32 values; piece h of every
+// lane's 32 lies in its own plane, so that reads of 16 bytes a lane are
+// contiguous (planes padded by 64 bytes for the writes).  B is in flight two
+// passes ahead.
+constexpr int kPass = 2048, kPlane = 64 * 16 + 64;
+
+template <int ROWS>
+struct GemvLoad {
+    u4 b[ROWS];
+    uint16_t s[ROWS], z[ROWS];
+};
+
+template <typename T, int MR, int ROWS>
 __global__ __launch_bounds__(64 * kGemvWaves) void w4g_gemv_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
                                                                    const uint16_t *__restrict__ scale,
                                                                    const uint16_t *__restrict__ zero, int gshift,
                                                                    uint16_t *__restrict__ C, int M, int N, int K)
 {
+    static_assert(64 * kGemvWaves * 8 == kPass, "a 16-byte piece of a row's pass per thread");
+    __shared__ __align__(16) uint8_t sa[2][MR][4 * kPlane];
+    __shared__ float ssum[2][MR][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = (blockIdx.x * kGemvWaves + wave) * ROWS;
-    if (n0 >= N)
-        return;
-    const int chunks = K / 32, groups = K >> gshift;
-    float acc[MR][ROWS] = {};
-    for (int c0 = 0; c0 < chunks; c0 += 64 * U) {
-        uint4 b[ROWS][U];
-        uint32_t sz[ROWS][U];
-        uint4 a[MR][U][4];
+    const int groups = K >> gshift;
+    const int64_t nb = min(n0, N - 1);  // a wavefront past the end loads nothing and only helps with A
+    const int rows = max(min(ROWS, N - n0), 0);
+    const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + nb * (K / 2), (int64_t)rows * (K / 2));
+    const Buf bs = buffer(scale + nb * groups, (int64_t)rows * groups * 2);
+    const Buf bz = buffer((zero ? zero : scale) + nb * groups, zero ? (int64_t)rows * groups * 2 : 0);
+
+    const auto load_b = [&](GemvLoad<ROWS> &x, int pass) {
+        const int k = pass * kPass + 32 * lane;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + lane + 64 * u;
-            const bool ok = c < chunks;
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                const int64_t n = min(n0 + r, N - 1);
-                b[r][u] = ok ? load_nt16(B + n * (K / 2) + (int64_t)c * 16) : make_uint4(0, 0, 0, 0);
-                const int64_t at = n * groups + (c >> (gshift - 5));
-                sz[r][u] = ok ? scale[at] | (zero ? (uint32_t)zero[at] << 16 : 0u) : 0u;
-            }
-#pragma unroll
-            for (int m = 0; m < MR; ++m)
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    a[m][u][h] = ok && m < M ? *(const uint4 *)(A + (int64_t)m * K + (int64_t)c * 32 + 8 * h)
-                                             : make_uint4(0, 0, 0, 0);
+        for (int r = 0; r < ROWS; ++r) {
+            x.b[r] = load16(bb, k < K ? r * (K / 2) + k / 2 : kOut);
+            const uint32_t at = k < K ? 2 * (r * groups + (k >> gshift)) : kOut;
+            x.s[r] = load2(bs, at);
+            x.z[r] = load2(bz, at);
         }
+    };
+    const auto load_a = [&](u4 *x, int pass) {
+        const int k = pass * kPass + 8 * (int)threadIdx.x;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float s0[MR][ROWS] = {}, s4[MR][ROWS] = {}, sum[MR] = {};
+        for (int m = 0; m < MR; ++m)
+            x[m] = load16(ba, k < K ? 2 * (m * K + k) : kOut);
+    };
+    const auto put_a = [&](const u4 *x, int buf) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t p[ROWS][4];
+        for (int m = 0; m < MR; ++m) {
+            const u4 v = {pack_lo(x[m].x, x[m].z), pack_hi(x[m].x, x[m].z), pack_lo(x[m].y, x[m].w), pack_hi(x[m].y, x[m].w)};
+            *(u4 *)&sa[buf][m][(threadIdx.x & 3) * kPlane + (threadIdx.x >> 2) * 16] = v;
+            float s = T::dot2(v.x, T::kOnes, T::dot2(v.y, T::kOnes, T::dot2(v.z, T::kOnes, T::dot2(v.w, T::kOnes, 0.0f))));
+            s += __shfl_xor(s, 1, 64);
+            s += __shfl_xor(s, 2, 64);
+            if ((threadIdx.x & 3) == 0)
+                ssum[buf][m][threadIdx.x >> 2] = s;
+        }
+    };
+
+    float acc[MR][ROWS] = {};
+    const auto compute = [&](const GemvLoad<ROWS> &x, int buf) {
+        float s0[MR][ROWS] = {}, s4[MR][ROWS] = {};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t p[ROWS][4];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                codes8<T>(x.b[r][h] ^ kFlip, p[r]);
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const u4 q = *(const u4 *)&sa[buf][m][h * kPlane + lane * 16];
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
-                    const uint32_t w[4] = {b[r][u].x, b[r][u].y, b[r][u].z, b[r][u].w};
-                    codes8<T>(w[h] ^ kFlip, p[r]);
-                }
-#pragma unroll
-                for (int m = 0; m < MR; ++m) {
-                    const uint4 v = a[m][u][h];
-                    const uint32_t q[4] = {pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sum[m] = T::dot2(q[i], T::kOnes, sum[m]);
-#pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        s0[m][r] = T::dot2(q[0], p[r][0], s0[m][r]);
-                        s4[m][r] = T::dot2(q[1], p[r][1], s4[m][r]);
-                        s0[m][r] = T::dot2(q[2], p[r][2], s0[m][r]);
-                        s4[m][r] = T::dot2(q[3], p[r][3], s4[m][r]);
-                    }
+                    s0[m][r] = T::dot2(q[0], p[r][0], s0[m][r]);
+                    s4[m][r] = T::dot2(q[1], p[r][1], s4[m][r]);
+                    s0[m][r] = T::dot2(q[2], p[r][2], s0[m][r]);
+                    s4[m][r] = T::dot2(q[3], p[r][3], s4[m][r]);
                 }
             }
+        }
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            const float sum = ssum[buf][m][lane];
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const float s = half_bits(sz[r][u] & 0xffffu), z = half_bits(sz[r][u] >> 16);
-#pragma unroll
-                for (int m = 0; m < MR; ++m) {
-                    const float dot = T::kBf16 ? s0[m][r] + s4[m][r] : s0[m][r] * 0x1p24f + s4[m][r] * 0x1p20f;
-                    acc[m][r] += s * (dot - ((T::kBf16 ? 136.0f : 8.0f) + z) * sum[m]);
-                }
+                const float s = half_bits(x.s[r]), z = half_bits(x.z[r]);
+                const float dot = T::kBf16 ? s0[m][r] + s4[m][r] : s0[m][r] * 0x1p24f + s4[m][r] * 0x1p20f;
+                acc[m][r] += s * (dot - ((T::kBf16 ? 136.0f : 8.0f) + z) * sum);
             }
+        }
+    };
+
+    const int passes = (K + kPass - 1) / kPass;
+    if (passes > 0) {
+        GemvLoad<ROWS> x, y;
+        u4 av[MR];
+        load_b(x, 0);
+        load_a(av, 0);
+        load_b(y, 1);  // past the end: zeros, no access
+        put_a(av, 0);
+        __syncthreads();
+        for (int p = 0; p < passes; ++p) {
+            load_a(av, p + 1);
+            compute(x, p & 1);
+            x = y;
+            load_b(y, p + 2);
+            put_a(av, (p + 1) & 1);
+            __syncthreads();
         }
     }
 #pragma unroll
@@ -135,8 +192,7 @@ hipError_t launch_gemv_t(const uint16_t *A, const uint8_t *B, const uint16_t *sc
     const int64_t wgs = ((int64_t)N + ROWS * kGemvWaves - 1) / (ROWS * kGemvWaves);
     if (!grid_fits(wgs, 64 * kGemvWaves))
         return kGridTooLarge;
-    w4g_gemv_kernel<T, MR, ROWS, MR == 4 ? 1 : 2><<<dim3((unsigned)wgs), 64 * kGemvWaves, 0, s>>>(A, B, scale, zero, gshift, C,
-                                                                                                 M, N, K);
+    w4g_gemv_kernel<T, MR, ROWS><<<dim3((unsigned)wgs), 64 * kGemvWaves, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
     return hipGetLastError();
 }
 
@@ -173,6 +229,14 @@ __device__ __forceinline__ void transpose4(uint32_t w[4])
     w[3] = s[1];
 }
 
+// What a wavefront loads for one 128-wide step.
+template <int NA, int NB>
+struct Step {
+    u4 w[NB];
+    uint16_t s[NB], z[NB];
+    u4 a[NA][4];
+};
+
 // NB tiles of 16 weight rows x NA tiles of 16 activation rows a workgroup;
 // wavefront w takes the 128-wide steps w, w + WAVES, ... of the workgroup's
 // part of K.  A 16-byte load hands lane (n, g) the 32 codes of row n at
@@ -205,58 +269,64 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
     }
     const u4 ones = {T::kOnes, T::kOnes, T::kOnes, T::kOnes};
     const int gmask = (1 << (gshift - 5)) - 1;  // 32-wide steps in a group, less one
-    for (int st = first + wave; st < last; st += WAVES) {
-        uint32_t w[NB][4];
-        uint32_t sz[NB][4];
-        u4 x[NA][4];
+    // B and its parameters from the workgroup's first row on, A whole
+    const int rows = min(16 * NB, N - n0);
+    const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + (int64_t)n0 * (K / 2), (int64_t)rows * (K / 2));
+    const Buf bs = buffer(scale + (int64_t)n0 * groups, (int64_t)rows * groups * 2);
+    const Buf bz = buffer((zero ? zero : scale) + (int64_t)n0 * groups, zero ? (int64_t)rows * groups * 2 : 0);
+    const auto load = [&](Step<NA, NB> &x, int st) {
+        const int k = st * 128 + 32 * g;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const int64_t n = min(n0 + 16 * b + l16, N - 1);
-            const int k = st * 128 + 32 * g;
-            const uint4 v = k < K ? load_nt16(B + n * (K / 2) + k / 2) : make_uint4(0, 0, 0, 0);
-            w[b][0] = v.x;
-            w[b][1] = v.y;
-            w[b][2] = v.z;
-            w[b][3] = v.w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int kk = min(st * 128 + 32 * j, K - 32);
-                const int64_t at = n * groups + (kk >> gshift);
-                sz[b][j] = scale[at] | (zero ? (uint32_t)zero[at] << 16 : 0u);
-            }
+            const uint32_t n = 16 * b + l16;
+            x.w[b] = load16(bb, k < K ? n * (K / 2) + k / 2 : kOut);
+            // scale and zero point of the lane's own 32 codes
+            const uint32_t at = k < K ? 2 * (n * groups + (k >> gshift)) : kOut;
+            x.s[b] = load2(bs, at);
+            x.z[b] = load2(bz, at);
         }
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-            const int64_t m = min(16 * a + l16, M - 1);
+        for (int a = 0; a < NA; ++a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = st * 128 + 32 * j + 8 * g;
-                x[a][j] = k < K ? *(const u4 *)(A + m * K + k) : (u4){0, 0, 0, 0};
+                const int ka = st * 128 + 32 * j + 8 * g;
+                x.a[a][j] = load16(ba, ka < K ? 2 * ((16 * a + l16) * K + ka) : kOut);
             }
-        }
+    };
+    const auto step = [&](const Step<NA, NB> &x) {
+        uint32_t w[NB][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[b][j] = x.w[b][j];
             transpose4(w[b]);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            u4 q[NA];
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
-                const u4 v = x[a][j];
-                x[a][j] = (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
-                sum[a] = T::mma(x[a][j], ones, sum[a]);
+                const u4 v = x.a[a][j];
+                q[a] = (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
+                sum[a] = T::mma(q[a], ones, sum[a]);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const u4 op = codes_op<T>(w[b][j] ^ kFlip);
 #pragma unroll
                 for (int a = 0; a < NA; ++a)
-                    part_acc[a][b] = T::mma(x[a][j], op, part_acc[a][b]);
+                    part_acc[a][b] = T::mma(q[a], op, part_acc[a][b]);
             }
             if ((j & gmask) == gmask) {  // a group ends
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const float s = half_bits(sz[b][j] & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
-                    const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz[b][j] >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
+                    // held by the lane whose codes are this group's
+                    uint32_t sz = x.s[b] | (uint32_t)x.z[b] << 16;
+                    if (gmask != 3)
+                        sz = __shfl(sz, l16 + 16 * j, 64);
+                    const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
+                    const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
 #pragma unroll
                     for (int a = 0; a < NA; ++a) {
 #pragma unroll
@@ -270,6 +340,28 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
                     sum[a] = zero4;
             }
         }
+    };
+    // Workgroups start at different places of K and go round: in step, all
+    // would read one 64-byte column of rows K/2 bytes apart, which meet in a
+    // few memory channels.
+    const int n = last - first;
+    int i = wave, st = n > 0 ? wave + (int)(blockIdx.x / ksplit) % n : 0;
+    if (i < n) {
+        if (st >= n)
+            st -= n;
+        // the next step's loads are in flight during a step's arithmetic
+        Step<NA, NB> x;
+        load(x, first + st);
+        for (; i + WAVES < n; i += WAVES) {
+            st += WAVES;
+            if (st >= n)
+                st -= n;
+            Step<NA, NB> y;
+            load(y, first + st);
+            step(x);
+            x = y;
+        }
+        step(x);
     }
     // join the wavefronts, 16 activation rows at a time
 #pragma unroll
