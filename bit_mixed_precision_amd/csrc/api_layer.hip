@@ -231,11 +231,7 @@ int64_t bq_attn_kv4_workspace_bytes(int64_t batch, int64_t max_q_len, int q_head
 {
     if (attn_shape(batch, max_q_len, q_heads, kv_heads, head_dim, max_len) != BQ_OK)
         return -BQ_ERR_SHAPE;
-    const int64_t items = batch * kv_heads * ((max_q_len * (q_heads / kv_heads) + 15) / 16);
-    if (items == 0)
-        return 0;
-    const int n = bq::attn_kv4_splits(items, max_len);
-    return n > 1 ? items * n * 16 * (head_dim + 2) * 4 : 0;
+    return bq::attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, head_dim, max_len).part_rows * (head_dim + 2) * 4;
 }
 
 int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
@@ -284,7 +280,7 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
     a.hkv = kv_heads;
     a.group = q_heads / kv_heads;
     a.cache = (const uint8_t *)cache;
-    a.num_pages = num_pages;
+    a.num_pages = (int)num_pages;
     while ((1 << a.page_shift) < page_size)
         ++a.page_shift;
     a.max_blocks = (int)max_blocks;
@@ -292,13 +288,12 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
     a.window = (int)window;
     a.out = out;
     a.lse = lse;
-    a.row_tiles = (int)((max_q_len * a.group + 15) / 16);
-    const int64_t items = batch * kv_heads * a.row_tiles;
-    const int64_t need = bq_attn_kv4_workspace_bytes(batch, max_q_len, q_heads, kv_heads, head_dim, max_len);
-    a.nsplit = need > 0 && workspace && workspace_bytes >= need ? bq::attn_kv4_splits(items, max_len) : 1;
+    const bq::AttnKv4Plan plan = bq::attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, head_dim, max_len);
+    a.row_tiles = (int)plan.row_tiles;
+    a.nsplit = plan.part_rows > 0 && workspace && workspace_bytes >= plan.part_rows * (head_dim + 2) * 4 ? plan.nsplit : 1;
     a.part = (float *)workspace;
-    a.part_ml = a.part + items * a.nsplit * 16 * head_dim;
-    return bq::launch_status(bq::launch_attn_kv4(a, head_dim, dtype == BQ_BF16, (hipStream_t)stream));
+    a.part_ml = a.part + plan.part_rows * head_dim;
+    return bq::launch_status(bq::launch_attn_kv4(a, head_dim, plan.rt, dtype == BQ_BF16, (hipStream_t)stream));
 }
 
 }  // extern "C"

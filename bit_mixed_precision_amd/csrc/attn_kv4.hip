@@ -54,6 +54,10 @@ struct Rows {
     int chunk;       // keys of one split
 };
 
+// Rows `tile` * ROWS on of sequence b.  Every split takes `chunk` keys, the
+// same for all sequences: workgroups then last equally long, and the shorter
+// sequences' last splits are empty.
+template <int ROWS>
 __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
 {
     Rows r;
@@ -69,23 +73,41 @@ __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
     r.q0 = start;
     r.rows = qlen * p.group;
     r.base = len - qlen;
-    const int first = tile * 16 / p.group, last = min(tile * 16 + 15, r.rows - 1) / p.group;
+    const int first = tile * ROWS / p.group, last = min(tile * ROWS + ROWS - 1, r.rows - 1) / p.group;
     r.pos_min = r.base + first;
     r.pos_max = r.base + last;
     r.lo = p.window > 0 ? max(0, r.pos_min - p.window + 1) & ~(kTile - 1) : 0;
     r.hi = max(r.pos_max + 1, r.lo);
-    const int n = r.hi - r.lo;
-    constexpr int step = kTile * kWaves;
-    r.chunk = p.nsplit == 1 ? n : ((n + p.nsplit - 1) / p.nsplit + step - 1) / step * step;
+    r.chunk = r.hi - r.lo;
+    if (p.nsplit > 1) {
+        int most = 0;
+        for (int i = threadIdx.x & 63; i < p.batch; i += 64)
+            most = max(most, p.seq_lens[i]);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1)
+            most = max(most, __shfl_xor(most, off, 64));
+        most = min(most, p.max_blocks << p.page_shift);
+        if (p.window > 0)  // keys of ROWS rows: their positions, the window, lo's alignment
+            most = min(most, p.window + (ROWS - 1) / p.group + 1 + kTile);
+        constexpr int step = kTile * kWaves;
+        r.chunk = __builtin_amdgcn_readfirstlane(((most + p.nsplit - 1) / p.nsplit + step - 1) / step * step);
+    }
     return r;
 }
 
+// Codes and parameters of 32 tokens, K or V.
 template <int D>
 struct Tile {
     static constexpr int kW = D / 32;  // dwords of codes per lane and 16 tokens
-    uint32_t k[2][kW], v[2][kW];
-    u4 kp[2], vp[2];
-    int lim[2];  // tokens at or past lim are not there
+    uint32_t c[2][kW];
+    u4 par[2];
+};
+
+// Where the two 16-token halves of a tile lie.
+struct Place {
+    const uint8_t *base[2];  // the kv head's part of the page
+    uint32_t in[2];          // first token in the page
+    int lim[2];              // tokens at or past lim are not there
 };
 
 template <int N>
@@ -105,38 +127,65 @@ __device__ __forceinline__ void load_dwords(uint32_t *dst, const uint8_t *src)
     }
 }
 
-template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &x, const AttnKv4Args &p, const int *table, int head, int t, int hi,
-                                          int lane)
+// Pages of the two 16-token halves of a tile; past the end the first half's.
+__device__ __forceinline__ void load_pages(int (&page)[2], const AttnKv4Args &p, const int *table, int t, int hi)
 {
-    const int g = lane >> 4, m = lane & 15;
+    page[0] = table[t >> p.page_shift];
+    page[1] = table[(t + 16 < hi ? t + 16 : t) >> p.page_shift];
+}
+
+template <int D>
+__device__ __forceinline__ Place place_of(const AttnKv4Args &p, const int (&pages)[2], int head, int t, int hi)
+{
+    Place x;
     const int P = 1 << p.page_shift;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        // 16 tokens lie in one page; past the end the first 16 are read again
+        // 16 tokens lie in one page
         const int tt = t + 16 * s < hi ? t + 16 * s : t;
-        int page = table[tt >> p.page_shift];
-        const bool there = page >= 0 && page < p.num_pages;
-        page = there ? page : 0;
+        const bool there = (uint32_t)pages[s] < (uint32_t)p.num_pages;
         x.lim[s] = there ? hi : 0;
-        const uint8_t *base = p.cache + (int64_t)((int64_t)page * p.hkv + head) * ((int64_t)P * (D + 8));
-        const uint32_t in = tt & (P - 1);
-        const uint8_t *kb = base + in * (D / 2), *vb = base + P * (D / 2) + in * (D / 2);
-        const uint8_t *pb = base + P * D + in * 4;
+        x.base[s] = p.cache + (int64_t)((int64_t)(there ? pages[s] : 0) * p.hkv + head) * (P * (D + 8));
+        x.in[s] = tt & (P - 1);
+    }
+    return x;
+}
+
+template <int D>
+__device__ __forceinline__ void load_k(Tile<D> &x, const Place &at, int page_shift, int lane)
+{
+    const uint32_t g = lane >> 4, m = lane & 15;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const uint8_t *kb = at.base[s] + at.in[s] * (D / 2);
         if constexpr (D == 64) {
-            load_dwords<2>(x.k[s], kb + m * 32 + g * 8);
-            load_dwords<2>(x.v[s], vb + g * 128 + m * 8);
+            load_dwords<2>(x.c[s], kb + (m * 32 + g * 8));
         } else if constexpr (D == 128) {
-            load_dwords<4>(x.k[s], kb + m * 64 + g * 16);
-            load_dwords<4>(x.v[s], vb + g * 256 + m * 16);
+            load_dwords<4>(x.c[s], kb + (m * 64 + g * 16));
         } else {
-            load_dwords<4>(x.k[s], kb + m * 128 + g * 32);
-            load_dwords<4>(x.k[s] + 4, kb + m * 128 + g * 32 + 16);
-            load_dwords<4>(x.v[s], vb + g * 512 + m * 16);
-            load_dwords<4>(x.v[s] + 4, vb + g * 512 + 256 + m * 16);
+            load_dwords<4>(x.c[s], kb + (m * 128 + g * 32));
+            load_dwords<4>(x.c[s] + 4, kb + (m * 128 + g * 32 + 16));
         }
-        x.kp[s] = *(const u4 *)(pb + g * 16);
-        x.vp[s] = *(const u4 *)(pb + 4 * P + g * 16);
+        x.par[s] = *(const u4 *)(at.base[s] + (D << page_shift) + at.in[s] * 4 + g * 16);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(Tile<D> &x, const Place &at, int page_shift, int lane)
+{
+    const uint32_t g = lane >> 4, m = lane & 15;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const uint8_t *vb = at.base[s] + ((D / 2) << page_shift) + at.in[s] * (D / 2);
+        if constexpr (D == 64) {
+            load_dwords<2>(x.c[s], vb + (g * 128 + m * 8));
+        } else if constexpr (D == 128) {
+            load_dwords<4>(x.c[s], vb + (g * 256 + m * 16));
+        } else {
+            load_dwords<4>(x.c[s], vb + (g * 512 + m * 16));
+            load_dwords<4>(x.c[s] + 4, vb + (g * 512 + 256 + m * 16));
+        }
+        x.par[s] = *(const u4 *)(at.base[s] + ((D + 4) << page_shift) + at.in[s] * 4 + g * 16);
     }
 }
 
@@ -144,27 +193,33 @@ constexpr uint32_t kM0 = 0x000f000fu, kM4 = 0x00f000f0u;
 
 // Codes at bits 0..3 (or, high, 4..7) of each half as the fp16 integers u - 8:
 // 0x6400 | u = 1024 + u, and (1024 + 16 u) / 16 - 72, both exact.
-__device__ __forceinline__ uint32_t centred(bool high, uint32_t w)
+// `bias` is 0x64006400 held in a register, which lets mask and merge be one
+// instruction.
+__device__ __forceinline__ uint32_t centred(bool high, uint32_t w, uint32_t bias)
 {
-    const h2 x = __builtin_bit_cast(h2, (w & (high ? kM4 : kM0)) | 0x64006400u);
+    const h2 x = __builtin_bit_cast(h2, (w & (high ? kM4 : kM0)) | bias);
     const h2 s = {(_Float16)0.0625f, (_Float16)0.0625f}, c = {(_Float16)-72.0f, (_Float16)-72.0f};
     const h2 b = {(_Float16)-1032.0f, (_Float16)-1032.0f};
     return __builtin_bit_cast(uint32_t, high ? __builtin_elementwise_fma(x, s, c) : x + b);
 }
 
-template <typename T, int D>
+// RT tiles of 16 query rows of one wavefront.
+template <typename T, int D, int RT>
 struct Wave {
     static constexpr int kQ = D / 64;   // operand pairs of the queries
     static constexpr int kMT = D / 16;  // output tiles of 16 channels
     static constexpr bool kLow = !T::kBf16;
-    u4 q0[kQ], q4[kQ];
-    float a1, b1;          // score = a1 sk (16 s0 + s4) + b1 mk, in powers of two
-    float mt, mref;        // reference maximum, and what is subtracted: mt - shift
-    float cap, shift;      // largest V scale that p sv 2^shift takes in fp16's range
-    float l, z;
-    f4 o[kMT];
+    u4 q0[RT][kQ], q4[RT][kQ];
+    // score = a1 (sk (16 s0 + s4) + b1 mk), in powers of two; a1 >= 0
+    float a1[RT], b1[RT];
+    float mt[RT], mref[RT];  // reference maximum of score / a1, and what is subtracted: mt a1 - shift
+    float l[RT], z[RT];
+    float cap, shift;        // largest V scale that p sv 2^shift takes in fp16's range
+    int pos[RT];
+    u4 ph[RT], pl[RT];       // p sv of the tile, high and low parts
+    f4 o[RT][kMT];
 
-    __device__ __forceinline__ void init(const uint16_t *q, bool ok, float scale, int lane)
+    __device__ __forceinline__ void init_row(int r, const uint16_t *q, bool ok, float scale, int lane)
     {
         const int g = lane >> 4;
         uint32_t w[D / 8];
@@ -176,6 +231,11 @@ struct Wave {
             w[4 * i + 1] = x.y;
             w[4 * i + 2] = x.z;
             w[4 * i + 3] = x.w;
+        }
+        if (scale < 0.0f) {  // the sign goes to the query
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                w[i] ^= 0x80008000u;
         }
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -189,12 +249,12 @@ struct Wave {
             sum += __shfl_xor(sum, off, 64);
             top = fmaxf(top, __shfl_xor(top, off, 64));
         }
-        float back = 1.0f;
+        float back = 1.0f, f = 1.0f;
         if constexpr (T::kBf16) {
             // a power of two brings the row into fp16's range: bf16's eight
             // bits survive down to 2^-24 of the row's largest value
             const uint32_t e = max((__float_as_uint(top) >> 23) & 255u, 11u);
-            const float f = e < 255u ? __uint_as_float((264u - e) << 23) : 1.0f;
+            f = e < 255u ? __uint_as_float((264u - e) << 23) : 1.0f;
             back = e < 255u ? __uint_as_float((e - 10u) << 23) : 1.0f;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -204,103 +264,146 @@ struct Wave {
 #pragma unroll
         for (int i = 0; i < kQ; ++i) {
             const uint32_t *c = w + 8 * i;
-            q0[i] = (u4){pack_lo(c[0], c[2]), pack_lo(c[1], c[3]), pack_lo(c[4], c[6]), pack_lo(c[5], c[7])};
-            q4[i] = (u4){pack_hi(c[0], c[2]), pack_hi(c[1], c[3]), pack_hi(c[4], c[6]), pack_hi(c[5], c[7])};
+            q0[r][i] = (u4){pack_lo(c[0], c[2]), pack_lo(c[1], c[3]), pack_lo(c[4], c[6]), pack_lo(c[5], c[7])};
+            q4[r][i] = (u4){pack_hi(c[0], c[2]), pack_hi(c[1], c[3]), pack_hi(c[4], c[6]), pack_hi(c[5], c[7])};
         }
-        a1 = back * 0x1p20f * (scale * kLog2e);
-        b1 = sum * (scale * kLog2e);
-        mt = mref = kNoMax;
-        cap = shift = 0.0f;
-        l = z = 0.0f;
+        a1[r] = fmaxf(back * 0x1p20f * (fabsf(scale) * kLog2e), 0x1p-120f);  // a masked score is -inf a1
+        b1[r] = sum * f * 0x1p-20f;
+        mt[r] = mref[r] = kNoMax;
+        l[r] = z[r] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
-            o[i] = (f4){0, 0, 0, 0};
+            o[r][i] = (f4){0, 0, 0, 0};
     }
 
-    template <bool MASK>
-    __device__ __forceinline__ void step(const Tile<D> &x, int t, int pos, int window, int lane)
+    // Scores of a tile, over a1.
+    __device__ __forceinline__ void scores(const Tile<D> &x, float (&s)[RT][8])
     {
-        const int g = lane >> 4;
-        float s[8], sv[8], mv[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            f4 s0 = {0, 0, 0, 0}, s4 = {0, 0, 0, 0};
+            f4 s0[RT], s4[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                s0[r] = s4[r] = (f4){0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < kQ; ++i) {
-                const uint32_t a = x.k[h][2 * i], b = x.k[h][2 * i + 1];
+                const uint32_t a = x.c[h][2 * i], b = x.c[h][2 * i + 1];
                 const uint32_t a8 = a >> 8, b8 = b >> 8;
-                s0 = F16::mma((u4){a & kM0, a8 & kM0, b & kM0, b8 & kM0}, q0[i], s0);
-                s4 = F16::mma((u4){a & kM4, a8 & kM4, b & kM4, b8 & kM4}, q4[i], s4);
+                const u4 c0 = {a & kM0, a8 & kM0, b & kM0, b8 & kM0}, c4 = {a & kM4, a8 & kM4, b & kM4, b8 & kM4};
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    s0[r] = F16::mma(c0, q0[r][i], s0[r]);
+                    s4[r] = F16::mma(c4, q4[r][i], s4[r]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float sk = half_bits(x.kp[h][i] & 0xffffu), mk = half_bits(x.kp[h][i] >> 16);
-                const int j = 4 * h + i;
-                s[j] = (s0[i] * 16.0f + s4[i]) * sk * a1 + mk * b1;
-                sv[j] = half_bits(x.vp[h][i] & 0xffffu);
-                mv[j] = half_bits(x.vp[h][i] >> 16) + 8.0f * sv[j];
-                if constexpr (MASK) {
-                    const int tok = t + 16 * h + 4 * g + i;
-                    const bool on = tok < x.lim[h] && tok <= pos && (window <= 0 || tok > pos - window);
-                    s[j] = on ? s[j] : -__builtin_inff();
-                    sv[j] = on ? sv[j] : 0.0f;
-                    mv[j] = on ? mv[j] : 0.0f;
+                const float sk = half_bits(x.par[h][i] & 0xffffu), mk = half_bits(x.par[h][i] >> 16);
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    s[r][4 * h + i] = (s0[r][i] * 16.0f + s4[r][i]) * sk + mk * b1[r];
+            }
+        }
+    }
+
+    // p of a tile and its V parameters; masked if not every row sees every key.
+    __device__ __forceinline__ void values(const Tile<D> &x, float (&s)[RT][8], bool masked, int t, const int (&lim)[2],
+                                           int window, int lane)
+    {
+        float sv[8], mv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t par = x.par[j >> 2][j & 3];
+            sv[j] = half_bits(par & 0xffffu);
+            mv[j] = half_bits(par >> 16) + 8.0f * sv[j];
+        }
+        if (masked) {
+            const int g = lane >> 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int tok = t + 16 * (j >> 2) + 4 * g + (j & 3);
+                const bool there = tok < lim[j >> 2];
+                // What lies in a masked place may be anything: parameters that are
+                // no numbers become 0, and make NaN only where a row sees them.
+                const bool number = __builtin_isfinite(mv[j]) && __builtin_isfinite(sv[j]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const bool on = there && tok <= pos[r] && (window <= 0 || tok > pos[r] - window);
+                    s[r][j] = on ? (number ? s[r][j] : __builtin_nanf("")) : -__builtin_inff();
                 }
+                sv[j] = there && number ? sv[j] : 0.0f;
+                mv[j] = there && number ? mv[j] : 0.0f;
             }
         }
-        float top = s[0], vtop = sv[0];
+        float vtop = sv[0];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) {
-            top = fmaxf(top, s[j]);
+        for (int j = 1; j < 8; ++j)
             vtop = fmaxf(vtop, sv[j]);
+        bool raise = vtop > cap;
+        float top[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            top[r] = s[r][0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                top[r] = fmaxf(top[r], s[r][j]);
+            raise |= top[r] * a1[r] - mref[r] > 8.0f + shift;
         }
-        if (__any(top > mt + 8.0f || vtop > cap)) {
+        if (__builtin_expect(__any(raise), 0)) {
 #pragma unroll
-            for (int off = 16; off < 64; off <<= 1) {
-                top = fmaxf(top, __shfl_xor(top, off, 64));
+            for (int off = 16; off < 64; off <<= 1)
                 vtop = fmaxf(vtop, __shfl_xor(vtop, off, 64));
-            }
-#pragma unroll
-            for (int off = 1; off < 16; off <<= 1)  // masked rows may hold back a scale
-                vtop = fmaxf(vtop, __shfl_xor(vtop, off, 64));
-            mt = fmaxf(mt, top);
             if (vtop > cap) {
-                const int e = (int)((__float_as_uint(vtop) >> 23) & 255u) - 125;
+                const int e = (int)((__float_as_uint(fminf(vtop, 65504.0f)) >> 23) & 255u) - 125;
                 cap = ldexpf(1.0f, e);
                 shift = (float)(6 - e);
             }
-            const float now = mt - shift, f = __builtin_amdgcn_exp2f(mref - now);
-            mref = now;
-            l *= f;
-            z *= f;
 #pragma unroll
-            for (int i = 0; i < kMT; ++i)
-                o[i] *= f;
-        }
-        u4 ph, pl;
+            for (int r = 0; r < RT; ++r) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(s[j] - mref), p1 = __builtin_amdgcn_exp2f(s[j + 1] - mref);
-            l += p0;
-            l += p1;
-            z += p0 * mv[j];
-            z += p1 * mv[j + 1];
-            const float v0 = p0 * sv[j], v1 = p1 * sv[j + 1];
-            const h2 hi = {(_Float16)v0, (_Float16)v1};
-            ph[j / 2] = __builtin_bit_cast(uint32_t, hi);
-            if constexpr (kLow)
-                pl[j / 2] = __builtin_bit_cast(uint32_t, (h2){(_Float16)(v0 - (float)hi[0]), (_Float16)(v1 - (float)hi[1])});
+                for (int off = 16; off < 64; off <<= 1)
+                    top[r] = fmaxf(top[r], __shfl_xor(top[r], off, 64));
+                mt[r] = fmaxf(mt[r], top[r] * a1[r]);
+                const float now = mt[r] - shift, f = __builtin_amdgcn_exp2f(mref[r] - now);
+                mref[r] = now;
+                l[r] *= f;
+                z[r] *= f;
+#pragma unroll
+                for (int i = 0; i < kMT; ++i)
+                    o[r][i] *= f;
+            }
         }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(s[r][j] * a1[r] - mref[r]);
+                const float p1 = __builtin_amdgcn_exp2f(s[r][j + 1] * a1[r] - mref[r]);
+                l[r] += p0;
+                l[r] += p1;
+                z[r] += p0 * mv[j];
+                z[r] += p1 * mv[j + 1];
+                const float v0 = p0 * sv[j], v1 = p1 * sv[j + 1];
+                const h2 hi = {(_Float16)v0, (_Float16)v1};
+                ph[r][j / 2] = __builtin_bit_cast(uint32_t, hi);
+                if constexpr (kLow)
+                    pl[r][j / 2] = __builtin_bit_cast(uint32_t, (h2){(_Float16)(v0 - (float)hi[0]), (_Float16)(v1 - (float)hi[1])});
+            }
+    }
+
+    // o += p sv (u - 8)
+    __device__ __forceinline__ void products(const Tile<D> &x, uint32_t bias)
+    {
 #pragma unroll
         for (int c = 0; c < (D == 256 ? 2 : 1); ++c) {
             // pairs of tokens of the same channels: codes 0..3 (and 4..7) of a unit
             u4 lo, hi;
             if constexpr (D == 64) {
-                lo = (u4){x.v[0][0], x.v[0][1], x.v[1][0], x.v[1][1]};
+                lo = (u4){x.c[0][0], x.c[0][1], x.c[1][0], x.c[1][1]};
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = x.v[i >> 1][4 * c + 2 * (i & 1)], b = x.v[i >> 1][4 * c + 2 * (i & 1) + 1];
+                    const uint32_t a = x.c[i >> 1][4 * c + 2 * (i & 1)], b = x.c[i >> 1][4 * c + 2 * (i & 1) + 1];
                     lo[i] = pack_lo(a, b);
                     hi[i] = pack_hi(a, b);
                 }
@@ -311,160 +414,189 @@ struct Wave {
                 u4 a;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    a[i] = centred(j & 1, (j & 2) ? w[i] >> 8 : w[i]);
-                f4 &acc = o[8 * c + j];
-                acc = F16::mma(a, ph, acc);
-                if constexpr (kLow)
-                    acc = F16::mma(a, pl, acc);
+                    a[i] = centred(j & 1, (j & 2) ? w[i] >> 8 : w[i], bias);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    f4 &acc = o[r][8 * c + j];
+                    acc = F16::mma(a, ph[r], acc);
+                    if constexpr (kLow)
+                        acc = F16::mma(a, pl[r], acc);
+                }
             }
         }
     }
 
-    // Sums of the row over its four lanes; the accumulators take in z.
+    // Sums of the rows over their four lanes; the accumulators take in z.
     __device__ __forceinline__ void finish()
     {
 #pragma unroll
-        for (int off = 16; off < 64; off <<= 1) {
-            l += __shfl_xor(l, off, 64);
-            z += __shfl_xor(z, off, 64);
-        }
+        for (int r = 0; r < RT; ++r) {
 #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-            o[i] += z;
+            for (int off = 16; off < 64; off <<= 1) {
+                l[r] += __shfl_xor(l[r], off, 64);
+                z[r] += __shfl_xor(z[r], off, 64);
+            }
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+                o[r][i] += z[r];
+        }
     }
 };
 
-template <typename T, int D>
+template <typename T, int D, int RT>
 __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
 {
     constexpr int DH = D > 128 ? 128 : D;  // channels joined at a time
+    constexpr int ROWS = 16 * RT;
     __shared__ float so[kWaves][16][DH + 4];
-    __shared__ float sm[kWaves][16], sl[kWaves][16];
+    __shared__ float sm[kWaves][ROWS], sl[kWaves][ROWS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int id = blockIdx.x;
-    const int split = id % p.nsplit;
-    const int item = id / p.nsplit;
+    const int split = blockIdx.x % p.nsplit, item = blockIdx.x / p.nsplit;
     const int tile = item % p.row_tiles;
     const int head = item / p.row_tiles % p.hkv;
     const int b = item / p.row_tiles / p.hkv;
-    const Rows r = rows_of(p, b, tile);
-    if (tile * 16 >= r.rows)
+    const Rows r = rows_of<ROWS>(p, b, tile);
+    if (tile * ROWS >= r.rows)
         return;
     const int start = r.lo + split * r.chunk, end = min(start + r.chunk, r.hi);
     if (split > 0 && start >= r.hi)
         return;
 
-    const int row = tile * 16 + (lane & 15);
-    const int qi = row / p.group, hg = row - qi * p.group;
-    const bool ok = row < r.rows;
-    const int pos = ok ? r.base + qi : r.pos_max;
-    Wave<T, D> w;
-    w.init((const uint16_t *)p.q + (int64_t)(r.q0 + qi) * p.q_stride + (head * p.group + hg) * D, ok, p.scale, lane);
+    Wave<T, D, RT> w;
+    w.cap = w.shift = 0.0f;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int row = tile * ROWS + 16 * i + (lane & 15);
+        const int qi = row / p.group, hg = row - qi * p.group;
+        const bool ok = row < r.rows;
+        w.pos[i] = ok ? r.base + qi : r.pos_max;
+        w.init_row(i, (const uint16_t *)p.q + (int64_t)(r.q0 + qi) * p.q_stride + (head * p.group + hg) * D, ok, p.scale, lane);
+    }
     const int *table = p.block_table + (int64_t)b * p.max_blocks;
-    const auto one = [&](const Tile<D> &x, int t) {
-        const int whole = min(min(x.lim[0], x.lim[1]), r.pos_min + 1);
-        if (t + kTile <= whole && (p.window <= 0 || t > r.pos_max - p.window))
-            w.template step<false>(x, t, pos, p.window, lane);
-        else
-            w.template step<true>(x, t, pos, p.window, lane);
-    };
+    constexpr int kStep = kWaves * kTile;
     int t = start + wave * kTile;
     if (t < end) {
-        // the next tile's loads are in flight during a tile's arithmetic
-        Tile<D> x;
-        load_tile<D>(x, p, table, head, t, end, lane);
-        for (; t + kWaves * kTile < end; t += kWaves * kTile) {
-            Tile<D> y;
-            load_tile<D>(y, p, table, head, t + kWaves * kTile, end, lane);
-            one(x, t);
-            x = y;
+        // K of the next tile is loaded when the scores have used this one's, V
+        // when the products have; page numbers come a tile earlier.
+        uint32_t bias = 0x64006400u;
+        asm volatile("" : "+v"(bias));
+        Tile<D> k, v;
+        int pages[2];
+        load_pages(pages, p, table, t, end);
+        Place at = place_of<D>(p, pages, head, t, end);
+        load_k<D>(k, at, p.page_shift, lane);
+        load_v<D>(v, at, p.page_shift, lane);
+        load_pages(pages, p, table, min(t + kStep, end - 1), end);
+        for (;;) {
+            const int u = t + kStep;
+            const int lim[2] = {at.lim[0], at.lim[1]};
+            float s[RT][8];
+            w.scores(k, s);
+            if (u < end) {
+                at = place_of<D>(p, pages, head, u, end);
+                load_k<D>(k, at, p.page_shift, lane);
+                load_pages(pages, p, table, min(u + kStep, end - 1), end);
+            }
+            const bool whole = t + kTile <= min(min(lim[0], lim[1]), r.pos_min + 1) && (p.window <= 0 || t > r.pos_max - p.window);
+            w.values(v, s, !whole, t, lim, p.window, lane);
+            w.products(v, bias);
+            if (u >= end)
+                break;
+            load_v<D>(v, at, p.page_shift, lane);
+            t = u;
         }
-        one(x, t);
     }
     w.finish();
 
     // join the wavefronts: thread (row, c) takes DH/16 channels
     const int g = lane >> 4, m = lane & 15;
     if (g == 0) {
-        sm[wave][m] = w.mref;
-        sl[wave][m] = w.l;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            sm[wave][16 * i + m] = w.mref[i];
+            sl[wave][16 * i + m] = w.l[i];
+        }
     }
     const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;
     constexpr int CH = DH / 16;
-    const int orow = tile * 16 + jr;
-    const int oqi = orow / p.group, ohg = orow - oqi * p.group;
-    const int64_t orow_at = (int64_t)(r.q0 + oqi) * p.hq + head * p.group + ohg;
-    const int64_t part = (int64_t)(item * (int64_t)p.nsplit + split) * 16 + jr;
 #pragma unroll
-    for (int c = 0; c < D / DH; ++c) {
-        if (c)
+    for (int i = 0; i < RT; ++i) {
+        const int orow = tile * ROWS + 16 * i + jr;
+        const int oqi = orow / p.group, ohg = orow - oqi * p.group;
+        const int64_t orow_at = (int64_t)(r.q0 + oqi) * p.hq + head * p.group + ohg;
+        const int64_t part = (item * (int64_t)p.nsplit + split) * ROWS + 16 * i + jr;
+#pragma unroll
+        for (int c = 0; c < D / DH; ++c) {
+            if (i || c)
+                __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < CH; j += 4) {
+                    const f4 *o = &w.o[i][8 * c + j];
+                    *(float4 *)&so[wave][m][(g * 4 + k) * CH + j] = make_float4(o[0][k], o[1][k], o[2][k], o[3][k]);
+                }
             __syncthreads();
+            float mm = sm[0][16 * i + jr];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int k = 1; k < kWaves; ++k)
+                mm = fmaxf(mm, sm[k][16 * i + jr]);
+            float l = 0.0f, acc[CH] = {};
 #pragma unroll
-            for (int j = 0; j < CH; j += 4)
-                *(float4 *)&so[wave][m][(g * 4 + i) * CH + j] =
-                    make_float4(w.o[8 * c + j][i], w.o[8 * c + j + 1][i], w.o[8 * c + j + 2][i], w.o[8 * c + j + 3][i]);
-        __syncthreads();
-        float mm = sm[0][jr];
+            for (int k = 0; k < kWaves; ++k) {
+                const float f = __builtin_amdgcn_exp2f(sm[k][16 * i + jr] - mm);
+                l += f * sl[k][16 * i + jr];
 #pragma unroll
-        for (int k = 1; k < kWaves; ++k)
-            mm = fmaxf(mm, sm[k][jr]);
-        float l = 0.0f, acc[CH] = {};
+                for (int j = 0; j < CH; ++j)
+                    acc[j] += f * so[k][jr][jc * CH + j];
+            }
+            if (orow < r.rows) {
+                if (p.nsplit == 1) {
+                    uint16_t *dst = (uint16_t *)p.out + orow_at * D + c * DH + jc * CH;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    uint32_t y[CH / 2];
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
-            const float f = __builtin_amdgcn_exp2f(sm[k][jr] - mm);
-            l += f * sl[k][jr];
+                    for (int j = 0; j < CH; j += 2)
+                        y[j / 2] = T::from_f32(acc[j] * inv) | (uint32_t)T::from_f32(acc[j + 1] * inv) << 16;
+                    if constexpr (CH == 8)
+                        *(u4 *)dst = (u4){y[0], y[1], y[2], y[3]};
+                    else
+                        *(u2 *)dst = (u2){y[0], y[1]};
+                    if (p.lse && c == 0 && jc == 0)
+                        p.lse[orow_at] = l == 0.0f ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(l)) * kLn2;
+                } else {
+                    float *dst = p.part + part * D + c * DH + jc * CH;
 #pragma unroll
-            for (int j = 0; j < CH; ++j)
-                acc[j] += f * so[k][jr][jc * CH + j];
-        }
-        if (orow < r.rows) {
-            if (p.nsplit == 1) {
-                uint16_t *dst = (uint16_t *)p.out + orow_at * D + c * DH + jc * CH;
-                uint32_t y[CH / 2];
-#pragma unroll
-                for (int j = 0; j < CH; j += 2)
-                    y[j / 2] = T::from_f32(l == 0.0f ? 0.0f : acc[j] / l) |
-                               (uint32_t)T::from_f32(l == 0.0f ? 0.0f : acc[j + 1] / l) << 16;
-                if constexpr (CH == 8)
-                    *(u4 *)dst = (u4){y[0], y[1], y[2], y[3]};
-                else
-                    *(u2 *)dst = (u2){y[0], y[1]};
-                if (p.lse && c == 0 && jc == 0)
-                    p.lse[orow_at] = l == 0.0f ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(l)) * kLn2;
-            } else {
-                float *dst = p.part + part * D + c * DH + jc * CH;
-#pragma unroll
-                for (int j = 0; j < CH; j += 4)
-                    *(float4 *)(dst + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                if (c == 0 && jc == 0)
-                    *(float2 *)(p.part_ml + part * 2) = make_float2(mm, l);
+                    for (int j = 0; j < CH; j += 4)
+                        *(float4 *)(dst + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                    if (c == 0 && jc == 0)
+                        *(float2 *)(p.part_ml + part * 2) = make_float2(mm, l);
+                }
             }
         }
     }
 }
 
-// Joins the splits of one query row: 256 threads, D/4 of them a split.
-template <typename T, int D>
+// Joins the splits of one query row: D/4 threads a split, blockDim.x of them.
+template <typename T, int D, int RT>
 __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
 {
-    constexpr int TPS = D / 4, G = 256 / TPS;
-    __shared__ float4 so[G][TPS];
-    const int item = blockIdx.x >> 4, jr = blockIdx.x & 15;
+    constexpr int TPS = D / 4, ROWS = 16 * RT;
+    __shared__ float4 so[256];
+    const int item = blockIdx.x / p.join_rows, jr = blockIdx.x % p.join_rows;
     const int tile = item % p.row_tiles;
     const int head = item / p.row_tiles % p.hkv;
     const int b = item / p.row_tiles / p.hkv;
-    const Rows r = rows_of(p, b, tile);
-    const int row = tile * 16 + jr;
+    const Rows r = rows_of<ROWS>(p, b, tile);
+    const int row = tile * ROWS + jr;
     if (row >= r.rows)
         return;
     const int n = r.hi > r.lo ? (r.hi - r.lo + r.chunk - 1) / r.chunk : 1;
-    const int64_t first = (int64_t)item * p.nsplit * 16 + jr;
+    const int64_t first = (int64_t)item * p.nsplit * ROWS + jr;
     const int lane = threadIdx.x & 63;
     // every wavefront holds all splits' maxima and sums, one a lane (nsplit <= 64)
-    const float2 ml = lane < n ? *(const float2 *)(p.part_ml + (first + 16 * lane) * 2) : make_float2(kNoMax, 0.0f);
+    const float2 ml = lane < n ? *(const float2 *)(p.part_ml + (first + ROWS * lane) * 2) : make_float2(kNoMax, 0.0f);
     float mm = ml.x;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
@@ -474,25 +606,24 @@ __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         l += __shfl_xor(l, off, 64);
-    const int gq = threadIdx.x / TPS, c = threadIdx.x % TPS;
+    const int G = blockDim.x / TPS, gq = threadIdx.x / TPS, c = threadIdx.x % TPS;
     float4 acc = make_float4(0, 0, 0, 0);
     for (int s0 = 0; s0 < n; s0 += G) {
         const int s = s0 + gq;
         const float fs = __shfl(f, s & 63, 64);
         if (s < n) {
-            const float4 o = *(const float4 *)(p.part + (first + 16 * (int64_t)s) * D + 4 * c);
+            const float4 o = *(const float4 *)(p.part + (first + ROWS * (int64_t)s) * D + 4 * c);
             acc.x += fs * o.x;
             acc.y += fs * o.y;
             acc.z += fs * o.z;
             acc.w += fs * o.w;
         }
     }
-    so[gq][c] = acc;
+    so[threadIdx.x] = acc;
     __syncthreads();
     if (gq == 0) {
-#pragma unroll
         for (int k = 1; k < G; ++k) {
-            const float4 o = so[k][c];
+            const float4 o = so[k * TPS + c];
             acc.x += o.x;
             acc.y += o.y;
             acc.z += o.z;
@@ -508,39 +639,61 @@ __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
     }
 }
 
-template <typename T, int D>
-hipError_t launch_t(const AttnKv4Args &p, int64_t items, hipStream_t s)
+template <typename T, int D, int RT>
+hipError_t launch_t(const AttnKv4Args &p, hipStream_t s)
 {
-    if (!grid_fits(items * p.nsplit, kThreads) || !grid_fits(items * 16, 256))
+    const int64_t items = (int64_t)p.batch * p.hkv * p.row_tiles;
+    if (!grid_fits(items * p.nsplit, kThreads) || !grid_fits(items * p.join_rows, 256))
         return kGridTooLarge;
-    attn_kv4_kernel<T, D><<<dim3((unsigned)(items * p.nsplit)), kThreads, 0, s>>>(p);
+    attn_kv4_kernel<T, D, RT><<<dim3((unsigned)(items * p.nsplit)), kThreads, 0, s>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.nsplit == 1)
         return e;
-    attn_kv4_join<T, D><<<dim3((unsigned)(items * 16)), 256, 0, s>>>(p);
+    int groups = 1;  // splits joined side by side: whole wavefronts, up to 256 threads
+    while (groups * (D / 4) < 256 && (groups < p.nsplit || groups * (D / 4) < 64))
+        groups *= 2;
+    attn_kv4_join<T, D, RT><<<dim3((unsigned)(items * p.join_rows)), groups * (D / 4), 0, s>>>(p);
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_d(const AttnKv4Args &p, int D, int64_t items, hipStream_t s)
+hipError_t launch_d(const AttnKv4Args &p, int D, int rt, hipStream_t s)
 {
-    return D == 64 ? launch_t<T, 64>(p, items, s) : D == 128 ? launch_t<T, 128>(p, items, s) : launch_t<T, 256>(p, items, s);
+    if (D == 64)
+        return rt == 4 ? launch_t<T, 64, 4>(p, s) : rt == 2 ? launch_t<T, 64, 2>(p, s) : launch_t<T, 64, 1>(p, s);
+    if (D == 128)
+        return rt == 2 ? launch_t<T, 128, 2>(p, s) : launch_t<T, 128, 1>(p, s);
+    return launch_t<T, 256, 1>(p, s);
 }
 
 }  // namespace
 
-int attn_kv4_splits(int64_t items, int64_t max_len)
+AttnKv4Plan attn_kv4_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int D, int64_t max_len)
 {
+    // Row tiles a wavefront: one decode of the codes serves them all, as many
+    // as registers allow while the chip is still full.
+    const int64_t rows = max_q_len * (q_heads / kv_heads), seqs = batch * kv_heads;
+    int rt = 1;
+    const int most_rt = D == 64 ? 4 : D == 128 ? 2 : 1;
+    while (rt < most_rt && rows > 16 * rt && seqs * ((rows + 32 * rt - 1) / (32 * rt)) >= 256)
+        rt *= 2;
+    AttnKv4Plan a;
+    a.rt = rt;
+    a.row_tiles = (rows + 16 * rt - 1) / (16 * rt);
+    const int64_t items = seqs * a.row_tiles;
     const int64_t step = kTile * kWaves;
-    const int64_t want = (1024 + items - 1) / items, most = (max_len + step - 1) / step;
+    const int64_t want = items > 0 ? (1536 + items - 1) / items : 1, most = (max_len + step - 1) / step;
     const int64_t n = want < most ? want : most;
-    return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+    a.nsplit = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+    a.part_rows = a.nsplit > 1 ? items * a.nsplit * 16 * rt : 0;
+    return a;
 }
 
-hipError_t launch_attn_kv4(const AttnKv4Args &p, int D, bool bf16, hipStream_t s)
+hipError_t launch_attn_kv4(AttnKv4Args &p, int D, int rt, bool bf16, hipStream_t s)
 {
-    const int64_t items = (int64_t)p.batch * p.hkv * p.row_tiles;
-    return bf16 ? launch_d<BF16>(p, D, items, s) : launch_d<F16>(p, D, items, s);
+    const int64_t rows = (int64_t)p.max_q_len * p.group;
+    p.join_rows = (int)(rows < 16 * rt ? rows : 16 * rt);
+    return bf16 ? launch_d<BF16>(p, D, rt, s) : launch_d<F16>(p, D, rt, s);
 }
 
 }  // namespace bq

@@ -151,18 +151,24 @@ struct AttnKv4Args {
     int batch, total_q, max_q_len;
     int hq, hkv, group;
     const uint8_t *cache;
-    int64_t num_pages;
+    int num_pages;
     int page_shift, max_blocks;
     float scale;
     int window;
     void *out;
     float *lse;
-    int row_tiles, nsplit;
+    int row_tiles, nsplit, join_rows;
     float *part, *part_ml;
 };
-// Splits of the keys for this many (sequence, kv head, 16-row tile) items.
-int attn_kv4_splits(int64_t items, int64_t max_len);
-hipError_t launch_attn_kv4(const AttnKv4Args &p, int D, bool bf16, hipStream_t s);
+// How a call is split: rt tiles of 16 query rows a workgroup, row_tiles
+// workgroups per sequence and kv head, times nsplit parts of the keys, whose
+// results take part_rows rows (of head_dim + 2 floats) of workspace.
+struct AttnKv4Plan {
+    int rt, nsplit;
+    int64_t row_tiles, part_rows;
+};
+AttnKv4Plan attn_kv4_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int D, int64_t max_len);
+hipError_t launch_attn_kv4(AttnKv4Args &p, int D, int rt, bool bf16, hipStream_t s);
 
 // 4-bit weights with group scales times 16-bit activations.  A call whose
 // outputs are few splits K over workgroups through `ws` when it is given.

@@ -229,34 +229,59 @@ __device__ __forceinline__ void transpose4(uint32_t w[4])
     w[3] = s[1];
 }
 
-// What a wavefront loads for one 128-wide step.
-template <int NA, int NB>
-struct Step {
-    u4 w[NB];
-    uint16_t s[NB], z[NB];
-    u4 a[NA][4];
-};
+// Scale and zero point of np groups from g0 on of ROWS rows, one dword each,
+// to LDS; eight loads of each are in flight per thread.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void params_to_lds(uint32_t *par, int pitch, int np, Buf bs, Buf bz, int g0, int groups)
+{
+    constexpr int kPer = THREADS / ROWS, kFly = 8;
+    const int n = threadIdx.x / kPer;
+    for (int i0 = threadIdx.x % kPer; i0 < np; i0 += kPer * kFly) {
+        uint16_t s[kFly], z[kFly];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int i = i0 + f * kPer;
+            const uint32_t at = i < np && g0 + i < groups ? 2 * (n * groups + g0 + i) : kOut;
+            s[f] = load2(bs, at);
+            z[f] = load2(bz, at);
+        }
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+            if (i0 + f * kPer < np)
+                par[n * pitch + i0 + f * kPer] = s[f] | (uint32_t)z[f] << 16;
+    }
+}
 
 // NB tiles of 16 weight rows x NA tiles of 16 activation rows a workgroup;
 // wavefront w takes the 128-wide steps w, w + WAVES, ... of the workgroup's
 // part of K.  A 16-byte load hands lane (n, g) the 32 codes of row n at
 // k = 32 g; the transpose makes matrix step j cover k = 32 j .. 32 j + 31,
-// which lies in one group.
-template <typename T, int NA, int NB, int WAVES>
+// which lies in one group.  Scales and zero points of a block of K go to LDS
+// first, row by row: read where they are used, two bytes of a line each,
+// they cost as many cache lines as the codes.  Codes are in flight DEPTH steps
+// ahead, activations (from the caches) one.
+constexpr int kParamWords = 8192;  // parameters in LDS: 16 NB rows x groups
+
+template <typename T, int NA, int NB, int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
                                                                 const uint16_t *__restrict__ scale,
                                                                 const uint16_t *__restrict__ zero, int gshift,
                                                                 uint16_t *__restrict__ C, float *__restrict__ part, int M,
                                                                 int N, int K, int ksplit)
 {
-    __shared__ float red[WAVES][16][16 * NB + 4];
+    constexpr int kRows = 16 * NB;
+    __shared__ union {
+        uint32_t par[kParamWords + kRows];
+        float red[WAVES][16][kRows + 4];
+    } sh;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int split = blockIdx.x % ksplit, n0 = blockIdx.x / ksplit * (16 * NB);
+    const int split = blockIdx.x % ksplit, n0 = blockIdx.x / ksplit * kRows;
     const int steps = (K + 127) / 128, per = (steps + ksplit - 1) / ksplit;
     const int first = split * per, last = min(first + per, steps);
     const int groups = K >> gshift;
+    const int sshift = 7 - gshift;  // groups of a step, as a shift
 
     f4 acc[NA][NB], part_acc[NA][NB], sum[NA];
     const f4 zero4 = {0, 0, 0, 0};
@@ -270,99 +295,97 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
     const u4 ones = {T::kOnes, T::kOnes, T::kOnes, T::kOnes};
     const int gmask = (1 << (gshift - 5)) - 1;  // 32-wide steps in a group, less one
     // B and its parameters from the workgroup's first row on, A whole
-    const int rows = min(16 * NB, N - n0);
+    const int rows = min(kRows, N - n0);
     const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + (int64_t)n0 * (K / 2), (int64_t)rows * (K / 2));
     const Buf bs = buffer(scale + (int64_t)n0 * groups, (int64_t)rows * groups * 2);
     const Buf bz = buffer((zero ? zero : scale) + (int64_t)n0 * groups, zero ? (int64_t)rows * groups * 2 : 0);
-    const auto load = [&](Step<NA, NB> &x, int st) {
+    const auto load_w = [&](u4 *w, int st, int end) {
         const int k = st * 128 + 32 * g;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t n = 16 * b + l16;
-            x.w[b] = load16(bb, k < K ? n * (K / 2) + k / 2 : kOut);
-            // scale and zero point of the lane's own 32 codes
-            const uint32_t at = k < K ? 2 * (n * groups + (k >> gshift)) : kOut;
-            x.s[b] = load2(bs, at);
-            x.z[b] = load2(bz, at);
-        }
+        for (int b = 0; b < NB; ++b)
+            w[b] = load16(bb, st < end && k < K ? (16 * b + l16) * (K / 2) + k / 2 : kOut);
+    };
+    const auto load_a = [&](u4 (*x)[4], int st, int end) {
 #pragma unroll
         for (int a = 0; a < NA; ++a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int ka = st * 128 + 32 * j + 8 * g;
-                x.a[a][j] = load16(ba, ka < K ? 2 * ((16 * a + l16) * K + ka) : kOut);
+                x[a][j] = load16(ba, st < end && ka < K ? 2 * ((16 * a + l16) * K + ka) : kOut);
             }
     };
-    const auto step = [&](const Step<NA, NB> &x) {
-        uint32_t w[NB][4];
+    const int block = (kParamWords / kRows) >> sshift;  // steps whose parameters fit
+    for (int b0 = first; b0 < last; b0 += block) {
+        const int b1 = min(b0 + block, last);
+        u4 w[DEPTH][NB], x[2][NA][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[b][j] = x.w[b][j];
-            transpose4(w[b]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            u4 q[NA];
-#pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                const u4 v = x.a[a][j];
-                q[a] = (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
-                sum[a] = T::mma(q[a], ones, sum[a]);
-            }
+        for (int d = 0; d < DEPTH; ++d)
+            load_w(w[d], b0 + wave + d * WAVES, b1);
+        load_a(x[0], b0 + wave, b1);
+        const int np = (b1 - b0) << sshift, pitch = np + 1;
+        if (b0 != first)
+            __syncthreads();
+        params_to_lds<kRows, 64 * WAVES>(sh.par, pitch, np, bs, bz, b0 << sshift, groups);
+        __syncthreads();
+        const auto step = [&](const u4 *wv, u4 (*xv)[4], int st) {
+            uint32_t c[NB][4];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const u4 op = codes_op<T>(w[b][j] ^ kFlip);
 #pragma unroll
-                for (int a = 0; a < NA; ++a)
-                    part_acc[a][b] = T::mma(q[a], op, part_acc[a][b]);
+                for (int j = 0; j < 4; ++j)
+                    c[b][j] = wv[b][j];
+                transpose4(c[b]);
             }
-            if ((j & gmask) == gmask) {  // a group ends
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    // held by the lane whose codes are this group's
-                    uint32_t sz = x.s[b] | (uint32_t)x.z[b] << 16;
-                    if (gmask != 3)
-                        sz = __shfl(sz, l16 + 16 * j, 64);
-                    const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
-                    const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
+            for (int j = 0; j < 4; ++j) {
+                u4 q[NA];
 #pragma unroll
-                    for (int a = 0; a < NA; ++a) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[a][b][i] += s * (part_acc[a][b][i] - z * sum[a][i]);
-                        part_acc[a][b] = zero4;
-                    }
+                for (int a = 0; a < NA; ++a) {
+                    const u4 v = xv[a][j];
+                    q[a] = (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
+                    sum[a] = T::mma(q[a], ones, sum[a]);
                 }
 #pragma unroll
-                for (int a = 0; a < NA; ++a)
-                    sum[a] = zero4;
+                for (int b = 0; b < NB; ++b) {
+                    const u4 op = codes_op<T>(c[b][j] ^ kFlip);
+#pragma unroll
+                    for (int a = 0; a < NA; ++a)
+                        part_acc[a][b] = T::mma(q[a], op, part_acc[a][b]);
+                }
+                if ((j & gmask) == gmask) {  // a group ends
+                    const int at = ((st - b0) << sshift) + (j >> (2 - sshift));
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t sz = sh.par[(16 * b + l16) * pitch + at];
+                        const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
+                        const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
+#pragma unroll
+                        for (int a = 0; a < NA; ++a) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc[a][b][i] += s * (part_acc[a][b][i] - z * sum[a][i]);
+                            part_acc[a][b] = zero4;
+                        }
+                    }
+#pragma unroll
+                    for (int a = 0; a < NA; ++a)
+                        sum[a] = zero4;
+                }
+            }
+        };
+        for (int st = b0 + wave; st < b1; st += DEPTH * WAVES) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                const int s = st + d * WAVES;
+                if (s < b1) {
+                    load_a(x[(d + 1) & 1], s + WAVES, b1);
+                    step(w[d], x[d & 1], s);
+                    load_w(w[d], s + DEPTH * WAVES, b1);
+                }
             }
         }
-    };
-    // Workgroups start at different places of K and go round: in step, all
-    // would read one 64-byte column of rows K/2 bytes apart, which meet in a
-    // few memory channels.
-    const int n = last - first;
-    int i = wave, st = n > 0 ? wave + (int)(blockIdx.x / ksplit) % n : 0;
-    if (i < n) {
-        if (st >= n)
-            st -= n;
-        // the next step's loads are in flight during a step's arithmetic
-        Step<NA, NB> x;
-        load(x, first + st);
-        for (; i + WAVES < n; i += WAVES) {
-            st += WAVES;
-            if (st >= n)
-                st -= n;
-            Step<NA, NB> y;
-            load(y, first + st);
-            step(x);
-            x = y;
-        }
-        step(x);
     }
+    __syncthreads();
     // join the wavefronts, 16 activation rows at a time
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
@@ -372,14 +395,14 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                red[wave][4 * g + i][16 * b + l16] = acc[a][b][i];
+                sh.red[wave][4 * g + i][16 * b + l16] = acc[a][b][i];
         __syncthreads();
         for (int e = threadIdx.x; e < 256 * NB; e += 64 * WAVES) {
             const int m = e / (16 * NB), n = e % (16 * NB);
             float v = 0.0f;
 #pragma unroll
             for (int q = 0; q < WAVES; ++q)
-                v += red[q][m][n];
+                v += sh.red[q][m][n];
             if (16 * a + m < M && n0 + n < N) {
                 const int64_t at = (int64_t)(16 * a + m) * N + n0 + n;
                 if (part)
@@ -389,6 +412,159 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
             }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// panel
+// ---------------------------------------------------------------------------
+
+// 16 weight rows a wavefront, WAVES * 16 a workgroup, all of the up to 16 NA
+// activation rows, and the workgroup's part of K in 128-wide steps.  A step
+// of A is put into LDS by the whole workgroup (in pair order, with the sums
+// over each group), so the caches deliver it once per WAVES * 16 weight rows;
+// each row's 16-byte pieces are permuted by the row's number, which gives the
+// operand reads of 16 rows different banks.  Codes go straight to registers,
+// DEPTH steps ahead; activations are loaded two steps ahead.
+template <typename T, int NA, int WAVES, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES) void w4g_panel_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
+                                                               const uint16_t *__restrict__ scale,
+                                                               const uint16_t *__restrict__ zero, int gshift,
+                                                               uint16_t *__restrict__ C, float *__restrict__ part, int M, int N,
+                                                               int K, int ksplit)
+{
+    constexpr int kRows = 16 * WAVES, kThreads = 64 * WAVES;
+    constexpr int kPieces = 16 * NA * 16, kPer = (kPieces + kThreads - 1) / kThreads;
+    constexpr int kWords = 16384;  // parameters of a block of K in LDS
+    __shared__ __align__(16) uint8_t sa[2][16 * NA][256];
+    __shared__ __align__(16) float ssum[2][4][16 * NA];
+    __shared__ uint32_t par[kWords + kRows];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, l16 = lane & 15;
+    const int split = blockIdx.x % ksplit, n0 = blockIdx.x / ksplit * kRows;
+    const int steps = (K + 127) / 128, per = (steps + ksplit - 1) / ksplit;
+    const int first = split * per, last = min(first + per, steps);
+    const int groups = K >> gshift, sshift = 7 - gshift;
+    const int gmask = (1 << (gshift - 5)) - 1;
+    const int rows = min(kRows, N - n0);
+    const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + (int64_t)n0 * (K / 2), (int64_t)rows * (K / 2));
+    const Buf bs = buffer(scale + (int64_t)n0 * groups, (int64_t)rows * groups * 2);
+    const Buf bz = buffer((zero ? zero : scale) + (int64_t)n0 * groups, zero ? (int64_t)rows * groups * 2 : 0);
+    const int wrow = 16 * wave + l16;
+
+    const auto load_w = [&](int st) {
+        const int k = st * 128 + 32 * g;
+        return load16(bb, st < last && k < K ? wrow * (K / 2) + k / 2 : kOut);
+    };
+    const auto load_a = [&](u4 *x, int st) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x + i * kThreads, k = st * 128 + 8 * (e & 15);
+            x[i] = load16(ba, e < kPieces && st < last && k < K ? 2 * ((e >> 4) * K + k) : kOut);
+        }
+    };
+    const auto put_a = [&](const u4 *x, int buf) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x + i * kThreads, row = e >> 4, piece = e & 15;
+            const u4 v = {pack_lo(x[i].x, x[i].z), pack_hi(x[i].x, x[i].z), pack_lo(x[i].y, x[i].w), pack_hi(x[i].y, x[i].w)};
+            float s = T::dot2(v.x, T::kOnes, T::dot2(v.y, T::kOnes, T::dot2(v.z, T::kOnes, T::dot2(v.w, T::kOnes, 0.0f))));
+            s += __shfl_xor(s, 1, 64);
+            s += __shfl_xor(s, 2, 64);
+            if (gshift > 5)
+                s += __shfl_xor(s, 4, 64);
+            if (gshift > 6)
+                s += __shfl_xor(s, 8, 64);
+            if (kPieces % kThreads == 0 || e < kPieces) {
+                *(u4 *)&sa[buf][row][16 * (piece ^ (row & 15))] = v;
+                if ((piece & (4 * gmask + 3)) == 0)
+                    ssum[buf][piece >> (gshift - 3)][row] = s;
+            }
+        }
+    };
+
+    f4 acc[NA], part_acc[NA];
+    const f4 zero4 = {0, 0, 0, 0};
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+        acc[a] = part_acc[a] = zero4;
+    constexpr int kAhead = DEPTH < 4 ? 2 : 4;  // steps of A in flight
+    u4 w[DEPTH], av[kAhead][kPer];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        w[d] = load_w(first + d);
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+        load_a(av[d], first + d);
+    const int block = (kWords / kRows) >> sshift;  // steps whose parameters fit
+    int b0 = first, pitch = 0;
+    const auto put_par = [&]() {
+        const int np = (min(b0 + block, last) - b0) << sshift;
+        pitch = np + 1;
+        params_to_lds<kRows, kThreads>(par, pitch, np, bs, bz, b0 << sshift, groups);
+    };
+    if (first < last) {
+        put_par();
+        put_a(av[0], 0);
+    }
+    __syncthreads();
+    const auto step = [&](const u4 &wv, int st, int buf) {
+        uint32_t c[4] = {wv.x, wv.y, wv.z, wv.w};
+        transpose4(c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u4 op = codes_op<T>(c[j] ^ kFlip);
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+                part_acc[a] = T::mma(*(const u4 *)&sa[buf][16 * a + l16][16 * ((4 * j + g) ^ l16)], op, part_acc[a]);
+            if ((j & gmask) == gmask) {  // a group ends
+                const int gi = j >> (2 - sshift);
+                const uint32_t sz = par[wrow * pitch + ((st - b0) << sshift) + gi];
+                const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
+                const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
+#pragma unroll
+                for (int a = 0; a < NA; ++a) {
+                    const f4 sum = *(const f4 *)&ssum[buf][gi][16 * a + 4 * g];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[a][i] += s * (part_acc[a][i] - z * sum[i]);
+                    part_acc[a] = zero4;
+                }
+            }
+        }
+    };
+    static_assert(DEPTH % 2 == 0, "a step's buffer is its parity");
+    for (int st = first; st < last; st += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int s = st + d;
+            if (s < last) {
+                if (s == b0 + block) {  // the parameters' next block
+                    b0 = s;
+                    put_par();
+                    __syncthreads();
+                }
+                load_a(av[d % kAhead], s + kAhead);
+                step(w[d], s, d & 1);
+                w[d] = load_w(s + DEPTH);
+                put_a(av[(d + 1) % kAhead], (d + 1) & 1);
+                __syncthreads();
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 16 * a + 4 * g + i, n = n0 + wrow;
+            if (m < M && n < N) {
+                const int64_t at = (int64_t)m * N + n;
+                if (part)
+                    part[(int64_t)split * M * N + at] = acc[a][i];
+                else
+                    C[at] = T::from_f32(acc[a][i]);
+            }
+        }
 }
 
 template <typename T>
@@ -404,18 +580,21 @@ __global__ __launch_bounds__(256) void w4g_join_kernel(const float *__restrict__
     C[i] = T::from_f32(v);
 }
 
-// Parts of K for the skinny kernel with a workspace.
-int skinny_split(int M, int N, int K)
+// Parts of K with a workspace: enough workgroups for the chip's 256 CUs, none
+// under four steps of K.  M <= 16 is not split: joining costs a launch
+// (4 us), more than it gains (M = 16, N = K = 4096: 8.1 us whole, 10.0 in two).
+int k_split(int M, int N, int K)
 {
-    if (M <= 16)
+    if (M <= 16 || M > 64)
         return 1;
-    const int tiles = (N + 63) / 64, steps = (K + 127) / 128;
-    int n = (512 + tiles - 1) / tiles;
+    const int rows = M <= 32 ? 32 : 128;
+    const int tiles = (N + rows - 1) / rows, steps = (K + 127) / 128;
+    int n = (256 + tiles / 2) / tiles;
     n = n < steps / 4 ? n : steps / 4;
     return n < 1 ? 1 : n > 16 ? 16 : n;
 }
 
-template <typename T, int NA, int NB, int WAVES>
+template <typename T, int NA, int NB, int WAVES, int DEPTH>
 hipError_t launch_skinny_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
                            uint16_t *C, int M, int N, int K, float *ws, int ksplit, hipStream_t s)
 {
@@ -423,8 +602,25 @@ hipError_t launch_skinny_t(const uint16_t *A, const uint8_t *B, const uint16_t *
     const int64_t total = (int64_t)M * N;
     if (!grid_fits(wgs, 64 * WAVES) || !grid_fits((total + 255) / 256, 256))
         return kGridTooLarge;
-    w4g_skinny_kernel<T, NA, NB, WAVES><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(
+    w4g_skinny_kernel<T, NA, NB, WAVES, DEPTH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(
         A, B, scale, zero, gshift, C, ksplit > 1 ? ws : nullptr, M, N, K, ksplit);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || ksplit == 1)
+        return e;
+    w4g_join_kernel<T><<<dim3((unsigned)((total + 255) / 256)), 256, 0, s>>>(ws, C, total, ksplit);
+    return hipGetLastError();
+}
+
+template <typename T, int NA, int WAVES, int DEPTH>
+hipError_t launch_panel_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
+                          uint16_t *C, int M, int N, int K, float *ws, int ksplit, hipStream_t s)
+{
+    const int64_t wgs = ((int64_t)N + 16 * WAVES - 1) / (16 * WAVES) * ksplit;
+    const int64_t total = (int64_t)M * N;
+    if (!grid_fits(wgs, 64 * WAVES) || !grid_fits((total + 255) / 256, 256))
+        return kGridTooLarge;
+    w4g_panel_kernel<T, NA, WAVES, DEPTH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(A, B, scale, zero, gshift, C,
+                                                                                     ksplit > 1 ? ws : nullptr, M, N, K, ksplit);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || ksplit == 1)
         return e;
@@ -521,20 +717,16 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
 {
     if (M == 1)
         return launch_gemv_t<T, 1, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
-    if (M == 2)
-        return launch_gemv_t<T, 2, 2>(A, B, scale, zero, gshift, C, M, N, K, s);
-    if (M <= 4)
-        return launch_gemv_t<T, 4, 2>(A, B, scale, zero, gshift, C, M, N, K, s);
-    const int64_t need = gemm_w4g_workspace_bytes(M, N, K);
-    const int ksplit = need && wsBytes >= need ? skinny_split(M, N, K) : 1;
     if (M <= 16)
-        return launch_skinny_t<T, 1, 1, 8>(A, B, scale, zero, gshift, C, M, N, K, ws, 1, s);
+        return launch_skinny_t<T, 1, 1, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, ws, 1, s);
+    const int64_t need = gemm_w4g_workspace_bytes(M, N, K);
+    const int ksplit = need && wsBytes >= need ? k_split(M, N, K) : 1;
     if (M <= 32)
-        return launch_skinny_t<T, 2, 4, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
+        return launch_skinny_t<T, 2, 2, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
     if (M <= 48)
-        return launch_skinny_t<T, 3, 4, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
+        return launch_panel_t<T, 3, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
     if (M <= 64)
-        return launch_skinny_t<T, 4, 4, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
+        return launch_panel_t<T, 4, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
     const int64_t wgs = (((int64_t)M + kBM - 1) / kBM) * (((int64_t)N + kBN - 1) / kBN);
     if (!grid_fits(wgs, 256))
         return kGridTooLarge;
@@ -546,9 +738,7 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
 
 int64_t gemm_w4g_workspace_bytes(int M, int N, int K)
 {
-    if (M <= 16 || M > 64)
-        return 0;
-    const int n = skinny_split(M, N, K);
+    const int n = k_split(M, N, K);
     return n > 1 ? (int64_t)n * M * N * 4 : 0;
 }
 

@@ -167,7 +167,7 @@ def attention(q, cache, table, seq_lens, starts, scale, window=0):
                 val = (uv[k] * sv[k] + mv[k])[on]
                 out[i, h] = p @ val
                 size[i, h] = p @ (uv[k] * sv[k] + mv[k].abs())[on]
-                big = (x.abs().sum() * (15 * sk[k] + mk[k].abs())[on].max()) * scale
-                trunc = d * 2.0 ** -14 * x.abs().max() * sk[k][on].max() * scale
+                big = (x.abs().sum() * (15 * sk[k] + mk[k].abs())[on].max()) * abs(scale)
+                trunc = d * 2.0 ** -14 * x.abs().max() * sk[k][on].max() * abs(scale)
                 delta[i, h] = trunc + 2.0 ** -21 * big + 2.0 ** -22 * z.abs().max()
     return out, lse, size, delta

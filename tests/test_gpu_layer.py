@@ -434,6 +434,44 @@ def test_attn_kv4_growing_scales(bq, dev):
         check_attn(run_attn(bq, dev, q, cache, tab, lens, hkv, page, ws=ws), q, cache, tab, lens, [0, 1], what="growing")
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1.0])
+@pytest.mark.parametrize("T", TYPES)
+def test_attn_kv4_scales(bq, dev, T, scale):
+    """Any sign of the softmax scale; 0 is the plain average."""
+    banner(f"attn scale {scale} {T}")
+    lens, hq, hkv, d, page = [77, 300], 4, 2, 64, 16
+    g = gen(14)
+    cache = make_cache(g, 26, hkv, d, page, T)
+    tab = tables(g, lens, page, 26)
+    q = torch.randn(2, hq, d, generator=g).to(T)
+    got = run_attn(bq, dev, q, cache, tab, lens, hkv, page, scale=scale)
+    check_attn(got, q, cache, tab, lens, [0, 1, 2], scale=scale, what="scale")
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("hq,d", [(2, 64), (8, 128), (64, 64), (2, 256)])
+def test_attn_kv4_masked_places_may_be_anything(bq, dev, T, hq, d):
+    """NaN and infinite parameters of keys that a row does not see (before its
+    window, after its own position) change nothing for it; a row that sees one
+    gets NaN."""
+    banner(f"attn masked places {hq} {d} {T}")
+    n, ql, hkv, page, window = 150, 8, 1, 16, 40
+    g = gen(15)
+    cache = make_cache(g, 10, hkv, d, page, T)
+    tab = torch.arange(10, dtype=torch.int32)[None]
+    q = torch.randn(ql, hq, d, generator=g).to(T)
+    want = run_attn(bq, dev, q, cache, tab, [n], hkv, page, window=window)
+    check_attn(want, q, cache, tab, [n], [0, ql], window, what="clean")
+    bad = torch.tensor([0, 126, 0, 124], dtype=torch.uint8)  # NaN, inf
+    for t in list(range(0, n - ql - window + 1)) + [n - 1]:  # before every window; the last key, seen by the last row
+        _, _, ak, av = cache._places(t % page)
+        cache.bytes[t // page][:, ak] = bad
+        cache.bytes[t // page][:, av] = bad
+    out, lse = run_attn(bq, dev, q, cache, tab, [n], hkv, page, window=window)
+    assert torch.equal(out[:-1], want[0][:-1]) and torch.equal(lse[:-1], want[1][:-1])
+    assert torch.isnan(out[-1]).all()
+
+
 def test_attn_kv4_large_cache_offsets(bq, dev):
     """A page more than 2^32 bytes into the cache."""
     banner("attn offsets past 32 bits")
