@@ -54,6 +54,18 @@ struct Rows {
     int chunk;       // keys of one split
 };
 
+// First query of sequence b, and its query rows per kv head.
+__device__ __forceinline__ void query_rows(const AttnKv4Args &p, int b, int &q0, int &rows)
+{
+    int qlen = p.max_q_len;
+    q0 = b * p.max_q_len;
+    if (p.q_start) {
+        q0 = max(p.q_start[b], 0);
+        qlen = min(max(min(p.q_start[b + 1], p.total_q) - q0, 0), p.max_q_len);
+    }
+    rows = qlen * p.group;
+}
+
 // Rows `tile` * ROWS on of sequence b.  Every split takes `chunk` keys, the
 // same for all sequences: workgroups then last equally long, and the shorter
 // sequences' last splits are empty.
@@ -61,18 +73,9 @@ template <int ROWS>
 __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
 {
     Rows r;
-    int start, qlen;
-    if (p.q_start) {
-        start = max(p.q_start[b], 0);
-        qlen = min(max(min(p.q_start[b + 1], p.total_q) - start, 0), p.max_q_len);
-    } else {
-        start = b * p.max_q_len;
-        qlen = p.max_q_len;
-    }
+    query_rows(p, b, r.q0, r.rows);
     const int len = min(max(p.seq_lens[b], 0), p.max_blocks << p.page_shift);
-    r.q0 = start;
-    r.rows = qlen * p.group;
-    r.base = len - qlen;
+    r.base = len - r.rows / p.group;
     const int first = tile * ROWS / p.group, last = min(tile * ROWS + ROWS - 1, r.rows - 1) / p.group;
     r.pos_min = r.base + first;
     r.pos_max = r.base + last;
@@ -219,19 +222,10 @@ struct Wave {
     u4 ph[RT], pl[RT];       // p sv of the tile, high and low parts
     f4 o[RT][kMT];
 
-    __device__ __forceinline__ void init_row(int r, const uint16_t *q, bool ok, float scale, int lane)
+    // w: the lane's quarter of a query row, as loaded
+    __device__ __forceinline__ void init_row(int r, uint32_t (&w)[D / 8], float scale)
     {
-        const int g = lane >> 4;
-        uint32_t w[D / 8];
         float sum = 0.0f, top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const u4 x = ok ? *(const u4 *)(q + g * (D / 4) + 8 * i) : (u4){0, 0, 0, 0};
-            w[4 * i] = x.x;
-            w[4 * i + 1] = x.y;
-            w[4 * i + 2] = x.z;
-            w[4 * i + 3] = x.w;
-        }
         if (scale < 0.0f) {  // the sign goes to the query
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -456,9 +450,22 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
     const int tile = item % p.row_tiles;
     const int head = item / p.row_tiles % p.hkv;
     const int b = item / p.row_tiles / p.hkv;
-    const Rows r = rows_of<ROWS>(p, b, tile);
-    if (tile * ROWS >= r.rows)
+    int q0, rows;
+    query_rows(p, b, q0, rows);
+    if (tile * ROWS >= rows)
         return;
+    // the queries are on their way while the keys are found
+    uint32_t qw[RT][D / 8];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int row = min(tile * ROWS + 16 * i + (lane & 15), rows - 1);
+        const int qi = row / p.group, hg = row - qi * p.group;
+        const uint16_t *q = (const uint16_t *)p.q + (int64_t)(q0 + qi) * p.q_stride + (head * p.group + hg) * D;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+            load_dwords<4>(qw[i] + 4 * k, (const uint8_t *)(q + (lane >> 4) * (D / 4) + 8 * k));
+    }
+    const Rows r = rows_of<ROWS>(p, b, tile);
     const int start = r.lo + split * r.chunk, end = min(start + r.chunk, r.hi);
     if (split > 0 && start >= r.hi)
         return;
@@ -468,10 +475,8 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int row = tile * ROWS + 16 * i + (lane & 15);
-        const int qi = row / p.group, hg = row - qi * p.group;
-        const bool ok = row < r.rows;
-        w.pos[i] = ok ? r.base + qi : r.pos_max;
-        w.init_row(i, (const uint16_t *)p.q + (int64_t)(r.q0 + qi) * p.q_stride + (head * p.group + hg) * D, ok, p.scale, lane);
+        w.pos[i] = row < r.rows ? r.base + row / p.group : r.pos_max;
+        w.init_row(i, qw[i], p.scale);
     }
     const int *table = p.block_table + (int64_t)b * p.max_blocks;
     constexpr int kStep = kWaves * kTile;
@@ -660,7 +665,7 @@ template <typename T>
 hipError_t launch_d(const AttnKv4Args &p, int D, int rt, hipStream_t s)
 {
     if (D == 64)
-        return rt == 4 ? launch_t<T, 64, 4>(p, s) : rt == 2 ? launch_t<T, 64, 2>(p, s) : launch_t<T, 64, 1>(p, s);
+        return rt == 2 ? launch_t<T, 64, 2>(p, s) : launch_t<T, 64, 1>(p, s);
     if (D == 128)
         return rt == 2 ? launch_t<T, 128, 2>(p, s) : launch_t<T, 128, 1>(p, s);
     return launch_t<T, 256, 1>(p, s);
@@ -670,19 +675,22 @@ hipError_t launch_d(const AttnKv4Args &p, int D, int rt, hipStream_t s)
 
 AttnKv4Plan attn_kv4_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int D, int64_t max_len)
 {
-    // Row tiles a wavefront: one decode of the codes serves them all, as many
-    // as registers allow while the chip is still full.
+    // Two row tiles a wavefront where there are two: one decode of the codes
+    // serves both (301 queries of 4 heads a kv head, D = 64: 43.5 against 45.7
+    // us; 7 of 8, D = 128: 35.0 against 38.6).
     const int64_t rows = max_q_len * (q_heads / kv_heads), seqs = batch * kv_heads;
-    int rt = 1;
-    const int most_rt = D == 64 ? 4 : D == 128 ? 2 : 1;
-    while (rt < most_rt && rows > 16 * rt && seqs * ((rows + 32 * rt - 1) / (32 * rt)) >= 256)
-        rt *= 2;
+    const int rt = D < 256 && rows > 16 ? 2 : 1;
     AttnKv4Plan a;
     a.rt = rt;
     a.row_tiles = (rows + 16 * rt - 1) / (16 * rt);
     const int64_t items = seqs * a.row_tiles;
+    // Splits until the workgroups that the registers let the 256 CUs hold are
+    // all there, but no more: they then run in one go and end together (3 x 8
+    // sequences and heads of 100001 keys: 76.5 us with 768 workgroups, 82 with
+    // 1536, 89 with 576).
+    const int64_t slots = 256 * (D == 256 || (D == 128 && rt == 2) ? 2 : D == 64 && rt == 1 ? 4 : 3);
     const int64_t step = kTile * kWaves;
-    const int64_t want = items > 0 ? (1536 + items - 1) / items : 1, most = (max_len + step - 1) / step;
+    const int64_t want = items > 0 ? slots / items : 1, most = (max_len + step - 1) / step;
     const int64_t n = want < most ? want : most;
     a.nsplit = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
     a.part_rows = a.nsplit > 1 ? items * a.nsplit * 16 * rt : 0;
