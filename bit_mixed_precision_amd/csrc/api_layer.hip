@@ -12,6 +12,13 @@ bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; 
 
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 bool page_size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
+int shift_of(int page_size)
+{
+    int s = 0;
+    while ((1 << s) < page_size && s < 8)
+        ++s;
+    return s;
+}
 constexpr int kMaxHeads = 65536;
 
 // A token-strided tensor: at least a token between tokens, whole 16-byte
@@ -25,7 +32,7 @@ int check_rows(const void *p, int64_t stride, int64_t token)
     return aligned(p, 16) && stride % 8 == 0 ? BQ_OK : BQ_ERR_ALIGN;
 }
 
-int check_rope(bq::QkRopeArgs &a, int dtype, bool cache)
+int check_rope(const bq::QkRopeArgs &a, int dtype, bool cache, int page_size)
 {
     if (dtype != BQ_F16 && dtype != BQ_BF16)
         return BQ_ERR_ARG;
@@ -36,7 +43,7 @@ int check_rope(bq::QkRopeArgs &a, int dtype, bool cache)
         return BQ_ERR_SHAPE;
     if (!(a.eps >= 0.0))
         return BQ_ERR_ARG;
-    if (cache && (!page_size_ok(a.page_size) || a.num_pages < 0 || a.num_pages > BQ_MAX_DIM))
+    if (cache && (!page_size_ok(page_size) || a.num_pages < 0 || a.num_pages > BQ_MAX_DIM))
         return BQ_ERR_SHAPE;
     if (a.tokens == 0 || a.hq + a.hkv == 0)
         return BQ_OK;
@@ -141,7 +148,7 @@ int bq_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_st
     a.D = head_dim;
     a.q_out = (uint16_t *)q_out;
     a.k_out = (uint16_t *)k_out;
-    const int st = check_rope(a, dtype, false);
+    const int st = check_rope(a, dtype, false, 0);
     if (st != BQ_OK || tokens == 0 || q_heads + kv_heads == 0)
         return st;
     return bq::launch_status(bq::launch_qk_norm_rope(a, dtype == BQ_BF16, (hipStream_t)stream));
@@ -183,11 +190,11 @@ int bq_qk_norm_rope_kv4(const void *q, int64_t q_stride, const void *k, int64_t 
     a.q_out = (uint16_t *)q_out;
     a.cache = (uint8_t *)cache;
     a.num_pages = num_pages;
-    a.page_size = page_size;
+    a.page_shift = shift_of(page_size);
     a.slots = slots;
     if (kv_heads < 1)
         return BQ_ERR_SHAPE;
-    const int st = check_rope(a, dtype, true);
+    const int st = check_rope(a, dtype, true, page_size);
     if (st != BQ_OK || tokens == 0)
         return st;
     return bq::launch_status(bq::launch_qk_norm_rope(a, dtype == BQ_BF16, (hipStream_t)stream));
@@ -210,8 +217,8 @@ int bq_kv4_read(const void *cache, int64_t num_pages, int page_size, int kv_head
     const int st = bq::device_status();
     if (st != BQ_OK)
         return st;
-    return bq::launch_status(bq::launch_kv4_read((const uint8_t *)cache, num_pages, page_size, kv_heads, head_dim, slots,
-                                                 tokens, (uint16_t *)k_out, (uint16_t *)v_out, dtype == BQ_BF16,
+    return bq::launch_status(bq::launch_kv4_read((const uint8_t *)cache, num_pages, shift_of(page_size), kv_heads, head_dim,
+                                                 slots, tokens, (uint16_t *)k_out, (uint16_t *)v_out, dtype == BQ_BF16,
                                                  (hipStream_t)stream));
 }
 
@@ -281,8 +288,7 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
     a.group = q_heads / kv_heads;
     a.cache = (const uint8_t *)cache;
     a.num_pages = (int)num_pages;
-    while ((1 << a.page_shift) < page_size)
-        ++a.page_shift;
+    a.page_shift = shift_of(page_size);
     a.max_blocks = (int)max_blocks;
     a.scale = softmax_scale;
     a.window = (int)window;

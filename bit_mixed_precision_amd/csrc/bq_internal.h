@@ -136,11 +136,11 @@ struct QkRopeArgs {
     uint16_t *q_out, *k_out;
     uint8_t *cache;
     int64_t num_pages;
-    int page_size;
+    int page_shift;
     const int64_t *slots;
 };
 hipError_t launch_qk_norm_rope(const QkRopeArgs &p, bool bf16, hipStream_t s);
-hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_size, int hkv, int D, const int64_t *slots,
+hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_shift, int hkv, int D, const int64_t *slots,
                            int64_t tokens, uint16_t *k, uint16_t *v, bool bf16, hipStream_t s);
 
 // Attention over the 4-bit paged cache.

@@ -34,40 +34,79 @@ __device__ __forceinline__ F row_sum(F v)
 }
 
 __device__ __forceinline__ float inv_rms(float ms) { return __builtin_amdgcn_rsqf(ms); }
-__device__ __forceinline__ double inv_rms(double ms) { return 1.0 / sqrt(ms); }
+// Two Newton steps from the hardware's estimate (about 2^-28): a few units of
+// 2^-53, which is far below where a rounding to 16 bits could turn over.
+__device__ __forceinline__ double inv_rms(double ms)
+{
+    double r = __builtin_amdgcn_rsq(ms);
+    r = r * (1.5 - 0.5 * ms * r * r);
+    return r * (1.5 - 0.5 * ms * r * r);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 raw, float (&y)[8])
+{
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = T::to_f32(r[i] & 0xffffu);
+        y[2 * i + 1] = T::to_f32(r[i] >> 16);
+    }
+}
 
 // Norm and rotation of one lane's eight channels in type F; the result in
-// the 16-bit type's bits (through fp32, as a conversion from fp64 goes).
+// the 16-bit type's bits (through fp32, as a conversion from fp64 goes).  A
+// rotation in halves needs another lane's channels: they come over as loaded
+// (four dwords) and are normalized again here.
 template <typename T, typename F, int LPR>
 __device__ __forceinline__ void norm_rope(const uint4 raw, const uint16_t *w, double eps, const float *cs, const float *sn,
                                           int rot, int inter, int sub, uint16_t out[8])
 {
-    F y[8];
-    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = (F)T::to_f32(r[i] & 0xffffu);
-        y[2 * i + 1] = (F)T::to_f32(r[i] >> 16);
-    }
-    if (w) {
-        F ss = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            ss += y[i] * y[i];
-        const F inv = inv_rms(row_sum<F, LPR>(ss) * (F)(1.0 / (8 * LPR)) + (F)eps);
-        const uint4 wr = *(const uint4 *)(w + 8 * sub);
-        const uint32_t wv[4] = {wr.x, wr.y, wr.z, wr.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[2 * i] = y[2 * i] * inv * (F)T::to_f32(wv[i] & 0xffffu);
-            y[2 * i + 1] = y[2 * i + 1] * inv * (F)T::to_f32(wv[i] >> 16);
+    const bool in = 8 * sub < rot;  // rot is a multiple of 16: whole lanes
+    const int hl = rot / 16;        // lanes of one half
+    const bool first = sub < hl;
+    const int other = in && !inter ? (first ? sub + hl : sub - hl) : sub;
+    // tables and weights are on their way during the sum
+    float4 c[2] = {}, s[2] = {};
+    if (in) {
+        const int at = inter ? 4 * sub : 8 * (first ? sub : sub - hl);
+        c[0] = *(const float4 *)(cs + at);
+        s[0] = *(const float4 *)(sn + at);
+        if (!inter) {
+            c[1] = *(const float4 *)(cs + at + 4);
+            s[1] = *(const float4 *)(sn + at + 4);
         }
     }
-    const bool in = 8 * sub < rot;  // rot is a multiple of 16: whole lanes
+    uint4 wr, wo;
+    if (w) {
+        wr = *(const uint4 *)(w + 8 * sub);
+        wo = *(const uint4 *)(w + 8 * other);
+    }
+    // y = inv (x w): the product of two 16-bit values is exact in fp32, and inv
+    // is the row's, so it is applied once, at the end
+    float x[8];
+    unpack8<T>(raw, x);
+    F inv = 1;
+    if (w) {
+        F sq = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sq += (F)x[i] * (F)x[i];
+        inv = inv_rms(row_sum<F, LPR>(sq) * (F)(1.0 / (8 * LPR)) + (F)eps);
+        float g[8];
+        unpack8<T>(wr, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] *= g[i];
+    }
+    F y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y[i] = (F)x[i];
+    const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+    const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
     if (inter) {
         if (in) {
-            const float4 c = *(const float4 *)(cs + 4 * sub), s = *(const float4 *)(sn + 4 * sub);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const F a = y[2 * i], b = y[2 * i + 1];
@@ -76,27 +115,29 @@ __device__ __forceinline__ void norm_rope(const uint4 raw, const uint16_t *w, do
             }
         }
     } else if (rot) {
-        const int hl = rot / 16;  // lanes of one half
-        const bool first = sub < hl;
-        const int lane = threadIdx.x & 63;
-        const int partner = in ? lane + (first ? hl : -hl) : lane;
-        F o[8];
+        const int lane = (threadIdx.x & 63) - sub + other;
+        const uint4 ro = make_uint4(__shfl(raw.x, lane, 64), __shfl(raw.y, lane, 64), __shfl(raw.z, lane, 64),
+                                    __shfl(raw.w, lane, 64));
+        if (in) {
+            float o[8];
+            unpack8<T>(ro, o);
+            if (w) {
+                float g[8];
+                unpack8<T>(wo, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] *= g[i];
+            }
+            const uint32_t sign = first ? 0x80000000u : 0u;  // a cos - b sin, b cos + a sin
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = y[i] * (F)cc[i] + (F)o[i] * (F)__uint_as_float(__float_as_uint(ss[i]) ^ sign);
+        }
+    }
+    if (w) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            o[i] = __shfl(y[i], partner, 64);
-        if (in) {
-            const int at = 8 * (first ? sub : sub - hl);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 c = *(const float4 *)(cs + at + 4 * h), s = *(const float4 *)(sn + at + 4 * h);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 4 * h + i;
-                    y[j] = first ? y[j] * (F)cc[i] - o[j] * (F)ss[i] : y[j] * (F)cc[i] + o[j] * (F)ss[i];
-                }
-            }
-        }
+            y[i] *= inv;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -121,7 +162,7 @@ __device__ __forceinline__ int64_t head_base(int64_t page, int head, int hkv, in
 }
 
 template <typename T, int LPR>
-__device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8_t *base, int tok, int page_size, int sub)
+__device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8_t *base, uint32_t tok, int page_size, int sub)
 {
     constexpr int D = 8 * LPR;
     float x[8];
@@ -142,11 +183,16 @@ __device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8
     // the stored parameters are fp16: bf16 values past its range are held at its ends
     const float mn = (float)(_Float16)fminf(fmaxf(lo, -65504.0f), 65504.0f);
     const float sc = (float)(_Float16)fminf((hi - mn) / 15.0f, 65504.0f);
+    // The correctly rounded quotient from the scale's correctly rounded
+    // reciprocal: one correction of d r by its exact remainder (Markstein).
+    // A scale of 0 (or no number) makes codes 0.
+    const float r = sc > 0.0f ? 1.0f / sc : 0.0f;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = sc > 0.0f ? fminf(fmaxf(rintf((x[i] - mn) / sc), 0.0f), 15.0f) : 0.0f;
-        w |= (uint32_t)q << (4 * i);
+        const float d = x[i] - mn, q0 = d * r;
+        const float q = __builtin_fmaf(__builtin_fmaf(-sc, q0, d), r, q0);
+        w |= (uint32_t)fminf(fmaxf(rintf(q), 0.0f), 15.0f) << (4 * i);
     }
     if (!isV) {
         *(uint32_t *)(base + tok * (D / 2) + 4 * sub) = w;
@@ -168,11 +214,13 @@ template <typename T, int LPR, bool CACHE>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs p)
 {
     constexpr int D = 8 * LPR;
-    const int heads = p.hq + p.hkv * (CACHE ? 2 : 1);
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const uint32_t heads = p.hq + p.hkv * (CACHE ? 2 : 1);
+    // the grid limit keeps rows below 2^32
+    const uint32_t row = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
     const int sub = threadIdx.x % LPR;
-    const int64_t tok = row / heads;
-    const int head = (int)(row - tok * heads);
+    const uint32_t tok32 = row / heads;
+    const int head = (int)(row - tok32 * heads);
+    const int64_t tok = tok32;
     if (tok >= p.tokens)
         return;
     // a row's lanes take one path together: every shuffle stays inside a row
@@ -197,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs
         const bool isV = head >= p.hq + p.hkv;
         const int h = head - p.hq - (isV ? p.hkv : 0);
         const int64_t slot = p.slots[tok];
-        if (slot < 0 || slot >= p.num_pages * p.page_size)
+        if (slot < 0 || slot >= p.num_pages << p.page_shift)
             return;
         const uint16_t *src = isV ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
         const uint4 raw = *(const uint4 *)(src + h * D + 8 * sub);
@@ -211,33 +259,34 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs
         } else {
             norm_rope<T, double, LPR>(raw, p.k_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
         }
-        const int64_t page = slot / p.page_size;
-        store_kv4<T, LPR>(o, isV, p.cache + head_base(page, h, p.hkv, p.page_size, D), (int)(slot - page * p.page_size),
-                          p.page_size, sub);
+        const int page_size = 1 << p.page_shift;
+        store_kv4<T, LPR>(o, isV, p.cache + head_base(slot >> p.page_shift, h, p.hkv, page_size, D),
+                          (uint32_t)slot & (page_size - 1), page_size, sub);
     }
 }
 
 // Eight channels a lane of K or V of one token: codes and parameters to the
 // 16-bit type, T(fp32(code * scale) + min): the product is exact.
 template <typename T, int LPR>
-__global__ __launch_bounds__(kThreads) void kv4_read_kernel(const uint8_t *cache, int64_t num_pages, int page_size, int hkv,
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(const uint8_t *cache, int64_t num_pages, int page_shift, int hkv,
                                                             const int64_t *slots, int64_t tokens, uint16_t *k, uint16_t *v)
 {
     constexpr int D = 8 * LPR;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const int page_size = 1 << page_shift;
+    const uint32_t row = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
     const int sub = threadIdx.x % LPR;
-    const int64_t tok = row / (2 * hkv);
+    const uint32_t tok32 = row / (2 * hkv);
+    const int64_t tok = tok32;
     if (tok >= tokens)
         return;
-    const int head = (int)(row - tok * 2 * hkv);
+    const int head = (int)(row - tok32 * 2 * hkv);
     const bool isV = head >= hkv;
     const int h = isV ? head - hkv : head;
     const int64_t slot = slots[tok];
-    if (slot < 0 || slot >= num_pages * page_size)
+    if (slot < 0 || slot >= num_pages << page_shift)
         return;
-    const int64_t page = slot / page_size;
-    const int t = (int)(slot - page * page_size);
-    const uint8_t *base = cache + head_base(page, h, hkv, page_size, D);
+    const uint32_t t = (uint32_t)slot & (page_size - 1);
+    const uint8_t *base = cache + head_base(slot >> page_shift, h, hkv, page_size, D);
     uint32_t w;
     if (!isV) {
         w = *(const uint32_t *)(base + t * (D / 2) + 4 * sub);
@@ -275,7 +324,7 @@ hipError_t launch_rope_t(const QkRopeArgs &p, int64_t rows, hipStream_t s)
 }
 
 template <typename T>
-hipError_t launch_read_t(const uint8_t *cache, int64_t num_pages, int page_size, int hkv, int D, const int64_t *slots,
+hipError_t launch_read_t(const uint8_t *cache, int64_t num_pages, int page_shift, int hkv, int D, const int64_t *slots,
                          int64_t tokens, uint16_t *k, uint16_t *v, hipStream_t s)
 {
     const int per = kThreads / (D / 8);
@@ -284,11 +333,11 @@ hipError_t launch_read_t(const uint8_t *cache, int64_t num_pages, int page_size,
         return kGridTooLarge;
     const dim3 grid((unsigned)wgs);
     if (D == 64)
-        kv4_read_kernel<T, 8><<<grid, kThreads, 0, s>>>(cache, num_pages, page_size, hkv, slots, tokens, k, v);
+        kv4_read_kernel<T, 8><<<grid, kThreads, 0, s>>>(cache, num_pages, page_shift, hkv, slots, tokens, k, v);
     else if (D == 128)
-        kv4_read_kernel<T, 16><<<grid, kThreads, 0, s>>>(cache, num_pages, page_size, hkv, slots, tokens, k, v);
+        kv4_read_kernel<T, 16><<<grid, kThreads, 0, s>>>(cache, num_pages, page_shift, hkv, slots, tokens, k, v);
     else
-        kv4_read_kernel<T, 32><<<grid, kThreads, 0, s>>>(cache, num_pages, page_size, hkv, slots, tokens, k, v);
+        kv4_read_kernel<T, 32><<<grid, kThreads, 0, s>>>(cache, num_pages, page_shift, hkv, slots, tokens, k, v);
     return hipGetLastError();
 }
 
@@ -302,11 +351,11 @@ hipError_t launch_qk_norm_rope(const QkRopeArgs &p, bool bf16, hipStream_t s)
     return bf16 ? launch_rope_t<BF16, false>(p, rows, s) : launch_rope_t<F16, false>(p, rows, s);
 }
 
-hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_size, int hkv, int D, const int64_t *slots,
+hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_shift, int hkv, int D, const int64_t *slots,
                            int64_t tokens, uint16_t *k, uint16_t *v, bool bf16, hipStream_t s)
 {
-    return bf16 ? launch_read_t<BF16>(cache, num_pages, page_size, hkv, D, slots, tokens, k, v, s)
-                : launch_read_t<F16>(cache, num_pages, page_size, hkv, D, slots, tokens, k, v, s);
+    return bf16 ? launch_read_t<BF16>(cache, num_pages, page_shift, hkv, D, slots, tokens, k, v, s)
+                : launch_read_t<F16>(cache, num_pages, page_shift, hkv, D, slots, tokens, k, v, s);
 }
 
 }  // namespace bq
