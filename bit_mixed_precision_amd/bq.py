@@ -461,9 +461,12 @@ def _dtype16(t: torch.Tensor, name: str) -> int:
 def _dense(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """The address of a dense GPU tensor of this type, shape (None: any) and
     device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_cuda and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
-        _check_tensor(t, name, dtype, shape, device)
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape) and t.is_cuda:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check_tensor(t, name, dtype, shape, device)
     return t.data_ptr()
 
 
@@ -472,22 +475,17 @@ def _rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     between its tokens."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    tokens, heads, dim = shape
-    s = t.stride()
-    if s[2] != 1 or (s[1] != dim and heads > 1):
+    if not (t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape):
+        _check_tensor(t, name, dtype, shape, device)  # says which, and raises
+    stride, by_head, by_dim = t.stride()
+    if by_dim != 1 or (by_head != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must be dense within a token")
-    return s[0] if tokens > 1 else heads * dim
+    return stride if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _enqueue(name: str, device: torch.device, *args):
     """The C call of this name on the device's current torch stream."""
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         _call(name, device, *args)
         return
     st = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
@@ -502,6 +500,14 @@ def _host_bytes(name: str, *args) -> int:
     if n < 0:
         raise BQError(-n, name)
     return n
+
+
+def _output(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """(tensor, address) of the output given, or of a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _dense(t, name, dtype, shape, device)
 
 
 def _workspace(t: Optional[torch.Tensor], nbytes: int, device):
@@ -545,9 +551,7 @@ def gemm_w4g_a16(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, zero: Op
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
     s = _dense(scale, "scale", torch.float16, None, dev)
     z = None if zero is None else _dense(zero, "zero", torch.float16, (N, groups), dev)
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=dev)
-    c = _dense(out, "out", dtype, (M, N), dev)
+    out, c = _output(out, "out", dtype, (M, N), dev)
     ws, wp, wn = _workspace(workspace, gemm_w4g_workspace_bytes(M, N, K), dev)
     _enqueue("bq_gemm_w4g_a16", dev, a, dt, b, s, z, group, c, M, N, K, wp, wn)
     return out
@@ -592,12 +596,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: Optional[torch.Tensor], 
     outside the table is left out: its outputs are not written."""
     dt, dtype, dev, tokens, hq, hkv, dim, qp, qs, kp, ks, wq, wk, c, s, max_pos, rot, at = _rope_args(
         q, k, cos, sin, positions, q_weight, k_weight)
-    if q_out is None:
-        q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=dev)
-    if k_out is None:
-        k_out = torch.empty((tokens, hkv, dim), dtype=dtype, device=dev)
-    qo = _dense(q_out, "q_out", dtype, (tokens, hq, dim), dev)
-    ko = _dense(k_out, "k_out", dtype, (tokens, hkv, dim), dev)
+    q_out, qo = _output(q_out, "q_out", dtype, (tokens, hq, dim), dev)
+    k_out, ko = _output(k_out, "k_out", dtype, (tokens, hkv, dim), dev)
     _enqueue("bq_qk_norm_rope", dev, qp, qs, kp, ks, dt, tokens, hq, hkv, dim, wq, wk, eps, c, s, max_pos, rot, interleaved, at,
              qo, ko)
     return q_out, k_out
@@ -631,9 +631,7 @@ def qk_norm_rope_kv4(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor
     sl = _dense(slots, "slots", torch.int64, (tokens,), dev)
     qo = None
     if q is not None:
-        if q_out is None:
-            q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=dev)
-        qo = _dense(q_out, "q_out", dtype, (tokens, hq, dim), dev)
+        q_out, qo = _output(q_out, "q_out", dtype, (tokens, hq, dim), dev)
     _enqueue("bq_qk_norm_rope_kv4", dev, qp, qs, kp, ks, v.data_ptr(), vs, dt, tokens, hq, hkv, dim, wq, wk, eps, c, s, max_pos,
              rot, interleaved, at, qo, pages, cache.shape[0], page_size, sl)
     return q_out
@@ -653,11 +651,8 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, page_size: int, kv_heads:
         raise ValueError("slots must be 1-D")
     sl = _dense(slots, "slots", torch.int64, None, dev)
     shape = (slots.shape[0], kv_heads, head_dim)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
-    ko, vo = _dense(k_out, "k_out", dtype, shape, dev), _dense(v_out, "v_out", dtype, shape, dev)
+    k_out, ko = _output(k_out, "k_out", dtype, shape, dev)
+    v_out, vo = _output(v_out, "v_out", dtype, shape, dev)
     _enqueue("bq_kv4_read", dev, pages, cache.shape[0], page_size, kv_heads, head_dim, sl, shape[0], _DTYPES16[dtype], ko, vo)
     return k_out, v_out
 
@@ -706,12 +701,10 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
         if max_q_len is None:
             raise ValueError("q_start needs max_q_len")
         starts = _dense(q_start, "q_start", torch.int32, (batch + 1,), dev)
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    if lse is None and return_lse:
-        lse = torch.empty((total, hq), dtype=torch.float32, device=dev)
-    o = _dense(out, "out", dtype, shape, dev)
-    e = None if lse is None else _dense(lse, "lse", torch.float32, (total, hq), dev)
+    out, o = _output(out, "out", dtype, shape, dev)
+    e = None
+    if lse is not None or return_lse:
+        lse, e = _output(lse, "lse", torch.float32, (total, hq), dev)
     ws, wp, wn = _workspace(workspace, attn_kv4_workspace_bytes(batch, max_q_len, hq, kv_heads, dim, blocks * page_size), dev)
     _enqueue("bq_attn_kv4", dev, q.data_ptr(), qs, dt, starts, lens, tab, batch, total, max_q_len, hq, kv_heads, dim, pages,
              cache.shape[0], page_size, blocks, dim ** -0.5 if scale is None else scale, window, o, e, wp, wn)

@@ -11,6 +11,7 @@
 //   sum_g s_g (sum_k a u - (8 + z_g) sum_k a).
 #include "bq_internal.h"
 #include "dtype16.h"
+#include "lds_dma.h"
 
 namespace bq {
 namespace {
@@ -632,83 +633,176 @@ hipError_t launch_panel_t(const uint16_t *A, const uint8_t *B, const uint16_t *s
 // tiled
 // ---------------------------------------------------------------------------
 
-constexpr int kBM = 128, kBN = 128, kBK = 64, kPad = 8;
-
+// The four codes pairs of a dword times scale, in order, each weight rounded
+// once to T.  A byte in both halves, masked to its low and high nibble, is
+// 1024 + u and 1024 + 16 u as fp16; one packed multiply-add makes both the
+// integer u - 8.  Without zero points fp16 takes the product there; else
+// (u - 8) s - z s goes through fp32.
 template <typename T>
-__global__ __launch_bounds__(256) void w4g_tiled_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
-                                                        const uint16_t *__restrict__ scale, const uint16_t *__restrict__ zero,
-                                                        int gshift, uint16_t *__restrict__ C, int M, int N, int K)
+__device__ __forceinline__ u4 weights8(uint32_t w, bool plain, uint32_t s2, float s, float off)
 {
-    __shared__ uint16_t sa[kBM][kBK + kPad], sb[kBN][kBK + kPad];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int g = lane >> 4, l16 = lane & 15;
-    const int tilesN = (N + kBN - 1) / kBN;
-    const int m0 = blockIdx.x / tilesN * kBM, n0 = blockIdx.x % tilesN * kBN;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const int groups = K >> gshift;
-    f4 acc[4][4];
+    const h2 mul = {(_Float16)1.0f, (_Float16)0.0625f}, add = {(_Float16)-1032.0f, (_Float16)-72.0f};
+    u4 y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[i][j] = (f4){0, 0, 0, 0};
-    // thread (row, half): 32 codes of a weight row; rows of A in 16-byte pieces
-    const int br = threadIdx.x >> 1, bh = threadIdx.x & 1;
-    const int64_t bn = min(n0 + br, N - 1);
-    for (int k0 = 0; k0 < K; k0 += kBK) {
-        const uint4 bw = *(const uint4 *)(B + bn * (K / 2) + k0 / 2 + 16 * bh);
-        const int64_t at = bn * groups + ((k0 + 32 * bh) >> gshift);
-        const float s = half_bits(scale[at]), off = -(8.0f + (zero ? half_bits(zero[at]) : 0.0f)) * s;
-        u4 av[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = threadIdx.x + 256 * i;
-            av[i] = *(const u4 *)(A + (int64_t)min(m0 + (e >> 3), M - 1) * K + k0 + 8 * (e & 7));
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = threadIdx.x + 256 * i;
-            *(u4 *)&sa[e >> 3][8 * (e & 7)] = av[i];
-        }
-        const uint32_t wd[4] = {bw.x, bw.y, bw.z, bw.w};
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const uint32_t w = wd[h] ^ kFlip;
-            u4 y;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float c0 = (float)((w >> (8 * i)) & 15u), c1 = (float)((w >> (8 * i + 4)) & 15u);
-                y[i] = T::from_f32(c0 * s + off) | (uint32_t)T::from_f32(c1 * s + off) << 16;
-            }
-            *(u4 *)&sb[br][32 * bh + 8 * h] = y;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kBK; kk += 32) {
-            u4 fa[4], fb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fa[i] = *(const u4 *)&sa[wm + 16 * i + l16][kk + 8 * g];
-                fb[i] = *(const u4 *)&sb[wn + 16 * i + l16][kk + 8 * g];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = T::mma(fa[i], fb[j], acc[i][j]);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __builtin_amdgcn_perm(0u, w, 0x0c000c00u | (uint32_t)i << 16 | (uint32_t)i);
+        const h2 u = __builtin_elementwise_fma(__builtin_bit_cast(h2, (b & 0x00f0000fu) | 0x64006400u), mul, add);
+        if (!T::kBf16 && plain) {
+            y[i] = __builtin_bit_cast(uint32_t, u * __builtin_bit_cast(h2, s2));
+        } else {
+            const float a = (float)u[0] * s + off, c = (float)u[1] * s + off;
+            y[i] = T::from_f32(a) | (uint32_t)T::from_f32(c) << 16;
         }
     }
+    return y;
+}
+
+constexpr int kBK = 64;
+
+// Two bytes a lane straight to LDS, as a dword at lds_addr + 4 lane.
+__device__ __forceinline__ void dma2(v4si rsrc, uint32_t lds_addr, uint32_t voff)
+{
+    asm volatile("buffer_load_ushort %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds_addr) : "memory");
+}
+
+// BM x BN outputs a workgroup of four wavefronts side by side, each all BM
+// rows of A and BN/4 weight rows, so that a code is decoded once; K in steps
+// of 64 through STAGES LDS buffers that the loads fill without registers,
+// STAGES - 1 steps ahead.  Codes stay packed in LDS and become operands in
+// registers (weights8) between the matrix instructions.  A row's eight
+// 16-byte pieces are permuted by its number, so that operand reads of eight
+// rows fall into different banks.  A lane takes k = 16 g .. 16 g + 15 of a
+// step, its codes being one 8-byte read.
+template <typename T, int BM, int BN, int STAGES, bool ZERO>
+__global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
+                                                           const uint16_t *__restrict__ scale,
+                                                           const uint16_t *__restrict__ zero, int gshift,
+                                                           uint16_t *__restrict__ C, int M, int N, int K)
+{
+    constexpr int FM = BM / 16, FN = BN / 64;
+    constexpr int kA = BM / 32, kB = BN < 128 ? 1 : BN / 128;  // loads of a wavefront a step: A, codes (and scales, zeros)
+    constexpr int kLoads = kA + kB * (ZERO ? 3 : 2);
+    constexpr int oB = BM * 128, oS = oB + BN * 32, oZ = oS + BN * 8, kStage = oZ + (ZERO ? BN * 8 : 0);
+    static_assert(BM % 32 == 0 && (BN == 64 || BN % 128 == 0), "whole loads");
+    static_assert((STAGES - 1) * kLoads < 64, "the wait counter");
+    __shared__ __align__(1024) uint8_t lds[STAGES * kStage];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, l16 = lane & 15;
+    const int tilesM = (M + BM - 1) / BM;
+    // neighbouring workgroups share weight rows: a die's L2 then reads them once
+    const int m0 = blockIdx.x % tilesM * BM, n0 = blockIdx.x / tilesM * BN;
+    const int groups = K >> gshift, steps = K / kBK;
+    const int mrows = min(BM, M - m0), nrows = min(BN, N - n0);
+    const v4si ra = make_rsrc(A + (int64_t)m0 * K, (uint32_t)mrows * K * 2);
+    const v4si rb = make_rsrc(B + (int64_t)n0 * (K / 2), (uint32_t)nrows * (K / 2));
+    const v4si rs = make_rsrc(scale + (int64_t)n0 * groups, (uint32_t)nrows * groups * 2);
+    const v4si rz = make_rsrc((ZERO ? zero : scale) + (int64_t)n0 * groups, (uint32_t)nrows * groups * 2);
+    const uint32_t base = lds_addr(lds);
+
+    const auto load = [&](int st) {
+        const uint32_t to = __builtin_amdgcn_readfirstlane(base + (uint32_t)(st % STAGES) * kStage);
+        const bool in = st < steps;  // past the end: zeros, no access
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kA; ++i) {
+            const int row = (wave * kA + i) * 8 + (lane >> 3), piece = (lane & 7) ^ (lane >> 3);
+            dma16(ra, to + (wave * kA + i) * 1024, in ? (uint32_t)(2 * (row * K + st * kBK) + 16 * piece) : kOOB, 0);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < kB; ++i) {
+            const int at = BN < 128 ? wave & 1 : wave * kB + i;
+            const int row = at * 32 + (lane >> 1);
+            dma16(rb, to + oB + at * 1024, in ? (uint32_t)(row * (K / 2) + st * (kBK / 2) + 16 * (lane & 1)) : kOOB, 0);
+            // a row's groups at k = 0 and 32 of the step
+            const uint32_t par = in ? 2u * (row * groups + ((st * kBK + 32 * (lane & 1)) >> gshift)) : kOOB;
+            dma2(rs, to + oS + at * 256, par);
+            if constexpr (ZERO)
+                dma2(rz, to + oZ + at * 256, par);
+        }
+    };
+
+    f4 acc[FM][FN];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int m = m0 + wm + 16 * i + 4 * g + r, n = n0 + wn + 16 * j + l16;
-                if (m < M && n < N)
-                    C[(int64_t)m * N + n] = T::from_f32(acc[i][j][r]);
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = (f4){0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        load(s);
+    const int wn = wave * (16 * FN);
+    for (int st = 0; st < steps; ++st) {
+        // this wavefront's loads of the step are there, then everyone's; and
+        // everyone is done with the buffer that is filled next
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
+        load(st + STAGES - 1);
+        const uint8_t *buf = lds + (st % STAGES) * kStage;
+        uint2 w[FN];
+        uint32_t s16[FN], z16[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int row = wn + 16 * j + l16;
+            w[j] = *(const uint2 *)(buf + oB + row * 32 + g * 8);
+            s16[j] = *(const uint32_t *)(buf + oS + row * 8 + (g >> 1) * 4);
+            z16[j] = ZERO ? *(const uint32_t *)(buf + oZ + row * 8 + (g >> 1) * 4) : 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u4 fa[FM], fb[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                fa[i] = *(const u4 *)(buf + (16 * i + l16) * 128 + 16 * ((2 * g + h) ^ (l16 & 7)));
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const float s = half_bits(s16[j]), off = -half_bits(z16[j]) * s;
+                fb[j] = weights8<T>((h ? w[j].y : w[j].x) ^ kFlip, !ZERO, s16[j] | s16[j] << 16, s, off);
             }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = T::mma(fb[j], fa[i], acc[i][j]);
+        }
+    }
+    // no load may still be on its way to LDS when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // a lane holds four neighbouring columns of one row
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int m = m0 + 16 * i + l16;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int n = n0 + wn + 16 * j + 4 * g;
+            uint16_t *dst = C + (int64_t)m * N + n;
+            uint32_t y[2] = {T::from_f32(acc[i][j][0]) | (uint32_t)T::from_f32(acc[i][j][1]) << 16,
+                             T::from_f32(acc[i][j][2]) | (uint32_t)T::from_f32(acc[i][j][3]) << 16};
+            if (m < M) {
+                if (n + 4 <= N && N % 4 == 0) {
+                    *(u2 *)dst = (u2){y[0], y[1]};
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (n + r < N)
+                            dst[r] = (uint16_t)(y[r >> 1] >> (16 * (r & 1)));
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int BM, int BN, int STAGES>
+hipError_t launch_tiled_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
+                          uint16_t *C, int M, int N, int K, hipStream_t s)
+{
+    const int64_t wgs = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
+    if (!grid_fits(wgs, 256))
+        return kGridTooLarge;
+    const dim3 grid((unsigned)wgs);
+    if (zero)
+        w4g_tiled_kernel<T, BM, BN, STAGES, true><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
+    else
+        w4g_tiled_kernel<T, BM, BN, STAGES, false><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
+    return hipGetLastError();
 }
 
 template <typename T>
@@ -727,11 +821,7 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
         return launch_panel_t<T, 3, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
     if (M <= 64)
         return launch_panel_t<T, 4, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
-    const int64_t wgs = (((int64_t)M + kBM - 1) / kBM) * (((int64_t)N + kBN - 1) / kBN);
-    if (!grid_fits(wgs, 256))
-        return kGridTooLarge;
-    w4g_tiled_kernel<T><<<dim3((unsigned)wgs), 256, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
-    return hipGetLastError();
+    return launch_tiled_t<T, 128, 128, 3>(A, B, scale, zero, gshift, C, M, N, K, s);
 }
 
 }  // namespace

@@ -54,29 +54,44 @@ __device__ __forceinline__ void unpack8(const uint4 raw, float (&y)[8])
     }
 }
 
+// What a lane needs of a token's rotation: its channels' cosines and sines,
+// and the lane that holds their partners (a rotation in halves).
+struct Turn {
+    float4 c[2], s[2];
+    bool in, first;
+    int other;  // partner's place in the row
+};
+
+__device__ __forceinline__ Turn turn_of(const float *cs, const float *sn, int rot, int inter, int sub)
+{
+    Turn t = {};
+    const int hl = rot / 16;  // lanes of one half; rot is a multiple of 16: whole lanes
+    t.in = 8 * sub < rot;
+    t.first = sub < hl;
+    t.other = t.in && !inter ? (t.first ? sub + hl : sub - hl) : sub;
+    if (t.in) {
+        const int at = inter ? 4 * sub : 8 * (t.first ? sub : sub - hl);
+        t.c[0] = *(const float4 *)(cs + at);
+        t.s[0] = *(const float4 *)(sn + at);
+        if (!inter) {
+            t.c[1] = *(const float4 *)(cs + at + 4);
+            t.s[1] = *(const float4 *)(sn + at + 4);
+        }
+    }
+    return t;
+}
+
 // Norm and rotation of one lane's eight channels in type F; the result in
 // the 16-bit type's bits (through fp32, as a conversion from fp64 goes).  A
 // rotation in halves needs another lane's channels: they come over as loaded
-// (four dwords) and are normalized again here.
+// (four dwords) and are scaled again here.
 template <typename T, typename F, int LPR>
-__device__ __forceinline__ void norm_rope(const uint4 raw, const uint16_t *w, double eps, const float *cs, const float *sn,
-                                          int rot, int inter, int sub, uint16_t out[8])
+__device__ __forceinline__ void norm_rope(const uint4 raw, const uint16_t *w, double eps, const Turn &turn, int rot, int inter,
+                                          int sub, uint16_t out[8])
 {
-    const bool in = 8 * sub < rot;  // rot is a multiple of 16: whole lanes
-    const int hl = rot / 16;        // lanes of one half
-    const bool first = sub < hl;
-    const int other = in && !inter ? (first ? sub + hl : sub - hl) : sub;
-    // tables and weights are on their way during the sum
-    float4 c[2] = {}, s[2] = {};
-    if (in) {
-        const int at = inter ? 4 * sub : 8 * (first ? sub : sub - hl);
-        c[0] = *(const float4 *)(cs + at);
-        s[0] = *(const float4 *)(sn + at);
-        if (!inter) {
-            c[1] = *(const float4 *)(cs + at + 4);
-            s[1] = *(const float4 *)(sn + at + 4);
-        }
-    }
+    const bool in = turn.in, first = turn.first;
+    const int other = turn.other;
+    const float4 *c = turn.c, *s = turn.s;
     uint4 wr, wo;
     if (w) {
         wr = *(const uint4 *)(w + 8 * sub);
@@ -210,19 +225,33 @@ __device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8
             F16::from_f32(sc) | (uint32_t)F16::from_f32(mn) << 16;
 }
 
-template <typename T, int LPR, bool CACHE>
+// A row's lanes take HB heads of one token, one after another: what belongs
+// to the token is found once, and the heads' loads are in flight together.
+template <typename T, int LPR, bool CACHE, int HB>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs p)
 {
     constexpr int D = 8 * LPR;
-    const uint32_t heads = p.hq + p.hkv * (CACHE ? 2 : 1);
-    // the grid limit keeps rows below 2^32
-    const uint32_t row = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const uint32_t heads = p.hq + p.hkv * (CACHE ? 2 : 1), units = (heads + HB - 1) / HB;
+    // the grid limit keeps units of all tokens below 2^32
+    const uint32_t unit = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
     const int sub = threadIdx.x % LPR;
-    const uint32_t tok32 = row / heads;
-    const int head = (int)(row - tok32 * heads);
+    const uint32_t tok32 = unit / units;
+    // heads `units` apart: neighbouring rows then hold neighbouring heads, mostly
+    // of one kind, and a wavefront runs one kind's code
+    const int head0 = (int)(unit - tok32 * units);
     const int64_t tok = tok32;
     if (tok >= p.tokens)
         return;
+    uint4 raw[HB];
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+        const int head = min(head0 + i * (int)units, (int)heads - 1);
+        const int kv = head - p.hq;
+        const uint16_t *src = kv < 0                ? p.q + tok * p.q_stride + head * D
+                              : !CACHE || kv < p.hkv ? p.k + tok * p.k_stride + kv * D
+                                                     : p.v + tok * p.v_stride + (kv - p.hkv) * D;
+        raw[i] = *(const uint4 *)(src + 8 * sub);
+    }
     // a row's lanes take one path together: every shuffle stays inside a row
     int64_t pos = 0;
     if (p.rot) {
@@ -230,38 +259,41 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs
         if (pos < 0 || pos >= p.max_pos)
             return;
     }
-    const float *cs = p.cos + pos * (p.rot / 2), *sn = p.sin + pos * (p.rot / 2);
-    uint16_t o[8];
-    if (head < p.hq) {
-        const uint4 raw = *(const uint4 *)(p.q + tok * p.q_stride + head * D + 8 * sub);
-        norm_rope<T, float, LPR>(raw, p.q_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
-        *(uint4 *)(p.q_out + (tok * p.hq + head) * D + 8 * sub) = pack8(o);
-    } else if constexpr (!CACHE) {
-        const int h = head - p.hq;
-        const uint4 raw = *(const uint4 *)(p.k + tok * p.k_stride + h * D + 8 * sub);
-        norm_rope<T, float, LPR>(raw, p.k_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
-        *(uint4 *)(p.k_out + (tok * p.hkv + h) * D + 8 * sub) = pack8(o);
-    } else {
-        const bool isV = head >= p.hq + p.hkv;
-        const int h = head - p.hq - (isV ? p.hkv : 0);
-        const int64_t slot = p.slots[tok];
-        if (slot < 0 || slot >= p.num_pages << p.page_shift)
-            return;
-        const uint16_t *src = isV ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
-        const uint4 raw = *(const uint4 *)(src + h * D + 8 * sub);
-        if (isV) {
-            const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+    const Turn turn = turn_of(p.cos + pos * (p.rot / 2), p.sin + pos * (p.rot / 2), p.rot, p.inter, sub);
+    int64_t slot = 0;
+    bool stored = false;
+    if constexpr (CACHE) {
+        slot = p.slots[tok];
+        stored = slot >= 0 && slot < p.num_pages << p.page_shift;
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[2 * i] = (uint16_t)r[i];
-                o[2 * i + 1] = (uint16_t)(r[i] >> 16);
+    for (int i = 0; i < HB; ++i) {
+        const int head = head0 + i * (int)units, kv = head - p.hq;
+        uint16_t o[8];
+        if (head >= (int)heads)
+            break;
+        if (kv < 0) {
+            norm_rope<T, float, LPR>(raw[i], p.q_weight, p.eps, turn, p.rot, p.inter, sub, o);
+            *(uint4 *)(p.q_out + (tok * p.hq + head) * D + 8 * sub) = pack8(o);
+        } else if constexpr (!CACHE) {
+            norm_rope<T, float, LPR>(raw[i], p.k_weight, p.eps, turn, p.rot, p.inter, sub, o);
+            *(uint4 *)(p.k_out + (tok * p.hkv + kv) * D + 8 * sub) = pack8(o);
+        } else if (stored) {
+            const bool isV = kv >= p.hkv;
+            if (isV) {
+                const uint32_t r[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[2 * j] = (uint16_t)r[j];
+                    o[2 * j + 1] = (uint16_t)(r[j] >> 16);
+                }
+            } else {
+                norm_rope<T, double, LPR>(raw[i], p.k_weight, p.eps, turn, p.rot, p.inter, sub, o);
             }
-        } else {
-            norm_rope<T, double, LPR>(raw, p.k_weight, p.eps, cs, sn, p.rot, p.inter, sub, o);
+            const int page_size = 1 << p.page_shift;
+            store_kv4<T, LPR>(o, isV, p.cache + head_base(slot >> p.page_shift, isV ? kv - p.hkv : kv, p.hkv, page_size, D),
+                              (uint32_t)slot & (page_size - 1), page_size, sub);
         }
-        const int page_size = 1 << p.page_shift;
-        store_kv4<T, LPR>(o, isV, p.cache + head_base(slot >> p.page_shift, h, p.hkv, page_size, D),
-                          (uint32_t)slot & (page_size - 1), page_size, sub);
     }
 }
 
@@ -306,21 +338,35 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(const uint8_t *cache
     *(uint4 *)((isV ? v : k) + (tok * hkv + h) * D + 8 * sub) = pack8(o);
 }
 
-template <typename T, bool CACHE>
-hipError_t launch_rope_t(const QkRopeArgs &p, int64_t rows, hipStream_t s)
+template <typename T, int LPR, bool CACHE>
+hipError_t launch_rope_t(const QkRopeArgs &p, hipStream_t s)
 {
-    const int per = kThreads / (p.D / 8);
-    const int64_t wgs = (rows + per - 1) / per;
+    const int64_t heads = p.hq + (int64_t)p.hkv * (CACHE ? 2 : 1);
+    // Four heads a row of lanes once that still gives each of the 1024 SIMDs
+    // four wavefronts (8191 tokens, 32 + 8 heads of 128: 35.7 against 38.4 us);
+    // one for shorter calls, and where a cache is written: its three kinds of
+    // heads then share wavefronts (4097 tokens, 16 + 16 + 16 of 64: 17.4 us,
+    // two heads 18.9, four 18.7).
+    constexpr int kPer = kThreads / LPR, kMany = CACHE ? 1 : 4;
+    const bool many = !CACHE && p.tokens * heads * LPR >= 4 * 64 * 4096;
+    const int64_t units = p.tokens * (many ? (heads + 3) / 4 : heads);
+    const int64_t wgs = (units + kPer - 1) / kPer;
     if (!grid_fits(wgs, kThreads))
         return kGridTooLarge;
     const dim3 grid((unsigned)wgs);
-    if (p.D == 64)
-        qk_norm_rope_kernel<T, 8, CACHE><<<grid, kThreads, 0, s>>>(p);
-    else if (p.D == 128)
-        qk_norm_rope_kernel<T, 16, CACHE><<<grid, kThreads, 0, s>>>(p);
+    if (many)
+        qk_norm_rope_kernel<T, LPR, CACHE, kMany><<<grid, kThreads, 0, s>>>(p);
     else
-        qk_norm_rope_kernel<T, 32, CACHE><<<grid, kThreads, 0, s>>>(p);
+        qk_norm_rope_kernel<T, LPR, CACHE, 1><<<grid, kThreads, 0, s>>>(p);
     return hipGetLastError();
+}
+
+template <typename T, bool CACHE>
+hipError_t launch_rope_d(const QkRopeArgs &p, hipStream_t s)
+{
+    return p.D == 64    ? launch_rope_t<T, 8, CACHE>(p, s)
+           : p.D == 128 ? launch_rope_t<T, 16, CACHE>(p, s)
+                        : launch_rope_t<T, 32, CACHE>(p, s);
 }
 
 template <typename T>
@@ -345,10 +391,9 @@ hipError_t launch_read_t(const uint8_t *cache, int64_t num_pages, int page_shift
 
 hipError_t launch_qk_norm_rope(const QkRopeArgs &p, bool bf16, hipStream_t s)
 {
-    const int64_t rows = p.tokens * (p.hq + (int64_t)p.hkv * (p.cache ? 2 : 1));
     if (p.cache)
-        return bf16 ? launch_rope_t<BF16, true>(p, rows, s) : launch_rope_t<F16, true>(p, rows, s);
-    return bf16 ? launch_rope_t<BF16, false>(p, rows, s) : launch_rope_t<F16, false>(p, rows, s);
+        return bf16 ? launch_rope_d<BF16, true>(p, s) : launch_rope_d<F16, true>(p, s);
+    return bf16 ? launch_rope_d<BF16, false>(p, s) : launch_rope_d<F16, false>(p, s);
 }
 
 hipError_t launch_kv4_read(const uint8_t *cache, int64_t num_pages, int page_shift, int hkv, int D, const int64_t *slots,
