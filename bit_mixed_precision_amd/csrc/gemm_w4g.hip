@@ -581,18 +581,23 @@ __global__ __launch_bounds__(256) void w4g_join_kernel(const float *__restrict__
     C[i] = T::from_f32(v);
 }
 
+// Tiles of BM x BN outputs.
+int64_t tiles_of(int M, int N, int BM, int BN) { return (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN); }
+
 // Parts of K with a workspace: enough workgroups for the chip's 256 CUs, none
-// under four steps of K.  M <= 16 is not split: joining costs a launch
+// under four 128-wide steps.  M <= 16 is not split: joining costs a launch
 // (4 us), more than it gains (M = 16, N = K = 4096: 8.1 us whole, 10.0 in two).
 int k_split(int M, int N, int K)
 {
-    if (M <= 16 || M > 64)
+    if (M <= 16)
         return 1;
-    const int rows = M <= 32 ? 32 : 128;
-    const int tiles = (N + rows - 1) / rows, steps = (K + 127) / 128;
-    int n = (256 + tiles / 2) / tiles;
+    const int64_t tiles = M <= 32   ? tiles_of(M, N, 32, 32)
+                          : M <= 64 ? tiles_of(M, N, 64, 128)
+                                    : tiles_of(M, N, 64, 64);
+    const int64_t steps = (K + 127) / 128;
+    int64_t n = (256 + tiles / 2) / tiles;
     n = n < steps / 4 ? n : steps / 4;
-    return n < 1 ? 1 : n > 16 ? 16 : n;
+    return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 
 template <typename T, int NA, int NB, int WAVES, int DEPTH>
@@ -633,20 +638,27 @@ hipError_t launch_panel_t(const uint16_t *A, const uint8_t *B, const uint16_t *s
 // tiled
 // ---------------------------------------------------------------------------
 
-// The four codes pairs of a dword times scale, in order, each weight rounded
-// once to T.  A byte in both halves, masked to its low and high nibble, is
+// The eight codes of a dword (two's complement nibbles) times scale, in
+// order, each weight rounded once to T.  A byte in both halves, masked to its
+// low and high nibble, is with these exponent bits (and the sign bits turned)
 // 1024 + u and 1024 + 16 u as fp16; one packed multiply-add makes both the
 // integer u - 8.  Without zero points fp16 takes the product there; else
-// (u - 8) s - z s goes through fp32.
+// (u - 8) s - z s goes through fp32.  Mask and bits are held in registers,
+// which lets both be one instruction.
+struct NibbleBits {
+    uint32_t mask = 0x00f0000fu, bits = 0x64806408u;
+    __device__ __forceinline__ void hold() { asm volatile("" : "+s"(mask), "+v"(bits)); }
+};
+
 template <typename T>
-__device__ __forceinline__ u4 weights8(uint32_t w, bool plain, uint32_t s2, float s, float off)
+__device__ __forceinline__ u4 weights8(uint32_t w, const NibbleBits &k, bool plain, uint32_t s2, float s, float off)
 {
     const h2 mul = {(_Float16)1.0f, (_Float16)0.0625f}, add = {(_Float16)-1032.0f, (_Float16)-72.0f};
     u4 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t b = __builtin_amdgcn_perm(0u, w, 0x0c000c00u | (uint32_t)i << 16 | (uint32_t)i);
-        const h2 u = __builtin_elementwise_fma(__builtin_bit_cast(h2, (b & 0x00f0000fu) | 0x64006400u), mul, add);
+        const h2 u = __builtin_elementwise_fma(__builtin_bit_cast(h2, (b & k.mask) ^ k.bits), mul, add);
         if (!T::kBf16 && plain) {
             y[i] = __builtin_bit_cast(uint32_t, u * __builtin_bit_cast(h2, s2));
         } else {
@@ -655,6 +667,18 @@ __device__ __forceinline__ u4 weights8(uint32_t w, bool plain, uint32_t s2, floa
         }
     }
     return y;
+}
+
+// Permutation of the eight 16-byte pieces of LDS row r, for 16-byte reads of
+// 16 rows by lanes (l, g) with piece 2 g + h.  The hardware serves lanes {0-3,
+// 12-15, 20-27} and {4-11, 16-19, 28-31} (and the same + 32) together, from 64
+// banks of four bytes: rows 0-3, 12-15 of one g with rows 4-11 of the next,
+// whose pieces differ in bit 1.  Rows of the first set take even pieces, of
+// the second odd ones, and differ among themselves in the other two bits.
+__device__ __forceinline__ int swizzle(int r)
+{
+    const int q = r >> 1;
+    return ((q >> 1 ^ q >> 2) & 1) | (q & 1) << 1 | (q & 4);
 }
 
 constexpr int kBK = 64;
@@ -677,12 +701,14 @@ template <typename T, int BM, int BN, int STAGES, bool ZERO>
 __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
                                                            const uint16_t *__restrict__ scale,
                                                            const uint16_t *__restrict__ zero, int gshift,
-                                                           uint16_t *__restrict__ C, int M, int N, int K)
+                                                           uint16_t *__restrict__ C, float *__restrict__ part, int M, int N,
+                                                           int K, int ksplit)
 {
     constexpr int FM = BM / 16, FN = BN / 64;
     constexpr int kA = BM / 32, kB = BN < 128 ? 1 : BN / 128;  // loads of a wavefront a step: A, codes (and scales, zeros)
     constexpr int kLoads = kA + kB * (ZERO ? 3 : 2);
     constexpr int oB = BM * 128, oS = oB + BN * 32, oZ = oS + BN * 8, kStage = oZ + (ZERO ? BN * 8 : 0);
+    constexpr int kSchedMfma = 8, kSchedValu = 2, kSchedDsRead = 0x100, kValu = (T::kBf16 || ZERO ? 30 : 20) * FN / (FM * FN) + 1;
     static_assert(BM % 32 == 0 && (BN == 64 || BN % 128 == 0), "whole loads");
     static_assert((STAGES - 1) * kLoads < 64, "the wait counter");
     __shared__ __align__(1024) uint8_t lds[STAGES * kStage];
@@ -691,8 +717,10 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
     const int g = lane >> 4, l16 = lane & 15;
     const int tilesM = (M + BM - 1) / BM;
     // neighbouring workgroups share weight rows: a die's L2 then reads them once
-    const int m0 = blockIdx.x % tilesM * BM, n0 = blockIdx.x / tilesM * BN;
-    const int groups = K >> gshift, steps = K / kBK;
+    const int split = blockIdx.x % ksplit, tile = blockIdx.x / ksplit;
+    const int m0 = tile % tilesM * BM, n0 = tile / tilesM * BN;
+    const int groups = K >> gshift, per = (K / kBK + ksplit - 1) / ksplit;
+    const int first = split * per, steps = min(first + per, K / kBK);
     const int mrows = min(BM, M - m0), nrows = min(BN, N - n0);
     const v4si ra = make_rsrc(A + (int64_t)m0 * K, (uint32_t)mrows * K * 2);
     const v4si rb = make_rsrc(B + (int64_t)n0 * (K / 2), (uint32_t)nrows * (K / 2));
@@ -700,12 +728,12 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
     const v4si rz = make_rsrc((ZERO ? zero : scale) + (int64_t)n0 * groups, (uint32_t)nrows * groups * 2);
     const uint32_t base = lds_addr(lds);
 
-    const auto load = [&](int st) {
-        const uint32_t to = __builtin_amdgcn_readfirstlane(base + (uint32_t)(st % STAGES) * kStage);
+    const auto load = [&](int st, int slot) {
+        const uint32_t to = base + slot * kStage;
         const bool in = st < steps;  // past the end: zeros, no access
 #pragma unroll
         for (int i = 0; i < kA; ++i) {
-            const int row = (wave * kA + i) * 8 + (lane >> 3), piece = (lane & 7) ^ (lane >> 3);
+            const int row = (wave * kA + i) * 8 + (lane >> 3), piece = (lane & 7) ^ swizzle(row & 15);
             dma16(ra, to + (wave * kA + i) * 1024, in ? (uint32_t)(2 * (row * K + st * kBK) + 16 * piece) : kOOB, 0);
         }
 #pragma unroll
@@ -729,16 +757,19 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
             acc[i][j] = (f4){0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
-        load(s);
+        load(first + s, s);
     const int wn = wave * (16 * FN);
-    for (int st = 0; st < steps; ++st) {
+    NibbleBits nibbles;
+    nibbles.hold();
+    const auto step = [&](int st, int slot) {
         // this wavefront's loads of the step are there, then everyone's; and
         // everyone is done with the buffer that is filled next
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
-        load(st + STAGES - 1);
-        const uint8_t *buf = lds + (st % STAGES) * kStage;
+        load(st + STAGES - 1, (slot + STAGES - 1) % STAGES);
+        const uint8_t *buf = lds + slot * kStage;
         uint2 w[FN];
         uint32_t s16[FN], z16[FN];
+        u4 fa[2][FM], fb[2][FN];
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int row = wn + 16 * j + l16;
@@ -746,23 +777,46 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
             s16[j] = *(const uint32_t *)(buf + oS + row * 8 + (g >> 1) * 4);
             z16[j] = ZERO ? *(const uint32_t *)(buf + oZ + row * 8 + (g >> 1) * 4) : 0u;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u4 fa[FM], fb[FN];
+        const auto read_a = [&](int h) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                fa[i] = *(const u4 *)(buf + (16 * i + l16) * 128 + 16 * ((2 * g + h) ^ (l16 & 7)));
+                fa[h][i] = *(const u4 *)(buf + (16 * i + l16) * 128 + 16 * ((2 * g + h) ^ swizzle(l16)));
+        };
+        const auto decode = [&](int h) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 const float s = half_bits(s16[j]), off = -half_bits(z16[j]) * s;
-                fb[j] = weights8<T>((h ? w[j].y : w[j].x) ^ kFlip, !ZERO, s16[j] | s16[j] << 16, s, off);
+                fb[h][j] = weights8<T>(h ? w[j].y : w[j].x, nibbles, !ZERO, s16[j] | s16[j] << 16, s, off);
             }
+        };
+        const auto products = [&](int h) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    acc[i][j] = T::mma(fb[j], fa[i], acc[i][j]);
+                    acc[i][j] = T::mma(fb[h][j], fa[h][i], acc[i][j]);
+        };
+        read_a(0);
+        decode(0);
+        __builtin_amdgcn_sched_barrier(0);
+        // the second half's reads and decode go between the first half's products
+        read_a(1);
+        decode(1);
+        products(0);
+#pragma unroll
+        for (int i = 0; i < FM * FN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedValu, kValu, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        products(1);
+    };
+    for (int st = first; st < steps; st += STAGES) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s)
+            if (st + s < steps)
+                step(st + s, s);
     }
     // no load may still be on its way to LDS when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -773,6 +827,14 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int n = n0 + wn + 16 * j + 4 * g;
+            if (part) {
+                float *to = part + ((int64_t)split * M + m) * N + n;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (m < M && n + r < N)
+                        to[r] = acc[i][j][r];
+                continue;
+            }
             uint16_t *dst = C + (int64_t)m * N + n;
             uint32_t y[2] = {T::from_f32(acc[i][j][0]) | (uint32_t)T::from_f32(acc[i][j][1]) << 16,
                              T::from_f32(acc[i][j][2]) | (uint32_t)T::from_f32(acc[i][j][3]) << 16};
@@ -792,16 +854,22 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
 
 template <typename T, int BM, int BN, int STAGES>
 hipError_t launch_tiled_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
-                          uint16_t *C, int M, int N, int K, hipStream_t s)
+                          uint16_t *C, int M, int N, int K, float *ws, int ksplit, hipStream_t s)
 {
-    const int64_t wgs = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
-    if (!grid_fits(wgs, 256))
+    const int64_t wgs = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN) * ksplit;
+    const int64_t total = (int64_t)M * N;
+    if (!grid_fits(wgs, 256) || (ksplit > 1 && !grid_fits((total + 255) / 256, 256)))
         return kGridTooLarge;
     const dim3 grid((unsigned)wgs);
+    float *part = ksplit > 1 ? ws : nullptr;
     if (zero)
-        w4g_tiled_kernel<T, BM, BN, STAGES, true><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
+        w4g_tiled_kernel<T, BM, BN, STAGES, true><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, part, M, N, K, ksplit);
     else
-        w4g_tiled_kernel<T, BM, BN, STAGES, false><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
+        w4g_tiled_kernel<T, BM, BN, STAGES, false><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, part, M, N, K, ksplit);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || ksplit == 1)
+        return e;
+    w4g_join_kernel<T><<<dim3((unsigned)((total + 255) / 256)), 256, 0, s>>>(ws, C, total, ksplit);
     return hipGetLastError();
 }
 
@@ -821,7 +889,14 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
         return launch_panel_t<T, 3, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
     if (M <= 64)
         return launch_panel_t<T, 4, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
-    return launch_tiled_t<T, 128, 128, 3>(A, B, scale, zero, gshift, C, M, N, K, s);
+    // Larger tiles move less, but need enough of them (M = 2048, N = K = 4096:
+    // 128 x 128 78 us, 128 x 64 99, 64 x 64 145; M = 512, K = 11008: 136, 98,
+    // 120; M = 100: 53, 37, 28, and with K in parts less).
+    if (tiles_of(M, N, 128, 128) >= 256)
+        return launch_tiled_t<T, 128, 128, 3>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
+    if (tiles_of(M, N, 128, 64) >= 256)
+        return launch_tiled_t<T, 128, 64, 4>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
+    return launch_tiled_t<T, 64, 64, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
 }
 
 }  // namespace
