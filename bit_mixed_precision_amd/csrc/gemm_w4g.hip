@@ -3,10 +3,11 @@
 //   C[m,n] = T(sum_k A[m,k] (c[n,k] - z[n,g]) s[n,g]),  g = k / group,
 // codes c in -8..7 packed as by bq_pack_int4 (u = c + 8 = nibble ^ 8), fp32
 // sums.  Three kernels by M:
-//  * gemv (M <= 4): dot products, a stream over B;
-//  * skinny (M <= 64): matrix instructions on the bare codes, K split over a
-//    workgroup's wavefronts (and over workgroups with a workspace);
-//  * tiled: the weights rounded once to T, through LDS.
+//  * gemv (M = 1): dot products, a stream over B;
+//  * skinny (M <= 32): matrix instructions on the bare codes, K split over a
+//    workgroup's wavefronts;
+//  * tiled: the weights rounded once to T between LDS and the matrix
+//    instructions, K in parts over workgroups where tiles are few.
 // The first two keep scale and zero point outside the sums:
 //   sum_g s_g (sum_k a u - (8 + z_g) sum_k a).
 #include "bq_internal.h"
@@ -15,6 +16,10 @@
 
 namespace bq {
 namespace {
+
+// M up to which the skinny kernel is taken: 16 weight rows a workgroup and all
+// of A's (M = 32, N = K = 4096: 10.2 us, tiled 13.3; M = 64: 16.7, tiled 15.4).
+constexpr int kSkinnyM = 32;
 
 constexpr uint32_t kFlip = 0x88888888u;  // two's complement nibble -> c + 8
 
@@ -230,57 +235,52 @@ __device__ __forceinline__ void transpose4(uint32_t w[4])
     w[3] = s[1];
 }
 
-// Scale and zero point of np groups from g0 on of ROWS rows, one dword each,
-// to LDS; eight loads of each are in flight per thread.
-template <int ROWS, int THREADS>
-__device__ __forceinline__ void params_to_lds(uint32_t *par, int pitch, int np, Buf bs, Buf bz, int g0, int groups)
+// What a wavefront loads for CH steps of 128.
+template <int NB, int NL, int CH>
+struct Steps {
+    u4 w[CH][NB], a[CH][NL];
+    uint16_t s[CH][NB], z[CH][NB];  // four groups each, one a quarter of the lanes
+};
+
+__device__ __forceinline__ void wave_sync()
 {
-    constexpr int kPer = THREADS / ROWS, kFly = 8;
-    const int n = threadIdx.x / kPer;
-    for (int i0 = threadIdx.x % kPer; i0 < np; i0 += kPer * kFly) {
-        uint16_t s[kFly], z[kFly];
-#pragma unroll
-        for (int f = 0; f < kFly; ++f) {
-            const int i = i0 + f * kPer;
-            const uint32_t at = i < np && g0 + i < groups ? 2 * (n * groups + g0 + i) : kOut;
-            s[f] = load2(bs, at);
-            z[f] = load2(bz, at);
-        }
-#pragma unroll
-        for (int f = 0; f < kFly; ++f)
-            if (i0 + f * kPer < np)
-                par[n * pitch + i0 + f * kPer] = s[f] | (uint32_t)z[f] << 16;
-    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// NB tiles of 16 weight rows x NA tiles of 16 activation rows a workgroup;
-// wavefront w takes the 128-wide steps w, w + WAVES, ... of the workgroup's
-// part of K.  A 16-byte load hands lane (n, g) the 32 codes of row n at
-// k = 32 g; the transpose makes matrix step j cover k = 32 j .. 32 j + 31,
-// which lies in one group.  Scales and zero points of a block of K go to LDS
-// first, row by row: read where they are used, two bytes of a line each,
-// they cost as many cache lines as the codes.  Codes are in flight DEPTH steps
-// ahead, activations (from the caches) one.
-constexpr int kParamWords = 8192;  // parameters in LDS: 16 NB rows x groups
-
-template <typename T, int NA, int NB, int WAVES, int DEPTH>
+// NB tiles of 16 weight rows x up to 4 NL activation rows a workgroup, whose
+// wavefronts take neighbouring parts of its K in steps of 128, CH steps'
+// loads at a time and the next CH in flight.
+//  * A 16-byte load hands lane (n, g) the 32 codes of row n at k = 32 g; the
+//    transpose makes matrix step j cover k = 32 j .. 32 j + 31, which lies in
+//    one group.
+//  * A is loaded in whole 256-byte pieces of rows, as many loads as there are
+//    four rows, and goes through a part of LDS of the wavefront's own into the
+//    codes' pair order: operand loads straight from memory, 64 bytes of 16
+//    rows each, took longer than the codes (M = 8, N = 12288, K = 4096: 16.9
+//    us, without them 10.2).  Pieces are permuted by the row's number: the 16
+//    rows of an operand read fall into different banks.
+//  * Scales and zero points come four groups of a row a load and are handed to
+//    the lanes of their row when the group ends.
+template <typename T, int NA, int NB, int NL, int WAVES, int CH>
 __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
                                                                 const uint16_t *__restrict__ scale,
                                                                 const uint16_t *__restrict__ zero, int gshift,
-                                                                uint16_t *__restrict__ C, float *__restrict__ part, int M,
-                                                                int N, int K, int ksplit)
+                                                                uint16_t *__restrict__ C, int M, int N, int K)
 {
-    constexpr int kRows = 16 * NB;
+    constexpr int kRows = 16 * NB, kLoaded = 4 * NL;
+    static_assert(kLoaded <= 16 * NA && (NA == 1 || kLoaded == 16 * NA), "rows of A");
     __shared__ union {
-        uint32_t par[kParamWords + kRows];
+        uint8_t a[WAVES][kLoaded][256];
         float red[WAVES][16][kRows + 4];
     } sh;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int split = blockIdx.x % ksplit, n0 = blockIdx.x / ksplit * kRows;
-    const int steps = (K + 127) / 128, per = (steps + ksplit - 1) / ksplit;
-    const int first = split * per, last = min(first + per, steps);
+    const int n0 = blockIdx.x * kRows;
+    const int steps = (K + 127) / 128, per = (steps + WAVES - 1) / WAVES;
+    const int first = wave * per, last = min(first + per, steps);
     const int groups = K >> gshift;
     const int sshift = 7 - gshift;  // groups of a step, as a shift
 
@@ -300,90 +300,98 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
     const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + (int64_t)n0 * (K / 2), (int64_t)rows * (K / 2));
     const Buf bs = buffer(scale + (int64_t)n0 * groups, (int64_t)rows * groups * 2);
     const Buf bz = buffer((zero ? zero : scale) + (int64_t)n0 * groups, zero ? (int64_t)rows * groups * 2 : 0);
-    const auto load_w = [&](u4 *w, int st, int end) {
-        const int k = st * 128 + 32 * g;
+    const auto load = [&](Steps<NB, NL, CH> &x, int c0) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-            w[b] = load16(bb, st < end && k < K ? (16 * b + l16) * (K / 2) + k / 2 : kOut);
-    };
-    const auto load_a = [&](u4 (*x)[4], int st, int end) {
-#pragma unroll
-        for (int a = 0; a < NA; ++a)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int ka = st * 128 + 32 * j + 8 * g;
-                x[a][j] = load16(ba, st < end && ka < K ? 2 * ((16 * a + l16) * K + ka) : kOut);
-            }
-    };
-    const int block = (kParamWords / kRows) >> sshift;  // steps whose parameters fit
-    for (int b0 = first; b0 < last; b0 += block) {
-        const int b1 = min(b0 + block, last);
-        u4 w[DEPTH][NB], x[2][NA][4];
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            load_w(w[d], b0 + wave + d * WAVES, b1);
-        load_a(x[0], b0 + wave, b1);
-        const int np = (b1 - b0) << sshift, pitch = np + 1;
-        if (b0 != first)
-            __syncthreads();
-        params_to_lds<kRows, 64 * WAVES>(sh.par, pitch, np, bs, bz, b0 << sshift, groups);
-        __syncthreads();
-        const auto step = [&](const u4 *wv, u4 (*xv)[4], int st) {
-            uint32_t c[NB][4];
+        for (int c = 0; c < CH; ++c) {
+            const int st = c0 + c, k = st * 128 + 32 * g, ka = st * 128 + 8 * l16;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c[b][j] = wv[b][j];
-                transpose4(c[b]);
+                const uint32_t n = 16 * b + l16;
+                x.w[c][b] = load16(bb, st < last && k < K ? n * (K / 2) + k / 2 : kOut);
+                // quarter g: group 4 c + g of the CH steps
+                const int gi = (c0 << sshift) + 4 * c + g;
+                const uint32_t at = c < (CH << sshift) / 4 + (CH < 4) && gi < groups ? 2 * (n * groups + gi) : kOut;
+                x.s[c][b] = load2(bs, at);
+                x.z[c][b] = load2(bz, at);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                u4 q[NA];
+            for (int i = 0; i < NL; ++i)
+                x.a[c][i] = load16(ba, st < last && ka < K ? 2 * ((4 * i + g) * K + ka) : kOut);
+        }
+    };
+    uint8_t(*const sa)[256] = sh.a[wave];
+    const auto step = [&](const Steps<NB, NL, CH> &x, int c) {
 #pragma unroll
-                for (int a = 0; a < NA; ++a) {
-                    const u4 v = xv[a][j];
-                    q[a] = (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
-                    sum[a] = T::mma(q[a], ones, sum[a]);
-                }
+        for (int i = 0; i < NL; ++i) {
+            const int row = 4 * i + g;
+            const u4 v = x.a[c][i];
+            *(u4 *)&sa[row][16 * (l16 ^ (row & 15))] =
+                (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
+        }
+        wave_sync();
+        uint32_t w[NB][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[b][j] = x.w[c][b][j];
+            transpose4(w[b]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u4 q[NA];
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                // rows past the loaded ones give outputs that are not written
+                const int row = (16 * a + l16) % kLoaded;
+                q[a] = *(const u4 *)&sa[row][16 * ((4 * j + g) ^ (row & 15))];
+                sum[a] = T::mma(q[a], ones, sum[a]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const u4 op = codes_op<T>(w[b][j] ^ kFlip);
+#pragma unroll
+                for (int a = 0; a < NA; ++a)
+                    part_acc[a][b] = T::mma(q[a], op, part_acc[a][b]);
+            }
+            if ((j & gmask) == gmask) {  // a group ends
+                const int gi = (c << sshift) + (j >> (2 - sshift));  // of the CH steps
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const u4 op = codes_op<T>(c[b][j] ^ kFlip);
+                    uint32_t sz = 0;
 #pragma unroll
-                    for (int a = 0; a < NA; ++a)
-                        part_acc[a][b] = T::mma(q[a], op, part_acc[a][b]);
-                }
-                if ((j & gmask) == gmask) {  // a group ends
-                    const int at = ((st - b0) << sshift) + (j >> (2 - sshift));
+                    for (int i = 0; i < CH; ++i)
+                        if (gi >> 2 == i)
+                            sz = x.s[i][b] | (uint32_t)x.z[i][b] << 16;
+                    sz = __shfl(sz, l16 + 16 * (gi & 3), 64);
+                    const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
+                    const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint32_t sz = sh.par[(16 * b + l16) * pitch + at];
-                        const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
-                        const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
+                    for (int a = 0; a < NA; ++a) {
 #pragma unroll
-                        for (int a = 0; a < NA; ++a) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[a][b][i] += s * (part_acc[a][b][i] - z * sum[a][i]);
-                            part_acc[a][b] = zero4;
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            acc[a][b][i] += s * (part_acc[a][b][i] - z * sum[a][i]);
+                        part_acc[a][b] = zero4;
                     }
-#pragma unroll
-                    for (int a = 0; a < NA; ++a)
-                        sum[a] = zero4;
                 }
-            }
-        };
-        for (int st = b0 + wave; st < b1; st += DEPTH * WAVES) {
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                const int s = st + d * WAVES;
-                if (s < b1) {
-                    load_a(x[(d + 1) & 1], s + WAVES, b1);
-                    step(w[d], x[d & 1], s);
-                    load_w(w[d], s + DEPTH * WAVES, b1);
-                }
+                for (int a = 0; a < NA; ++a)
+                    sum[a] = zero4;
             }
+        }
+        wave_sync();
+    };
+    if (first < last) {
+        Steps<NB, NL, CH> x, y;
+        load(x, first);
+        for (int c0 = first; c0 < last; c0 += CH) {
+            if (c0 + CH < last)
+                load(y, c0 + CH);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (c0 + c < last)
+                    step(x, c);
+            x = y;
         }
     }
     __syncthreads();
@@ -404,168 +412,10 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
 #pragma unroll
             for (int q = 0; q < WAVES; ++q)
                 v += sh.red[q][m][n];
-            if (16 * a + m < M && n0 + n < N) {
-                const int64_t at = (int64_t)(16 * a + m) * N + n0 + n;
-                if (part)
-                    part[(int64_t)split * M * N + at] = v;
-                else
-                    C[at] = T::from_f32(v);
-            }
+            if (16 * a + m < M && n0 + n < N)
+                C[(int64_t)(16 * a + m) * N + n0 + n] = T::from_f32(v);
         }
     }
-}
-
-// ---------------------------------------------------------------------------
-// panel
-// ---------------------------------------------------------------------------
-
-// 16 weight rows a wavefront, WAVES * 16 a workgroup, all of the up to 16 NA
-// activation rows, and the workgroup's part of K in 128-wide steps.  A step
-// of A is put into LDS by the whole workgroup (in pair order, with the sums
-// over each group), so the caches deliver it once per WAVES * 16 weight rows;
-// each row's 16-byte pieces are permuted by the row's number, which gives the
-// operand reads of 16 rows different banks.  Codes go straight to registers,
-// DEPTH steps ahead; activations are loaded two steps ahead.
-template <typename T, int NA, int WAVES, int DEPTH>
-__global__ __launch_bounds__(64 * WAVES) void w4g_panel_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
-                                                               const uint16_t *__restrict__ scale,
-                                                               const uint16_t *__restrict__ zero, int gshift,
-                                                               uint16_t *__restrict__ C, float *__restrict__ part, int M, int N,
-                                                               int K, int ksplit)
-{
-    constexpr int kRows = 16 * WAVES, kThreads = 64 * WAVES;
-    constexpr int kPieces = 16 * NA * 16, kPer = (kPieces + kThreads - 1) / kThreads;
-    constexpr int kWords = 16384;  // parameters of a block of K in LDS
-    __shared__ __align__(16) uint8_t sa[2][16 * NA][256];
-    __shared__ __align__(16) float ssum[2][4][16 * NA];
-    __shared__ uint32_t par[kWords + kRows];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4, l16 = lane & 15;
-    const int split = blockIdx.x % ksplit, n0 = blockIdx.x / ksplit * kRows;
-    const int steps = (K + 127) / 128, per = (steps + ksplit - 1) / ksplit;
-    const int first = split * per, last = min(first + per, steps);
-    const int groups = K >> gshift, sshift = 7 - gshift;
-    const int gmask = (1 << (gshift - 5)) - 1;
-    const int rows = min(kRows, N - n0);
-    const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + (int64_t)n0 * (K / 2), (int64_t)rows * (K / 2));
-    const Buf bs = buffer(scale + (int64_t)n0 * groups, (int64_t)rows * groups * 2);
-    const Buf bz = buffer((zero ? zero : scale) + (int64_t)n0 * groups, zero ? (int64_t)rows * groups * 2 : 0);
-    const int wrow = 16 * wave + l16;
-
-    const auto load_w = [&](int st) {
-        const int k = st * 128 + 32 * g;
-        return load16(bb, st < last && k < K ? wrow * (K / 2) + k / 2 : kOut);
-    };
-    const auto load_a = [&](u4 *x, int st) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = threadIdx.x + i * kThreads, k = st * 128 + 8 * (e & 15);
-            x[i] = load16(ba, e < kPieces && st < last && k < K ? 2 * ((e >> 4) * K + k) : kOut);
-        }
-    };
-    const auto put_a = [&](const u4 *x, int buf) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = threadIdx.x + i * kThreads, row = e >> 4, piece = e & 15;
-            const u4 v = {pack_lo(x[i].x, x[i].z), pack_hi(x[i].x, x[i].z), pack_lo(x[i].y, x[i].w), pack_hi(x[i].y, x[i].w)};
-            float s = T::dot2(v.x, T::kOnes, T::dot2(v.y, T::kOnes, T::dot2(v.z, T::kOnes, T::dot2(v.w, T::kOnes, 0.0f))));
-            s += __shfl_xor(s, 1, 64);
-            s += __shfl_xor(s, 2, 64);
-            if (gshift > 5)
-                s += __shfl_xor(s, 4, 64);
-            if (gshift > 6)
-                s += __shfl_xor(s, 8, 64);
-            if (kPieces % kThreads == 0 || e < kPieces) {
-                *(u4 *)&sa[buf][row][16 * (piece ^ (row & 15))] = v;
-                if ((piece & (4 * gmask + 3)) == 0)
-                    ssum[buf][piece >> (gshift - 3)][row] = s;
-            }
-        }
-    };
-
-    f4 acc[NA], part_acc[NA];
-    const f4 zero4 = {0, 0, 0, 0};
-#pragma unroll
-    for (int a = 0; a < NA; ++a)
-        acc[a] = part_acc[a] = zero4;
-    constexpr int kAhead = DEPTH < 4 ? 2 : 4;  // steps of A in flight
-    u4 w[DEPTH], av[kAhead][kPer];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        w[d] = load_w(first + d);
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-        load_a(av[d], first + d);
-    const int block = (kWords / kRows) >> sshift;  // steps whose parameters fit
-    int b0 = first, pitch = 0;
-    const auto put_par = [&]() {
-        const int np = (min(b0 + block, last) - b0) << sshift;
-        pitch = np + 1;
-        params_to_lds<kRows, kThreads>(par, pitch, np, bs, bz, b0 << sshift, groups);
-    };
-    if (first < last) {
-        put_par();
-        put_a(av[0], 0);
-    }
-    __syncthreads();
-    const auto step = [&](const u4 &wv, int st, int buf) {
-        uint32_t c[4] = {wv.x, wv.y, wv.z, wv.w};
-        transpose4(c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const u4 op = codes_op<T>(c[j] ^ kFlip);
-#pragma unroll
-            for (int a = 0; a < NA; ++a)
-                part_acc[a] = T::mma(*(const u4 *)&sa[buf][16 * a + l16][16 * ((4 * j + g) ^ l16)], op, part_acc[a]);
-            if ((j & gmask) == gmask) {  // a group ends
-                const int gi = j >> (2 - sshift);
-                const uint32_t sz = par[wrow * pitch + ((st - b0) << sshift) + gi];
-                const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
-                const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
-#pragma unroll
-                for (int a = 0; a < NA; ++a) {
-                    const f4 sum = *(const f4 *)&ssum[buf][gi][16 * a + 4 * g];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[a][i] += s * (part_acc[a][i] - z * sum[i]);
-                    part_acc[a] = zero4;
-                }
-            }
-        }
-    };
-    static_assert(DEPTH % 2 == 0, "a step's buffer is its parity");
-    for (int st = first; st < last; st += DEPTH) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int s = st + d;
-            if (s < last) {
-                if (s == b0 + block) {  // the parameters' next block
-                    b0 = s;
-                    put_par();
-                    __syncthreads();
-                }
-                load_a(av[d % kAhead], s + kAhead);
-                step(w[d], s, d & 1);
-                w[d] = load_w(s + DEPTH);
-                put_a(av[(d + 1) % kAhead], (d + 1) & 1);
-                __syncthreads();
-            }
-        }
-    }
-#pragma unroll
-    for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = 16 * a + 4 * g + i, n = n0 + wrow;
-            if (m < M && n < N) {
-                const int64_t at = (int64_t)m * N + n;
-                if (part)
-                    part[(int64_t)split * M * N + at] = acc[a][i];
-                else
-                    C[at] = T::from_f32(acc[a][i]);
-            }
-        }
 }
 
 template <typename T>
@@ -581,56 +431,14 @@ __global__ __launch_bounds__(256) void w4g_join_kernel(const float *__restrict__
     C[i] = T::from_f32(v);
 }
 
-// Tiles of BM x BN outputs.
-int64_t tiles_of(int M, int N, int BM, int BN) { return (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN); }
-
-// Parts of K with a workspace: enough workgroups for the chip's 256 CUs, none
-// under four 128-wide steps.  M <= 16 is not split: joining costs a launch
-// (4 us), more than it gains (M = 16, N = K = 4096: 8.1 us whole, 10.0 in two).
-int k_split(int M, int N, int K)
-{
-    if (M <= 16)
-        return 1;
-    const int64_t tiles = M <= 32   ? tiles_of(M, N, 32, 32)
-                          : M <= 64 ? tiles_of(M, N, 64, 128)
-                                    : tiles_of(M, N, 64, 64);
-    const int64_t steps = (K + 127) / 128;
-    int64_t n = (256 + tiles / 2) / tiles;
-    n = n < steps / 4 ? n : steps / 4;
-    return n < 1 ? 1 : n > 16 ? 16 : (int)n;
-}
-
-template <typename T, int NA, int NB, int WAVES, int DEPTH>
+template <typename T, int NA, int NL, int WAVES, int CH>
 hipError_t launch_skinny_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
-                           uint16_t *C, int M, int N, int K, float *ws, int ksplit, hipStream_t s)
+                           uint16_t *C, int M, int N, int K, hipStream_t s)
 {
-    const int64_t wgs = ((int64_t)N + 16 * NB - 1) / (16 * NB) * ksplit;
-    const int64_t total = (int64_t)M * N;
-    if (!grid_fits(wgs, 64 * WAVES) || !grid_fits((total + 255) / 256, 256))
+    const int64_t wgs = ((int64_t)N + 15) / 16;
+    if (!grid_fits(wgs, 64 * WAVES))
         return kGridTooLarge;
-    w4g_skinny_kernel<T, NA, NB, WAVES, DEPTH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(
-        A, B, scale, zero, gshift, C, ksplit > 1 ? ws : nullptr, M, N, K, ksplit);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || ksplit == 1)
-        return e;
-    w4g_join_kernel<T><<<dim3((unsigned)((total + 255) / 256)), 256, 0, s>>>(ws, C, total, ksplit);
-    return hipGetLastError();
-}
-
-template <typename T, int NA, int WAVES, int DEPTH>
-hipError_t launch_panel_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
-                          uint16_t *C, int M, int N, int K, float *ws, int ksplit, hipStream_t s)
-{
-    const int64_t wgs = ((int64_t)N + 16 * WAVES - 1) / (16 * WAVES) * ksplit;
-    const int64_t total = (int64_t)M * N;
-    if (!grid_fits(wgs, 64 * WAVES) || !grid_fits((total + 255) / 256, 256))
-        return kGridTooLarge;
-    w4g_panel_kernel<T, NA, WAVES, DEPTH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(A, B, scale, zero, gshift, C,
-                                                                                     ksplit > 1 ? ws : nullptr, M, N, K, ksplit);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || ksplit == 1)
-        return e;
-    w4g_join_kernel<T><<<dim3((unsigned)((total + 255) / 256)), 256, 0, s>>>(ws, C, total, ksplit);
+    w4g_skinny_kernel<T, NA, 1, NL, WAVES, CH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
     return hipGetLastError();
 }
 
@@ -873,22 +681,46 @@ hipError_t launch_tiled_t(const uint16_t *A, const uint8_t *B, const uint16_t *s
     return hipGetLastError();
 }
 
+// Tiles of BM x BN outputs.
+int64_t tiles_of(int M, int N, int BM, int BN) { return (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN); }
+
+// Parts of K with a workspace, for M > 32: enough workgroups of 64 x 64 tiles
+// for the chip's 256 CUs, none under four 128-wide steps (M = 100, N = K =
+// 4096, 128 tiles: 27 us whole, 21 in two parts, 24 in four; M = 200, 256
+// tiles: 21, 27, 33).
+int k_split(int M, int N, int K)
+{
+    if (M <= kSkinnyM)
+        return 1;
+    const int64_t tiles = tiles_of(M, N, 64, 64), steps = (K + 127) / 128;
+    int64_t n = (256 + tiles / 2) / tiles;
+    n = n < steps / 4 ? n : steps / 4;
+    return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
+
 template <typename T>
 hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
                       uint16_t *C, int M, int N, int K, float *ws, int64_t wsBytes, hipStream_t s)
 {
+    // M = 1: a row of B a wavefront (N = K = 4096 5.1 us, the skinny kernel
+    // 5.6; N = 11008 9.4, 11.2).  Above, the skinny kernel with as many loads
+    // of A as it has rows; with few tiles of N the wavefronts share them out
+    // further and hold more in flight (M = 4, N = 4096, K = 4096: eight
+    // wavefronts, four steps 5.9 us, four wavefronts 6.6; N = 11008: 16.5,
+    // 14.1).
     if (M == 1)
         return launch_gemv_t<T, 1, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
+    if (M <= 4)
+        return N <= 16 * 512 ? launch_skinny_t<T, 1, 1, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, s)
+                             : launch_skinny_t<T, 1, 1, 4, 4>(A, B, scale, zero, gshift, C, M, N, K, s);
+    if (M <= 8)
+        return launch_skinny_t<T, 1, 2, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, s);
     if (M <= 16)
-        return launch_skinny_t<T, 1, 1, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, ws, 1, s);
+        return launch_skinny_t<T, 1, 4, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
+    if (M <= kSkinnyM)
+        return launch_skinny_t<T, 2, 8, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
     const int64_t need = gemm_w4g_workspace_bytes(M, N, K);
     const int ksplit = need && wsBytes >= need ? k_split(M, N, K) : 1;
-    if (M <= 32)
-        return launch_skinny_t<T, 2, 2, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
-    if (M <= 48)
-        return launch_panel_t<T, 3, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
-    if (M <= 64)
-        return launch_panel_t<T, 4, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
     // Larger tiles move less, but need enough of them (M = 2048, N = K = 4096:
     // 128 x 128 78 us, 128 x 64 99, 64 x 64 145; M = 512, K = 11008: 136, 98,
     // 120; M = 100: 53, 37, 28, and with K in parts less).
