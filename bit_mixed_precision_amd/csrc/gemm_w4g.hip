@@ -4,7 +4,7 @@
 // codes c in -8..7 packed as by bq_pack_int4 (u = c + 8 = nibble ^ 8), fp32
 // sums.  Three kernels by M:
 //  * gemv (M = 1): dot products, a stream over B;
-//  * skinny (M <= 32): matrix instructions on the bare codes, K split over a
+//  * skinny (M <= 16): matrix instructions on the bare codes, K split over a
 //    workgroup's wavefronts;
 //  * tiled: the weights rounded once to T between LDS and the matrix
 //    instructions, K in parts over workgroups where tiles are few.
@@ -18,8 +18,9 @@ namespace bq {
 namespace {
 
 // M up to which the skinny kernel is taken: 16 weight rows a workgroup and all
-// of A's (M = 32, N = K = 4096: 10.2 us, tiled 13.3; M = 64: 16.7, tiled 15.4).
-constexpr int kSkinnyM = 32;
+// of A's (M = 16, N = K = 4096: 7.4 us, tiled 12.6; M = 20, N = 11008: 26.4,
+// tiled 13.6).
+constexpr int kSkinnyM = 16;
 
 constexpr uint32_t kFlip = 0x88888888u;  // two's complement nibble -> c + 8
 
@@ -497,38 +498,46 @@ __device__ __forceinline__ void dma2(v4si rsrc, uint32_t lds_addr, uint32_t voff
     asm volatile("buffer_load_ushort %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds_addr) : "memory");
 }
 
-// BM x BN outputs a workgroup of four wavefronts side by side, each all BM
-// rows of A and BN/4 weight rows, so that a code is decoded once; K in steps
-// of 64 through STAGES LDS buffers that the loads fill without registers,
-// STAGES - 1 steps ahead.  Codes stay packed in LDS and become operands in
-// registers (weights8) between the matrix instructions.  A row's eight
-// 16-byte pieces are permuted by its number, so that operand reads of eight
-// rows fall into different banks.  A lane takes k = 16 g .. 16 g + 15 of a
-// step, its codes being one 8-byte read.
-template <typename T, int BM, int BN, int STAGES, bool ZERO>
-__global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
-                                                           const uint16_t *__restrict__ scale,
-                                                           const uint16_t *__restrict__ zero, int gshift,
-                                                           uint16_t *__restrict__ C, float *__restrict__ part, int M, int N,
-                                                           int K, int ksplit)
+// BM x BN outputs a workgroup, KW teams of four wavefronts.  A team's
+// wavefronts lie side by side, each with all BM rows of A and BN/4 weight rows,
+// so that a code is decoded once; the teams take turns at the 64-wide steps of
+// K, and their sums are added at the end.  A stage of KW steps goes through
+// one of three LDS buffers that loads fill without registers, two stages
+// ahead.  A row's codes and parameters of a stage are loaded together: each
+// cache line that a load touches costs the same, whether 32 bytes of it are
+// taken or 128, and with a step's codes, scales and zeros loaded by themselves
+// those lines were what bounded the kernel.  Codes stay packed in LDS and
+// become operands in registers (weights8) between the matrix instructions.
+// The 16-byte pieces of LDS rows are permuted by the row's number, so that
+// operand reads fall into different banks.  A lane takes k = 16 g .. 16 g + 15
+// of a step, its codes being one 8-byte read.
+template <typename T, int BM, int BN, int KW, bool ZERO>
+__global__ __launch_bounds__(256 * KW, 1) void w4g_tiled_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
+                                                                const uint16_t *__restrict__ scale,
+                                                                const uint16_t *__restrict__ zero, int gshift,
+                                                                uint16_t *__restrict__ C, float *__restrict__ part, int M,
+                                                                int N, int K, int ksplit)
 {
+    constexpr int STAGES = 3, kSpan = kBK * KW;
     constexpr int FM = BM / 16, FN = BN / 64;
-    constexpr int kA = BM / 32, kB = BN < 128 ? 1 : BN / 128;  // loads of a wavefront a step: A, codes (and scales, zeros)
-    constexpr int kLoads = kA + kB * (ZERO ? 3 : 2);
-    constexpr int oB = BM * 128, oS = oB + BN * 32, oZ = oS + BN * 8, kStage = oZ + (ZERO ? BN * 8 : 0);
-    constexpr int kSchedMfma = 8, kSchedValu = 2, kSchedDsRead = 0x100, kValu = (T::kBf16 || ZERO ? 30 : 20) * FN / (FM * FN) + 1;
-    static_assert(BM % 32 == 0 && (BN == 64 || BN % 128 == 0), "whole loads");
-    static_assert((STAGES - 1) * kLoads < 64, "the wait counter");
+    constexpr int kA = BM / 32;                  // loads of A a wavefront and stage
+    constexpr int nB = BN * KW / 32;             // loads of codes a stage, and of scales, and of zeros
+    constexpr bool kShare = nB < 4 * KW;         // half the wavefronts load codes, half scales
+    constexpr int kLoads = kA + (kShare ? 1 : 2) + (ZERO ? 1 : 0);
+    constexpr int kPieces = 2 * KW, kTurn = KW == 4 ? 1 : 2;  // 16-byte pieces of a row of codes; rows of 256 bytes, as a shift
+    constexpr int oB = KW * BM * 128, oS = oB + nB * 1024, oZ = oS + nB * 256, kStage = oZ + (ZERO ? nB * 256 : 0);
+    constexpr int kSchedMfma = 8, kSchedValu = 2, kSchedDsRead = 0x100, kValu = (T::kBf16 || ZERO ? 24 : 16) / FM + 1;
+    static_assert(BM % 32 == 0 && (KW == 2 || KW == 4) && (nB == 4 * KW || nB == 2 * KW), "whole loads");
     __shared__ __align__(1024) uint8_t lds[STAGES * kStage];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wid >> 2, wave = wid & 3;
     const int g = lane >> 4, l16 = lane & 15;
     const int tilesM = (M + BM - 1) / BM;
     // neighbouring workgroups share weight rows: a die's L2 then reads them once
     const int split = blockIdx.x % ksplit, tile = blockIdx.x / ksplit;
     const int m0 = tile % tilesM * BM, n0 = tile / tilesM * BN;
-    const int groups = K >> gshift, per = (K / kBK + ksplit - 1) / ksplit;
-    const int first = split * per, steps = min(first + per, K / kBK);
+    const int groups = K >> gshift, spans = (K + kSpan - 1) / kSpan, per = (spans + ksplit - 1) / ksplit;
+    const int first = split * per, last = min(first + per, spans);
     const int mrows = min(BM, M - m0), nrows = min(BN, N - n0);
     const v4si ra = make_rsrc(A + (int64_t)m0 * K, (uint32_t)mrows * K * 2);
     const v4si rb = make_rsrc(B + (int64_t)n0 * (K / 2), (uint32_t)nrows * (K / 2));
@@ -538,23 +547,27 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
 
     const auto load = [&](int st, int slot) {
         const uint32_t to = base + slot * kStage;
-        const bool in = st < steps;  // past the end: zeros, no access
+        const bool in = st < last;  // past the end: zeros, no access
+        const int k0 = st * kSpan;
 #pragma unroll
         for (int i = 0; i < kA; ++i) {
-            const int row = (wave * kA + i) * 8 + (lane >> 3), piece = (lane & 7) ^ swizzle(row & 15);
-            dma16(ra, to + (wave * kA + i) * 1024, in ? (uint32_t)(2 * (row * K + st * kBK) + 16 * piece) : kOOB, 0);
+            const int at = wave * kA + i, row = at * 8 + (lane >> 3), piece = (lane & 7) ^ swizzle(row & 15);
+            const int k = k0 + team * kBK + 8 * piece;
+            dma16(ra, to + (team * BM * 128 + at * 1024), in && k < K ? (uint32_t)(2 * (row * K + k)) : kOOB, 0);
         }
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            const int at = BN < 128 ? wave & 1 : wave * kB + i;
-            const int row = at * 32 + (lane >> 1);
-            dma16(rb, to + oB + at * 1024, in ? (uint32_t)(row * (K / 2) + st * (kBK / 2) + 16 * (lane & 1)) : kOOB, 0);
-            // a row's groups at k = 0 and 32 of the step
-            const uint32_t par = in ? 2u * (row * groups + ((st * kBK + 32 * (lane & 1)) >> gshift)) : kOOB;
-            dma2(rs, to + oS + at * 256, par);
-            if constexpr (ZERO)
-                dma2(rz, to + oZ + at * 256, par);
+        const int at = wid % nB;
+        if (!kShare || wid < nB) {
+            const int row = at * (64 / kPieces) + lane / kPieces, piece = (lane % kPieces) ^ (row >> kTurn & (kPieces - 1));
+            const int k = k0 + 32 * piece;
+            dma16(rb, to + (oB + at * 1024), in && k < K ? (uint32_t)(row * (K / 2) + k / 2) : kOOB, 0);
         }
+        // a row's groups at every 32nd k of the stage
+        const int row = at * (64 / kPieces) + lane / kPieces, k = k0 + 32 * (lane % kPieces);
+        const uint32_t par = in && k < K ? 2u * (row * groups + (k >> gshift)) : kOOB;
+        if (!kShare || wid >= nB)
+            dma2(rs, to + (oS + at * 256), par);
+        if constexpr (ZERO)
+            dma2(rz, to + (oZ + at * 256), par);
     };
 
     f4 acc[FM][FN];
@@ -563,17 +576,16 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = (f4){0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        load(first + s, s);
+    load(first, 0);
+    load(first + 1, 1);
     const int wn = wave * (16 * FN);
     NibbleBits nibbles;
     nibbles.hold();
     const auto step = [&](int st, int slot) {
-        // this wavefront's loads of the step are there, then everyone's; and
+        // this wavefront's loads of the stage are there, then everyone's; and
         // everyone is done with the buffer that is filled next
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
-        load(st + STAGES - 1, (slot + STAGES - 1) % STAGES);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+        load(st + 2, (slot + 2) % STAGES);
         const uint8_t *buf = lds + slot * kStage;
         uint2 w[FN];
         uint32_t s16[FN], z16[FN];
@@ -581,14 +593,15 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int row = wn + 16 * j + l16;
-            w[j] = *(const uint2 *)(buf + oB + row * 32 + g * 8);
-            s16[j] = *(const uint32_t *)(buf + oS + row * 8 + (g >> 1) * 4);
-            z16[j] = ZERO ? *(const uint32_t *)(buf + oZ + row * 8 + (g >> 1) * 4) : 0u;
+            const int piece = 2 * team + (g >> 1);
+            w[j] = *(const uint2 *)(buf + oB + row * (16 * kPieces) + 16 * (piece ^ (row >> kTurn & (kPieces - 1))) + 8 * (g & 1));
+            s16[j] = *(const uint32_t *)(buf + oS + (row * kPieces + piece) * 4);
+            z16[j] = ZERO ? *(const uint32_t *)(buf + oZ + (row * kPieces + piece) * 4) : 0u;
         }
         const auto read_a = [&](int h) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                fa[h][i] = *(const u4 *)(buf + (16 * i + l16) * 128 + 16 * ((2 * g + h) ^ swizzle(l16)));
+                fa[h][i] = *(const u4 *)(buf + team * BM * 128 + (16 * i + l16) * 128 + 16 * ((2 * g + h) ^ swizzle(l16)));
         };
         const auto decode = [&](int h) {
 #pragma unroll
@@ -620,14 +633,35 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
         __builtin_amdgcn_sched_barrier(0);
         products(1);
     };
-    for (int st = first; st < steps; st += STAGES) {
+    for (int st = first; st < last; st += STAGES) {
 #pragma unroll
         for (int s = 0; s < STAGES; ++s)
-            if (st + s < steps)
+            if (st + s < last)
                 step(st + s, s);
     }
     // no load may still be on its way to LDS when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    // the teams' sums, in order
+    static_assert(STAGES * kStage >= (KW - 1) * BM * BN * 4, "room for the sums");
+    f4 *const sums = (f4 *)lds;
+    if (team) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                sums[(((team - 1) * FM + i) * FN + j) * 256 + (threadIdx.x & 255)] = acc[i][j];
+    }
+    __syncthreads();
+    if (team)
+        return;
+#pragma unroll
+    for (int k = 0; k < KW - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] += sums[((k * FM + i) * FN + j) * 256 + threadIdx.x];
     // a lane holds four neighbouring columns of one row
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -660,20 +694,20 @@ __global__ __launch_bounds__(256, 1) void w4g_tiled_kernel(const uint16_t *__res
     }
 }
 
-template <typename T, int BM, int BN, int STAGES>
+template <typename T, int BM, int BN, int KW>
 hipError_t launch_tiled_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
                           uint16_t *C, int M, int N, int K, float *ws, int ksplit, hipStream_t s)
 {
     const int64_t wgs = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN) * ksplit;
     const int64_t total = (int64_t)M * N;
-    if (!grid_fits(wgs, 256) || (ksplit > 1 && !grid_fits((total + 255) / 256, 256)))
+    if (!grid_fits(wgs, 256 * KW) || (ksplit > 1 && !grid_fits((total + 255) / 256, 256)))
         return kGridTooLarge;
     const dim3 grid((unsigned)wgs);
     float *part = ksplit > 1 ? ws : nullptr;
     if (zero)
-        w4g_tiled_kernel<T, BM, BN, STAGES, true><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, part, M, N, K, ksplit);
+        w4g_tiled_kernel<T, BM, BN, KW, true><<<grid, 256 * KW, 0, s>>>(A, B, scale, zero, gshift, C, part, M, N, K, ksplit);
     else
-        w4g_tiled_kernel<T, BM, BN, STAGES, false><<<grid, 256, 0, s>>>(A, B, scale, zero, gshift, C, part, M, N, K, ksplit);
+        w4g_tiled_kernel<T, BM, BN, KW, false><<<grid, 256 * KW, 0, s>>>(A, B, scale, zero, gshift, C, part, M, N, K, ksplit);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || ksplit == 1)
         return e;
@@ -684,15 +718,14 @@ hipError_t launch_tiled_t(const uint16_t *A, const uint8_t *B, const uint16_t *s
 // Tiles of BM x BN outputs.
 int64_t tiles_of(int M, int N, int BM, int BN) { return (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN); }
 
-// Parts of K with a workspace, for M > 32: enough workgroups of 64 x 64 tiles
-// for the chip's 256 CUs, none under four 128-wide steps (M = 100, N = K =
-// 4096, 128 tiles: 27 us whole, 21 in two parts, 24 in four; M = 200, 256
-// tiles: 21, 27, 33).
+// Parts of K with a workspace: enough workgroups of the smaller tiles for the
+// chip's 256 CUs, none under four 128-wide steps (M = 100, N = K = 4096, 128
+// tiles: two parts 18.9 us, four 21; M = 200, 256 tiles: 21.9, two parts 27).
 int k_split(int M, int N, int K)
 {
     if (M <= kSkinnyM)
         return 1;
-    const int64_t tiles = tiles_of(M, N, 64, 64), steps = (K + 127) / 128;
+    const int64_t tiles = tiles_of(M, N, M <= 32 ? 32 : 64, 64), steps = (K + 127) / 128;
     int64_t n = (256 + tiles / 2) / tiles;
     n = n < steps / 4 ? n : steps / 4;
     return n < 1 ? 1 : n > 16 ? 16 : (int)n;
@@ -717,18 +750,18 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
         return launch_skinny_t<T, 1, 2, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, s);
     if (M <= 16)
         return launch_skinny_t<T, 1, 4, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
-    if (M <= kSkinnyM)
-        return launch_skinny_t<T, 2, 8, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
+    // Larger tiles move less, but there have to be enough of them (M = 2048, N =
+    // K = 4096: 128 x 128 80 us, 128 x 64 106; M = 256, N = 11008, 172 tiles of
+    // 128 x 128: 46, 59, 64 x 64 58; M = 512, N = 4096, K = 11008, 128 tiles: 113,
+    // 78, 100; M = 200, N = K = 4096: 64 x 64 21.9, 128 x 64 in two parts 25.9).
+    if (tiles_of(M, N, 128, 128) >= 160)
+        return launch_tiled_t<T, 128, 128, 2>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
+    if (tiles_of(M, N, 128, 64) >= 256)
+        return launch_tiled_t<T, 128, 64, 2>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
     const int64_t need = gemm_w4g_workspace_bytes(M, N, K);
     const int ksplit = need && wsBytes >= need ? k_split(M, N, K) : 1;
-    // Larger tiles move less, but need enough of them (M = 2048, N = K = 4096:
-    // 128 x 128 78 us, 128 x 64 99, 64 x 64 145; M = 512, K = 11008: 136, 98,
-    // 120; M = 100: 53, 37, 28, and with K in parts less).
-    if (tiles_of(M, N, 128, 128) >= 256)
-        return launch_tiled_t<T, 128, 128, 3>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
-    if (tiles_of(M, N, 128, 64) >= 256)
-        return launch_tiled_t<T, 128, 64, 4>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
-    return launch_tiled_t<T, 64, 64, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
+    return M <= 32 ? launch_tiled_t<T, 32, 64, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s)
+                   : launch_tiled_t<T, 64, 64, 4>(A, B, scale, zero, gshift, C, M, N, K, ws, ksplit, s);
 }
 
 }  // namespace

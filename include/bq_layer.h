@@ -63,7 +63,7 @@ enum bq_dtype {
  *              bq_gemm_w4g_workspace_bytes, for none (K is not split, the sums
  *              are taken in another order).  Calls that share one must not
  *              overlap.
- * M > 32 rounds each weight once to dtype; smaller M uses the exact weights.
+ * M > 16 rounds each weight once to dtype; smaller M uses the exact weights.
  * 0 <= M, N <= BQ_MAX_DIM, M * N <= BQ_MAX_OUT, 0 <= K <= BQ_MAX_K, K a
  * multiple of 64 and of group (BQ_ERR_SHAPE); pointers 16-byte aligned.
  * K == 0 writes zeros.

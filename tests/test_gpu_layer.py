@@ -3,11 +3,11 @@ oracle/layer.py.
 
 Bounds (u = 2^-24; e = half a step of the output type, 2^-11 fp16, 2^-8 bf16):
 
-* w4g, M <= 32: |C - S| <= e |S| + T, T = 2^-13 sum_k |a| s (twice the
+* w4g, M <= 16: |C - S| <= e |S| + T, T = 2^-13 sum_k |a| s (twice the
   truncation of a matrix step: products with the subnormal codes are aligned
   24 bits below the largest exponent, 2^-13 of a code unit times |a|)
   + (K + 64) u sum_k |a| s (151 + |z|) (fp32 sums of a (c + 136) and of
-  (136 + z) sum a).  M > 32 rounds each weight: + e sum_k |a W|.
+  (136 + z) sum a).  M > 16 rounds each weight: + e sum_k |a W|.
 * norm and rotation: fp32, at most 40 roundings per term (D = 256: 8 + 5 for
   the sum of squares, the root, the products): e |y| + 40 u size, size the sum
   of the magnitudes of y's terms.
@@ -82,7 +82,7 @@ def check_w4g(bq, dev, M, N, K, group, zero, T, seed=0, workspace=None, A=None):
     zz = z.to(F64).abs().repeat_interleave(group, 1) if zero else 0.0
     a = A.to(F64).abs()
     tol = half_step(T) * S.abs() + 2.0 ** -13 * (a @ big.t()) + (K + 64) * U * (a @ (big * (151 + zz)).t()) + 2.0 ** -25
-    if M > 32:
+    if M > 16:
         tol = tol + half_step(T) * (a @ W.abs().t()) * (1 + 2.0 ** -8)
     within(out, S, tol, f"w4g {M}x{N}x{K} g{group} {T}")
     return out, S
@@ -108,7 +108,7 @@ def test_w4g(bq, dev, shape, T, zero):
 @pytest.mark.parametrize("T", TYPES)
 def test_w4g_weights_one_by_one(bq, dev, M, T):
     """One-hot rows pick single weights: C[m, n] = T(W[n, k]) to the bound of
-    one product (M > 32: exactly, the weight's own rounding)."""
+    one product (M > 16: exactly, the weight's own rounding)."""
     banner(f"w4g one-hot M={M} {T}")
     N, K, group = 96, 256, 32
     A = torch.zeros(M, K)
@@ -569,6 +569,7 @@ def test_layer_step_together(bq, dev, T):
         S = A @ W.t()
         big = o[s].cpu().to(F64).repeat_interleave(64, 1)
         tol = half_step(T) * S.abs() + 2.0 ** -13 * (A.abs() @ big.t()) + (A.shape[1] + 64) * U * (A.abs() @ (big * 151).t())
+        tol = tol + half_step(T) * (A.abs() @ W.abs().t()) * (1 + 2.0 ** -8)  # 20 rows: each weight rounded once
         within(c, S, tol, "layer: product")
 
 
