@@ -344,6 +344,10 @@ ATTN = [
     ([10, 70], 33, 2, 1, 128, 16, 20),
     ([5], 9, 3, 1, 64, 16, 0),
     ([150], 64, 8, 8, 256, 16, 48),
+    ([1100, 37, 1025], 1, 4, 1, 128, 64, 0),
+    ([1500], 1, 3, 1, 64, 32, 0),
+    ([1200, 260], 5, 8, 2, 128, 16, 700),
+    ([1300], 1, 2, 1, 256, 16, 0),
 ]
 
 
@@ -411,10 +415,10 @@ def test_attn_kv4_bad_pages_and_lengths(bq, dev, T):
 def test_attn_kv4_ranges(bq, dev, T, k_off, v_mul, q_mul):
     """Small and large values, keys with a large common offset, peaked softmax."""
     banner(f"attn ranges {k_off} {v_mul} {q_mul} {T}")
-    lens, hq, hkv, d, page = [333, 64], 8, 2, 128, 16
+    lens, hq, hkv, d, page = [333, 1064], 8, 2, 128, 16
     g = gen(9)
-    cache = make_cache(g, 26, hkv, d, page, T, k_off, v_mul)
-    tab = tables(g, lens, page, 26)
+    cache = make_cache(g, 90, hkv, d, page, T, k_off, v_mul)
+    tab = tables(g, lens, page, 90)
     q = (torch.randn(2, hq, d, generator=g) * q_mul).to(T)
     got = run_attn(bq, dev, q, cache, tab, lens, hkv, page)
     check_attn(got, q, cache, tab, lens, [0, 1, 2], what="ranges")
@@ -423,12 +427,12 @@ def test_attn_kv4_ranges(bq, dev, T, k_off, v_mul, q_mul):
 def test_attn_kv4_growing_scales(bq, dev):
     """V scales that grow along the sequence, by 2^16 over it."""
     banner("attn growing V scales")
-    T, lens, hq, hkv, d, page = torch.float16, [500], 4, 1, 128, 16
+    T, lens, hq, hkv, d, page = torch.float16, [1090], 4, 1, 128, 16
     g = gen(10)
-    cache = layer.Cache(32, hkv, d, page)
-    for s in range(512):
-        cache.write(s, torch.randn(hkv, d, generator=g).to(T), (torch.randn(hkv, d, generator=g) * 2.0 ** (s / 32 - 6)).to(T))
-    tab = torch.arange(32, dtype=torch.int32)[None]
+    cache = layer.Cache(72, hkv, d, page)
+    for s in range(1152):
+        cache.write(s, torch.randn(hkv, d, generator=g).to(T), (torch.randn(hkv, d, generator=g) * 2.0 ** (s / 72 - 6)).to(T))
+    tab = torch.arange(72, dtype=torch.int32)[None]
     q = torch.randn(1, hq, d, generator=g).to(T)
     for ws in ("none", "full"):
         check_attn(run_attn(bq, dev, q, cache, tab, lens, hkv, page, ws=ws), q, cache, tab, lens, [0, 1], what="growing")
@@ -512,7 +516,7 @@ def _layer_step(bq, o):
 def _layer_state(bq, dev, T, B=20):
     g = gen(77)
     hq, hkv, d, page, hidden = 8, 2, 128, 16, 512
-    lens = [5 + 37 * i for i in range(B)]
+    lens = [5 + 61 * i for i in range(B)]
     pages = sum(-(-n // page) for n in lens)
     tab = tables(g, lens, page, pages)
     o = dict(hq=hq, hkv=hkv, d=d, page=page)
@@ -522,7 +526,7 @@ def _layer_state(bq, dev, T, B=20):
     for name, shape in (("qkv", (n, hidden)), ("o", (hidden, hq * d))):
         B4, s, _ = layer.quantize_w4g(torch.randn(*shape, generator=g) * 0.04, 64, False)
         o["w" + name], o["s" + name] = dv(B4), dv(s)
-    o["cos"], o["sin"] = (dv(t) for t in table(1024, d))
+    o["cos"], o["sin"] = (dv(t) for t in table(2048, d))
     o["pos"] = dv(torch.tensor(lens, dtype=torch.int32) - 1)
     o["lens"], o["table"] = dv(torch.tensor(lens, dtype=torch.int32)), dv(tab)
     o["slots"] = dv(torch.tensor([int(tab[b, (x - 1) // page]) * page + (x - 1) % page for b, x in enumerate(lens)]))

@@ -140,6 +140,7 @@ def test_attn_kv4_workspace(bq):
     f = bq.attn_kv4_workspace_bytes
     assert f(0, 1, 8, 2, 128, 1000) == 0
     assert f(1, 1, 8, 2, 128, 16) == 0            # too short to split
+    assert f(1, 1, 8, 2, 128, 1024) == 0
     assert f(1, 1, 8, 2, 128, 100000) > 0
     assert f(1, 1, 8, 2, 128, 100000) % (2 * 16 * 130 * 4) == 0
     for bad in ((-1, 1, 8, 2, 128, 10), (1, 1, 7, 2, 128, 10), (1, 1, 8, 2, 100, 10), (1, 1, 8, 2, 128, 2**31),
