@@ -271,7 +271,7 @@ struct Wave {
     }
 
     // Scores of a tile, over a1.
-    __device__ __forceinline__ void scores(const Tile<D> &x, float (&s)[RT][8])
+    __device__ __forceinline__ void scores(const Tile<D> &x, float (&s)[RT][8], float nothing)
     {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -295,7 +295,7 @@ struct Wave {
                 const float sk = half_bits(x.par[h][i] & 0xffffu), mk = half_bits(x.par[h][i] >> 16);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    s[r][4 * h + i] = (s0[r][i] * 16.0f + s4[r][i]) * sk + mk * b1[r];
+                    s[r][4 * h + i] = __builtin_fmaf(s0[r][i] * 16.0f + s4[r][i], sk, __builtin_fmaf(mk, b1[r], nothing));
             }
         }
     }
@@ -486,6 +486,10 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
         // when the products have; page numbers come a tile earlier.
         uint32_t bias = 0x64006400u;
         asm volatile("" : "+v"(bias));
+        // -0 that the compiler does not know: a product with a 16-bit factor then
+        // is one mixed multiply-add instead of a conversion and a multiply
+        float nothing = -0.0f;
+        asm volatile("" : "+v"(nothing));
         Tile<D> k, v;
         int pages[2];
         load_pages(pages, p, table, t, end);
@@ -497,7 +501,7 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
             const int u = t + kStep;
             const int lim[2] = {at.lim[0], at.lim[1]};
             float s[RT][8];
-            w.scores(k, s);
+            w.scores(k, s, nothing);
             if (u < end) {
                 at = place_of<D>(p, pages, head, u, end);
                 load_k<D>(k, at, p.page_shift, lane);
