@@ -66,113 +66,88 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t p[4])
     }
 }
 
-// A wavefront takes ROWS rows of B and walks them 2048 codes a pass, lane l
-// the 32 codes (16 bytes, inside one group) from 32 l on, so a row is read in
-// whole kilobytes.  The workgroup puts the pass of A into LDS once, already in
-// the codes' pair order and with the sum of every 32 values; piece h of every
-// lane's 32 lies in its own plane, so that reads of 16 bytes a lane are
-// contiguous (planes padded by 64 bytes for the writes).  B is in flight two
-// passes ahead.
+// One row of A.  A wavefront takes a row of B and walks it 2048 codes a pass,
+// lane l the 32 codes (16 bytes, inside one group) from 32 l on, so a row is
+// read in whole kilobytes.  The workgroup puts the pass of A into LDS once,
+// already in the codes' pair order and with the sum of every 32 values; piece
+// h of every lane's 32 lies in its own plane, so that reads of 16 bytes a lane
+// are contiguous (planes padded by 64 bytes for the writes).  B is in flight
+// two passes ahead.
 constexpr int kPass = 2048, kPlane = 64 * 16 + 64;
 
-template <int ROWS>
 struct GemvLoad {
-    u4 b[ROWS];
-    uint16_t s[ROWS], z[ROWS];
+    u4 b;
+    uint16_t s, z;
 };
 
-template <typename T, int MR, int ROWS>
+template <typename T>
 __global__ __launch_bounds__(64 * kGemvWaves) void w4g_gemv_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
                                                                    const uint16_t *__restrict__ scale,
                                                                    const uint16_t *__restrict__ zero, int gshift,
-                                                                   uint16_t *__restrict__ C, int M, int N, int K)
+                                                                   uint16_t *__restrict__ C, int N, int K)
 {
-    static_assert(64 * kGemvWaves * 8 == kPass, "a 16-byte piece of a row's pass per thread");
-    __shared__ __align__(16) uint8_t sa[2][MR][4 * kPlane];
-    __shared__ float ssum[2][MR][64];
+    static_assert(64 * kGemvWaves * 8 == kPass, "a 16-byte piece of the pass per thread");
+    __shared__ __align__(16) uint8_t sa[2][4 * kPlane];
+    __shared__ float ssum[2][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = (blockIdx.x * kGemvWaves + wave) * ROWS;
+    const int64_t n = (int64_t)blockIdx.x * kGemvWaves + wave;
     const int groups = K >> gshift;
-    const int64_t nb = min(n0, N - 1);  // a wavefront past the end loads nothing and only helps with A
-    const int rows = max(min(ROWS, N - n0), 0);
-    const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + nb * (K / 2), (int64_t)rows * (K / 2));
-    const Buf bs = buffer(scale + nb * groups, (int64_t)rows * groups * 2);
-    const Buf bz = buffer((zero ? zero : scale) + nb * groups, zero ? (int64_t)rows * groups * 2 : 0);
+    const bool in = n < N;  // a wavefront past the end loads nothing and only helps with A
+    const int64_t nb = in ? n : 0;
+    const Buf ba = buffer(A, (int64_t)K * 2), bb = buffer(B + nb * (K / 2), in ? K / 2 : 0);
+    const Buf bs = buffer(scale + nb * groups, in ? (int64_t)groups * 2 : 0);
+    const Buf bz = buffer((zero ? zero : scale) + nb * groups, in && zero ? (int64_t)groups * 2 : 0);
 
-    const auto load_b = [&](GemvLoad<ROWS> &x, int pass) {
+    const auto load_b = [&](GemvLoad &x, int pass) {
         const int k = pass * kPass + 32 * lane;
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            x.b[r] = load16(bb, k < K ? r * (K / 2) + k / 2 : kOut);
-            const uint32_t at = k < K ? 2 * (r * groups + (k >> gshift)) : kOut;
-            x.s[r] = load2(bs, at);
-            x.z[r] = load2(bz, at);
-        }
+        x.b = load16(bb, k < K ? k / 2 : kOut);
+        const uint32_t at = k < K ? 2 * (k >> gshift) : kOut;
+        x.s = load2(bs, at);
+        x.z = load2(bz, at);
     };
-    const auto load_a = [&](u4 *x, int pass) {
+    const auto load_a = [&](int pass) {
         const int k = pass * kPass + 8 * (int)threadIdx.x;
-#pragma unroll
-        for (int m = 0; m < MR; ++m)
-            x[m] = load16(ba, k < K ? 2 * (m * K + k) : kOut);
+        return load16(ba, k < K ? 2 * k : kOut);
     };
-    const auto put_a = [&](const u4 *x, int buf) {
-#pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            const u4 v = {pack_lo(x[m].x, x[m].z), pack_hi(x[m].x, x[m].z), pack_lo(x[m].y, x[m].w), pack_hi(x[m].y, x[m].w)};
-            *(u4 *)&sa[buf][m][(threadIdx.x & 3) * kPlane + (threadIdx.x >> 2) * 16] = v;
-            float s = T::dot2(v.x, T::kOnes, T::dot2(v.y, T::kOnes, T::dot2(v.z, T::kOnes, T::dot2(v.w, T::kOnes, 0.0f))));
-            s += __shfl_xor(s, 1, 64);
-            s += __shfl_xor(s, 2, 64);
-            if ((threadIdx.x & 3) == 0)
-                ssum[buf][m][threadIdx.x >> 2] = s;
-        }
+    const auto put_a = [&](const u4 x, int buf) {
+        const u4 v = {pack_lo(x.x, x.z), pack_hi(x.x, x.z), pack_lo(x.y, x.w), pack_hi(x.y, x.w)};
+        *(u4 *)&sa[buf][(threadIdx.x & 3) * kPlane + (threadIdx.x >> 2) * 16] = v;
+        float s = T::dot2(v.x, T::kOnes, T::dot2(v.y, T::kOnes, T::dot2(v.z, T::kOnes, T::dot2(v.w, T::kOnes, 0.0f))));
+        s += __shfl_xor(s, 1, 64);
+        s += __shfl_xor(s, 2, 64);
+        if ((threadIdx.x & 3) == 0)
+            ssum[buf][threadIdx.x >> 2] = s;
     };
 
-    float acc[MR][ROWS] = {};
-    const auto compute = [&](const GemvLoad<ROWS> &x, int buf) {
-        float s0[MR][ROWS] = {}, s4[MR][ROWS] = {};
+    float acc = 0.0f;
+    const auto compute = [&](const GemvLoad &x, int buf) {
+        float s0 = 0.0f, s4 = 0.0f;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            uint32_t p[ROWS][4];
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                codes8<T>(x.b[r][h] ^ kFlip, p[r]);
-#pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                const u4 q = *(const u4 *)&sa[buf][m][h * kPlane + lane * 16];
-#pragma unroll
-                for (int r = 0; r < ROWS; ++r) {
-                    s0[m][r] = T::dot2(q[0], p[r][0], s0[m][r]);
-                    s4[m][r] = T::dot2(q[1], p[r][1], s4[m][r]);
-                    s0[m][r] = T::dot2(q[2], p[r][2], s0[m][r]);
-                    s4[m][r] = T::dot2(q[3], p[r][3], s4[m][r]);
-                }
-            }
+            uint32_t p[4];
+            codes8<T>(x.b[h] ^ kFlip, p);
+            const u4 q = *(const u4 *)&sa[buf][h * kPlane + lane * 16];
+            s0 = T::dot2(q[0], p[0], s0);
+            s4 = T::dot2(q[1], p[1], s4);
+            s0 = T::dot2(q[2], p[2], s0);
+            s4 = T::dot2(q[3], p[3], s4);
         }
-#pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            const float sum = ssum[buf][m][lane];
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                const float s = half_bits(x.s[r]), z = half_bits(x.z[r]);
-                const float dot = T::kBf16 ? s0[m][r] + s4[m][r] : s0[m][r] * 0x1p24f + s4[m][r] * 0x1p20f;
-                acc[m][r] += s * (dot - ((T::kBf16 ? 136.0f : 8.0f) + z) * sum);
-            }
-        }
+        const float s = half_bits(x.s), z = half_bits(x.z);
+        const float dot = T::kBf16 ? s0 + s4 : s0 * 0x1p24f + s4 * 0x1p20f;
+        acc += s * (dot - ((T::kBf16 ? 136.0f : 8.0f) + z) * ssum[buf][lane]);
     };
 
     const int passes = (K + kPass - 1) / kPass;
     if (passes > 0) {
-        GemvLoad<ROWS> x, y;
-        u4 av[MR];
+        GemvLoad x, y;
         load_b(x, 0);
-        load_a(av, 0);
+        u4 av = load_a(0);
         load_b(y, 1);  // past the end: zeros, no access
         put_a(av, 0);
         __syncthreads();
         for (int p = 0; p < passes; ++p) {
-            load_a(av, p + 1);
+            av = load_a(p + 1);
             compute(x, p & 1);
             x = y;
             load_b(y, p + 2);
@@ -181,25 +156,20 @@ __global__ __launch_bounds__(64 * kGemvWaves) void w4g_gemv_kernel(const uint16_
         }
     }
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1)
-                acc[m][r] += __shfl_xor(acc[m][r], off, 64);
-            if (lane == m * ROWS + r && m < M && n0 + r < N)
-                C[(int64_t)m * N + n0 + r] = T::from_f32(acc[m][r]);
-        }
+    for (int off = 32; off > 0; off >>= 1)
+        acc += __shfl_xor(acc, off, 64);
+    if (lane == 0 && in)
+        C[n] = T::from_f32(acc);
 }
 
-template <typename T, int MR, int ROWS>
+template <typename T>
 hipError_t launch_gemv_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
-                         uint16_t *C, int M, int N, int K, hipStream_t s)
+                         uint16_t *C, int N, int K, hipStream_t s)
 {
-    const int64_t wgs = ((int64_t)N + ROWS * kGemvWaves - 1) / (ROWS * kGemvWaves);
+    const int64_t wgs = ((int64_t)N + kGemvWaves - 1) / kGemvWaves;
     if (!grid_fits(wgs, 64 * kGemvWaves))
         return kGridTooLarge;
-    w4g_gemv_kernel<T, MR, ROWS><<<dim3((unsigned)wgs), 64 * kGemvWaves, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
+    w4g_gemv_kernel<T><<<dim3((unsigned)wgs), 64 * kGemvWaves, 0, s>>>(A, B, scale, zero, gshift, C, N, K);
     return hipGetLastError();
 }
 
@@ -237,10 +207,10 @@ __device__ __forceinline__ void transpose4(uint32_t w[4])
 }
 
 // What a wavefront loads for CH steps of 128.
-template <int NB, int NL, int CH>
+template <int NL, int CH>
 struct Steps {
-    u4 w[CH][NB], a[CH][NL];
-    uint16_t s[CH][NB], z[CH][NB];  // four groups each, one a quarter of the lanes
+    u4 w[CH], a[CH][NL];
+    uint16_t s[CH], z[CH];  // four groups each, one a quarter of the lanes
 };
 
 __device__ __forceinline__ void wave_sync()
@@ -250,9 +220,9 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// NB tiles of 16 weight rows x up to 4 NL activation rows a workgroup, whose
-// wavefronts take neighbouring parts of its K in steps of 128, CH steps'
-// loads at a time and the next CH in flight.
+// 16 weight rows x up to 4 NL activation rows a workgroup, whose wavefronts
+// take neighbouring parts of its K in steps of 128, CH steps' loads at a time
+// and the next CH in flight.
 //  * A 16-byte load hands lane (n, g) the 32 codes of row n at k = 32 g; the
 //    transpose makes matrix step j cover k = 32 j .. 32 j + 31, which lies in
 //    one group.
@@ -264,64 +234,53 @@ __device__ __forceinline__ void wave_sync()
 //    rows of an operand read fall into different banks.
 //  * Scales and zero points come four groups of a row a load and are handed to
 //    the lanes of their row when the group ends.
-template <typename T, int NA, int NB, int NL, int WAVES, int CH>
+template <typename T, int NL, int WAVES, int CH>
 __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *__restrict__ A, const uint8_t *__restrict__ B,
                                                                 const uint16_t *__restrict__ scale,
                                                                 const uint16_t *__restrict__ zero, int gshift,
                                                                 uint16_t *__restrict__ C, int M, int N, int K)
 {
-    constexpr int kRows = 16 * NB, kLoaded = 4 * NL;
-    static_assert(kLoaded <= 16 * NA && (NA == 1 || kLoaded == 16 * NA), "rows of A");
-    __shared__ union {
+    constexpr int kLoaded = 4 * NL;
+    static_assert(kLoaded <= 16, "rows of A");
+    __shared__ __align__(16) union {
         uint8_t a[WAVES][kLoaded][256];
-        float red[WAVES][16][kRows + 4];
+        float red[WAVES][16][20];
     } sh;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int n0 = blockIdx.x * kRows;
+    const int n0 = blockIdx.x * 16;
     const int steps = (K + 127) / 128, per = (steps + WAVES - 1) / WAVES;
     const int first = wave * per, last = min(first + per, steps);
     const int groups = K >> gshift;
     const int sshift = 7 - gshift;  // groups of a step, as a shift
 
-    f4 acc[NA][NB], part_acc[NA][NB], sum[NA];
     const f4 zero4 = {0, 0, 0, 0};
-#pragma unroll
-    for (int a = 0; a < NA; ++a) {
-        sum[a] = zero4;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            acc[a][b] = part_acc[a][b] = zero4;
-    }
+    f4 acc = zero4, part_acc = zero4, sum = zero4;
     const u4 ones = {T::kOnes, T::kOnes, T::kOnes, T::kOnes};
     const int gmask = (1 << (gshift - 5)) - 1;  // 32-wide steps in a group, less one
     // B and its parameters from the workgroup's first row on, A whole
-    const int rows = min(kRows, N - n0);
+    const int rows = min(16, N - n0);
     const Buf ba = buffer(A, (int64_t)M * K * 2), bb = buffer(B + (int64_t)n0 * (K / 2), (int64_t)rows * (K / 2));
     const Buf bs = buffer(scale + (int64_t)n0 * groups, (int64_t)rows * groups * 2);
     const Buf bz = buffer((zero ? zero : scale) + (int64_t)n0 * groups, zero ? (int64_t)rows * groups * 2 : 0);
-    const auto load = [&](Steps<NB, NL, CH> &x, int c0) {
+    const auto load = [&](Steps<NL, CH> &x, int c0) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int st = c0 + c, k = st * 128 + 32 * g, ka = st * 128 + 8 * l16;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint32_t n = 16 * b + l16;
-                x.w[c][b] = load16(bb, st < last && k < K ? n * (K / 2) + k / 2 : kOut);
-                // quarter g: group 4 c + g of the CH steps
-                const int gi = (c0 << sshift) + 4 * c + g;
-                const uint32_t at = c < (CH << sshift) / 4 + (CH < 4) && gi < groups ? 2 * (n * groups + gi) : kOut;
-                x.s[c][b] = load2(bs, at);
-                x.z[c][b] = load2(bz, at);
-            }
+            x.w[c] = load16(bb, st < last && k < K ? l16 * (K / 2) + k / 2 : kOut);
+            // quarter g: group 4 c + g of the CH steps
+            const int gi = (c0 << sshift) + 4 * c + g;
+            const uint32_t at = c < (CH << sshift) / 4 + (CH < 4) && gi < groups ? 2 * (l16 * groups + gi) : kOut;
+            x.s[c] = load2(bs, at);
+            x.z[c] = load2(bz, at);
 #pragma unroll
             for (int i = 0; i < NL; ++i)
                 x.a[c][i] = load16(ba, st < last && ka < K ? 2 * ((4 * i + g) * K + ka) : kOut);
         }
     };
     uint8_t(*const sa)[256] = sh.a[wave];
-    const auto step = [&](const Steps<NB, NL, CH> &x, int c) {
+    const auto step = [&](const Steps<NL, CH> &x, int c) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const int row = 4 * i + g;
@@ -330,60 +289,34 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
                 (u4){pack_lo(v.x, v.z), pack_hi(v.x, v.z), pack_lo(v.y, v.w), pack_hi(v.y, v.w)};
         }
         wave_sync();
-        uint32_t w[NB][4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[b][j] = x.w[c][b][j];
-            transpose4(w[b]);
-        }
+        uint32_t w[4] = {x.w[c].x, x.w[c].y, x.w[c].z, x.w[c].w};
+        transpose4(w);
+        const int row = l16 % kLoaded;  // rows past the loaded ones give outputs that are not written
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            u4 q[NA];
-#pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                // rows past the loaded ones give outputs that are not written
-                const int row = (16 * a + l16) % kLoaded;
-                q[a] = *(const u4 *)&sa[row][16 * ((4 * j + g) ^ (row & 15))];
-                sum[a] = T::mma(q[a], ones, sum[a]);
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const u4 op = codes_op<T>(w[b][j] ^ kFlip);
-#pragma unroll
-                for (int a = 0; a < NA; ++a)
-                    part_acc[a][b] = T::mma(q[a], op, part_acc[a][b]);
-            }
+            const u4 q = *(const u4 *)&sa[row][16 * ((4 * j + g) ^ row)];
+            sum = T::mma(q, ones, sum);
+            part_acc = T::mma(q, codes_op<T>(w[j] ^ kFlip), part_acc);
             if ((j & gmask) == gmask) {  // a group ends
                 const int gi = (c << sshift) + (j >> (2 - sshift));  // of the CH steps
+                uint32_t sz = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint32_t sz = 0;
+                for (int i = 0; i < CH; ++i)
+                    if (gi >> 2 == i)
+                        sz = x.s[i] | (uint32_t)x.z[i] << 16;
+                sz = __shfl(sz, l16 + 16 * (gi & 3), 64);
+                const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
+                const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
 #pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        if (gi >> 2 == i)
-                            sz = x.s[i][b] | (uint32_t)x.z[i][b] << 16;
-                    sz = __shfl(sz, l16 + 16 * (gi & 3), 64);
-                    const float s = half_bits(sz & 0xffffu) * (T::kBf16 ? 1.0f : 0x1p20f);
-                    const float z = ((T::kBf16 ? 136.0f : 8.0f) + half_bits(sz >> 16)) * (T::kBf16 ? 1.0f : 0x1p-20f);
-#pragma unroll
-                    for (int a = 0; a < NA; ++a) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[a][b][i] += s * (part_acc[a][b][i] - z * sum[a][i]);
-                        part_acc[a][b] = zero4;
-                    }
-                }
-#pragma unroll
-                for (int a = 0; a < NA; ++a)
-                    sum[a] = zero4;
+                for (int i = 0; i < 4; ++i)
+                    acc[i] += s * (part_acc[i] - z * sum[i]);
+                part_acc = sum = zero4;
             }
         }
         wave_sync();
     };
     if (first < last) {
-        Steps<NB, NL, CH> x, y;
+        Steps<NL, CH> x, y;
         load(x, first);
         for (int c0 = first; c0 < last; c0 += CH) {
             if (c0 + CH < last)
@@ -396,26 +329,19 @@ __global__ __launch_bounds__(64 * WAVES) void w4g_skinny_kernel(const uint16_t *
         }
     }
     __syncthreads();
-    // join the wavefronts, 16 activation rows at a time
+    // join the wavefronts
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-        if (a)
-            __syncthreads();
+    for (int i = 0; i < 4; ++i)
+        sh.red[wave][4 * g + i][l16] = acc[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 256; e += 64 * WAVES) {
+        const int m = e >> 4, n = e & 15;
+        float v = 0.0f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sh.red[wave][4 * g + i][16 * b + l16] = acc[a][b][i];
-        __syncthreads();
-        for (int e = threadIdx.x; e < 256 * NB; e += 64 * WAVES) {
-            const int m = e / (16 * NB), n = e % (16 * NB);
-            float v = 0.0f;
-#pragma unroll
-            for (int q = 0; q < WAVES; ++q)
-                v += sh.red[q][m][n];
-            if (16 * a + m < M && n0 + n < N)
-                C[(int64_t)(16 * a + m) * N + n0 + n] = T::from_f32(v);
-        }
+        for (int q = 0; q < WAVES; ++q)
+            v += sh.red[q][m][n];
+        if (m < M && n0 + n < N)
+            C[(int64_t)m * N + n0 + n] = T::from_f32(v);
     }
 }
 
@@ -432,14 +358,14 @@ __global__ __launch_bounds__(256) void w4g_join_kernel(const float *__restrict__
     C[i] = T::from_f32(v);
 }
 
-template <typename T, int NA, int NL, int WAVES, int CH>
+template <typename T, int NL, int WAVES, int CH>
 hipError_t launch_skinny_t(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
                            uint16_t *C, int M, int N, int K, hipStream_t s)
 {
     const int64_t wgs = ((int64_t)N + 15) / 16;
     if (!grid_fits(wgs, 64 * WAVES))
         return kGridTooLarge;
-    w4g_skinny_kernel<T, NA, 1, NL, WAVES, CH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
+    w4g_skinny_kernel<T, NL, WAVES, CH><<<dim3((unsigned)wgs), 64 * WAVES, 0, s>>>(A, B, scale, zero, gshift, C, M, N, K);
     return hipGetLastError();
 }
 
@@ -742,14 +668,14 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
     // wavefronts, four steps 5.9 us, four wavefronts 6.6; N = 11008: 16.5,
     // 14.1).
     if (M == 1)
-        return launch_gemv_t<T, 1, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
+        return launch_gemv_t<T>(A, B, scale, zero, gshift, C, N, K, s);
     if (M <= 4)
-        return N <= 16 * 512 ? launch_skinny_t<T, 1, 1, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, s)
-                             : launch_skinny_t<T, 1, 1, 4, 4>(A, B, scale, zero, gshift, C, M, N, K, s);
+        return N <= 16 * 512 ? launch_skinny_t<T, 1, 8, 4>(A, B, scale, zero, gshift, C, M, N, K, s)
+                             : launch_skinny_t<T, 1, 4, 4>(A, B, scale, zero, gshift, C, M, N, K, s);
     if (M <= 8)
-        return launch_skinny_t<T, 1, 2, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, s);
+        return launch_skinny_t<T, 2, 8, 2>(A, B, scale, zero, gshift, C, M, N, K, s);
     if (M <= 16)
-        return launch_skinny_t<T, 1, 4, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
+        return launch_skinny_t<T, 4, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
     // Larger tiles move less, but there have to be enough of them (M = 2048, N =
     // K = 4096: 128 x 128 80 us, 128 x 64 106; M = 256, N = 11008, 172 tiles of
     // 128 x 128: 46, 59, 64 x 64 58; M = 512, N = 4096, K = 11008, 128 tiles: 113,

@@ -391,6 +391,23 @@ def test_attn_kv4_ragged_queries(bq, dev, T):
 
 
 @pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("ws", ["auto", "full"])
+def test_attn_kv4_many_short_one_long(bq, dev, T, ws):
+    """More sequences than a wavefront has lanes, the longest of them last,
+    short ones whose later splits are empty."""
+    banner(f"attn: many sequences {T} {ws}")
+    g = gen(99)
+    lens = [(7 * i) % 23 for i in range(69)] + [1300]
+    hq, d, page = 3, 64, 16
+    pages = sum(-(-n // page) for n in lens) + 2
+    cache = make_cache(g, pages, 1, d, page, T)
+    tab = tables(g, lens, page, pages)
+    q = (torch.randn(len(lens), hq, d, generator=g) * 1.5).to(T)
+    got = run_attn(bq, dev, q, cache, tab, lens, 1, page, ws=ws)
+    check_attn(got, q, cache, tab, lens, list(range(len(lens) + 1)), what="many sequences")
+
+
+@pytest.mark.parametrize("T", TYPES)
 def test_attn_kv4_bad_pages_and_lengths(bq, dev, T):
     """Pages outside the cache are not attended to; lengths are taken within
     the block table; max_q_len and the queries' range bound what is written."""
@@ -630,3 +647,59 @@ def test_layer_other_stream(bq, dev):
         _layer_step(bq, p)
     s.synchronize()
     assert torch.equal(p["y"], want)
+
+
+def test_layer_two_streams_at_once(bq, dev):
+    """Two streams' calls, each with workspaces of its own, at the same time."""
+    banner("layer steps on two streams")
+    states = [_layer_state(bq, dev, T)[0] for T in TYPES]
+    wants = []
+    for o in states:
+        _layer_step(bq, o)
+        torch.cuda.synchronize()
+        wants.append(o["y"].clone())
+        o["y"].zero_()
+    streams = [torch.cuda.Stream() for _ in states]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for o, s in zip(states, streams):
+            with torch.cuda.stream(s):
+                _layer_step(bq, o)
+    torch.cuda.synchronize()
+    for o, want in zip(states, wants):
+        assert torch.equal(o["y"], want)
+
+
+def test_layer_workspaces_from_the_graphs_pool(bq, dev):
+    """Workspaces that the calls allocate themselves under capture: two graphs
+    replayed in turn, each against the eager results."""
+    banner("layer products and attention in two graphs, workspaces allocated under capture")
+    graphs, wants, outs = [], [], []
+    for T in TYPES:
+        o, _, _ = _layer_state(bq, dev, T, B=18)
+
+        def step(o=o):
+            bq.gemm_w4g_a16(o["x"], o["wqkv"], o["sqkv"], out=o["qkv"])
+            bq.attn_kv4(o["qkv"].view(18, -1, o["d"])[:, :o["hq"]], o["cache"], o["table"], o["lens"], o["page"], o["hkv"],
+                        out=o["o"], lse=o["lse"])
+
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()
+        torch.cuda.synchronize()
+        wants.append((o["qkv"].clone(), o["o"].clone(), o["lse"].clone()))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+        graphs.append(g)
+        outs.append((o["qkv"], o["o"], o["lse"]))
+    for rep in range(3):
+        for g, got, want in zip(graphs, outs, wants):
+            for t in got:
+                t.fill_(3)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a, b), f"replay {rep}"
