@@ -225,33 +225,37 @@ __device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8
             F16::from_f32(sc) | (uint32_t)F16::from_f32(mn) << 16;
 }
 
-// A row's lanes take HB heads of one token, one after another: what belongs
-// to the token is found once, and the heads' loads are in flight together.
+// A wavefront takes one unit of 64 / LPR tokens: HB neighbouring heads of one
+// kind (queries, keys, values), a row of lanes a token.  So all of it runs one
+// kind's code, the head is the same in all lanes, and what belongs to the token
+// (position, slot, cosines) is found once for HB heads, whose loads are in
+// flight together.  Units of the same heads and kTokens tokens are neighbours:
+// where slots are neighbours too, their codes fill cache lines together.
+// (Rows that took the heads of one token after another mixed kinds in a
+// wavefront: 4096 tokens of 32 + 8 heads of 128 with a cache 35.6 us, so 31.0.)
+constexpr int kTokens = 16;
+
 template <typename T, int LPR, bool CACHE, int HB>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs p)
 {
-    constexpr int D = 8 * LPR;
-    const uint32_t heads = p.hq + p.hkv * (CACHE ? 2 : 1), units = (heads + HB - 1) / HB;
+    constexpr int D = 8 * LPR, kRows = 64 / LPR, kPer = kTokens / kRows;
+    const uint32_t uq = (p.hq + HB - 1) / HB, uk = (p.hkv + HB - 1) / HB, units = uq + uk * (CACHE ? 2 : 1);
     // the grid limit keeps units of all tokens below 2^32
-    const uint32_t unit = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + threadIdx.x / 64);
+    const uint32_t block = wave / (units * kPer), in_block = wave - block * (units * kPer);
+    uint32_t unit = in_block / kPer;
+    const int64_t tok = (block * kPer + in_block % kPer) * kRows + (threadIdx.x & 63) / LPR;
     const int sub = threadIdx.x % LPR;
-    const uint32_t tok32 = unit / units;
-    // heads `units` apart: neighbouring rows then hold neighbouring heads, mostly
-    // of one kind, and a wavefront runs one kind's code
-    const int head0 = (int)(unit - tok32 * units);
-    const int64_t tok = tok32;
     if (tok >= p.tokens)
         return;
+    const bool isQ = unit < uq, isV = unit >= uq + uk;
+    unit -= isQ ? 0 : isV ? uq + uk : uq;
+    const int heads = isQ ? p.hq : p.hkv, head0 = unit * HB;
+    const uint16_t *src = isQ ? p.q + tok * p.q_stride : isV ? p.v + tok * p.v_stride : p.k + tok * p.k_stride;
     uint4 raw[HB];
 #pragma unroll
-    for (int i = 0; i < HB; ++i) {
-        const int head = min(head0 + i * (int)units, (int)heads - 1);
-        const int kv = head - p.hq;
-        const uint16_t *src = kv < 0                ? p.q + tok * p.q_stride + head * D
-                              : !CACHE || kv < p.hkv ? p.k + tok * p.k_stride + kv * D
-                                                     : p.v + tok * p.v_stride + (kv - p.hkv) * D;
-        raw[i] = *(const uint4 *)(src + 8 * sub);
-    }
+    for (int i = 0; i < HB; ++i)
+        raw[i] = *(const uint4 *)(src + min(head0 + i, heads - 1) * D + 8 * sub);
     // a row's lanes take one path together: every shuffle stays inside a row
     int64_t pos = 0;
     if (p.rot) {
@@ -259,27 +263,36 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs
         if (pos < 0 || pos >= p.max_pos)
             return;
     }
-    const Turn turn = turn_of(p.cos + pos * (p.rot / 2), p.sin + pos * (p.rot / 2), p.rot, p.inter, sub);
-    int64_t slot = 0;
-    bool stored = false;
-    if constexpr (CACHE) {
-        slot = p.slots[tok];
-        stored = slot >= 0 && slot < p.num_pages << p.page_shift;
-    }
+    if (!CACHE || isQ) {
+        const Turn turn = turn_of(p.cos + pos * (p.rot / 2), p.sin + pos * (p.rot / 2), p.rot, p.inter, sub);
+        const uint16_t *w = isQ ? p.q_weight : p.k_weight;
+        uint16_t *out = (isQ ? p.q_out : p.k_out) + tok * heads * D + 8 * sub;
 #pragma unroll
-    for (int i = 0; i < HB; ++i) {
-        const int head = head0 + i * (int)units, kv = head - p.hq;
-        uint16_t o[8];
-        if (head >= (int)heads)
-            break;
-        if (kv < 0) {
-            norm_rope<T, float, LPR>(raw[i], p.q_weight, p.eps, turn, p.rot, p.inter, sub, o);
-            *(uint4 *)(p.q_out + (tok * p.hq + head) * D + 8 * sub) = pack8(o);
-        } else if constexpr (!CACHE) {
-            norm_rope<T, float, LPR>(raw[i], p.k_weight, p.eps, turn, p.rot, p.inter, sub, o);
-            *(uint4 *)(p.k_out + (tok * p.hkv + kv) * D + 8 * sub) = pack8(o);
-        } else if (stored) {
-            const bool isV = kv >= p.hkv;
+        for (int i = 0; i < HB; ++i) {
+            if (head0 + i >= heads)
+                break;
+            uint16_t o[8];
+            norm_rope<T, float, LPR>(raw[i], w, p.eps, turn, p.rot, p.inter, sub, o);
+            *(uint4 *)(out + (head0 + i) * D) = pack8(o);
+        }
+    }
+    if constexpr (CACHE) {
+        if (isQ)
+            return;
+        const int64_t slot = p.slots[tok];
+        if (slot < 0 || slot >= p.num_pages << p.page_shift)
+            return;
+        const int page_size = 1 << p.page_shift;
+        const uint32_t at = (uint32_t)slot & (page_size - 1);
+        uint8_t *base = p.cache + head_base(slot >> p.page_shift, head0, p.hkv, page_size, D);
+        Turn turn;
+        if (!isV)
+            turn = turn_of(p.cos + pos * (p.rot / 2), p.sin + pos * (p.rot / 2), p.rot, p.inter, sub);
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            if (head0 + i >= heads)
+                break;
+            uint16_t o[8];
             if (isV) {
                 const uint32_t r[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
@@ -290,9 +303,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs
             } else {
                 norm_rope<T, double, LPR>(raw[i], p.k_weight, p.eps, turn, p.rot, p.inter, sub, o);
             }
-            const int page_size = 1 << p.page_shift;
-            store_kv4<T, LPR>(o, isV, p.cache + head_base(slot >> p.page_shift, isV ? kv - p.hkv : kv, p.hkv, page_size, D),
-                              (uint32_t)slot & (page_size - 1), page_size, sub);
+            store_kv4<T, LPR>(o, isV, base + i * (int64_t)page_size * (D + 8), at, page_size, sub);
         }
     }
 }
@@ -342,15 +353,15 @@ template <typename T, int LPR, bool CACHE>
 hipError_t launch_rope_t(const QkRopeArgs &p, hipStream_t s)
 {
     const int64_t heads = p.hq + (int64_t)p.hkv * (CACHE ? 2 : 1);
-    // Four heads a row of lanes once that still gives each of the 1024 SIMDs
-    // four wavefronts (8191 tokens, 32 + 8 heads of 128: 35.7 against 38.4 us);
-    // one for shorter calls, and where a cache is written: its three kinds of
-    // heads then share wavefronts (4097 tokens, 16 + 16 + 16 of 64: 17.4 us,
-    // two heads 18.9, four 18.7).
-    constexpr int kPer = kThreads / LPR, kMany = CACHE ? 1 : 4;
-    const bool many = !CACHE && p.tokens * heads * LPR >= 4 * 64 * 4096;
-    const int64_t units = p.tokens * (many ? (heads + 3) / 4 : heads);
-    const int64_t wgs = (units + kPer - 1) / kPer;
+    // Four heads a row of lanes once there are 12 wavefronts' work for each of
+    // the 1024 SIMDs, one for shorter calls.  With a cache, heads of 128, 32 + 8:
+    // 4096 tokens 31.0 us, with one head 37.3; 512 tokens 8.8, with one 7.5;
+    // heads of 64, 16 + 16: 2048 tokens 10.5 against 10.8, 1024 8.7 against 6.1.
+    constexpr int kMany = 4;
+    const bool many = p.tokens * heads * LPR >= 3 * 64 * 4096;
+    const auto units = [&](int64_t per) { return (p.hq + per - 1) / per + (CACHE ? 2 : 1) * ((p.hkv + per - 1) / per); };
+    const int64_t waves = (p.tokens + kTokens - 1) / kTokens * (kTokens * LPR / 64) * units(many ? kMany : 1);
+    const int64_t wgs = (waves + kThreads / 64 - 1) / (kThreads / 64);
     if (!grid_fits(wgs, kThreads))
         return kGridTooLarge;
     const dim3 grid((unsigned)wgs);

@@ -245,6 +245,21 @@ def test_qk_norm_rope_kv4_and_read(bq, dev, c, T):
             within(got[t], want, half_step(T) * want.abs() * (1 + 2.0 ** -10) + 2.0 ** -25, "cache: read")
 
 
+# calls long enough for several heads a row of lanes; head counts that no group divides
+@pytest.mark.parametrize("c", [(2500, 17, 3, 128, 128, False, True), (820, 17, 15, 256, 96, True, True),
+                               (3301, 17, 15, 64, 64, False, True), (2600, 18, 1, 128, 64, False, False)])
+@pytest.mark.parametrize("T", TYPES)
+def test_qk_norm_rope_long(bq, dev, c, T):
+    test_qk_norm_rope(bq, dev, c, T)
+
+
+@pytest.mark.parametrize("c", [(1410, 17, 9, 128, 128, False, True, 16), (707, 17, 9, 256, 64, True, True, 32),
+                               (2811, 17, 9, 64, 64, False, True, 64), (3109, 0, 8, 128, 0, False, False, 16)])
+@pytest.mark.parametrize("T", TYPES)
+def test_qk_norm_rope_kv4_and_read_long(bq, dev, c, T):
+    test_qk_norm_rope_kv4_and_read(bq, dev, c, T)
+
+
 def test_kv4_nonfinite_stays_in_its_head(bq, dev):
     """NaN and infinities make unspecified codes of their own token and head only."""
     banner("cache, non-finite values")
