@@ -38,8 +38,7 @@
 namespace bq {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kWaves = 4, kMany = 8;  // wavefronts of a workgroup
 constexpr int kTile = 32;      // tokens of a step
 constexpr float kNoMax = -3.0e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -437,13 +436,14 @@ struct Wave {
     }
 };
 
-template <typename T, int D, int RT>
-__global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
+// WAVES: kWaves, or kMany where `many_waves` says so.
+template <typename T, int D, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args p)
 {
     constexpr int DH = D > 128 ? 128 : D;  // channels joined at a time
     constexpr int ROWS = 16 * RT;
-    __shared__ float so[kWaves][16][DH + 4];
-    __shared__ float sm[kWaves][ROWS], sl[kWaves][ROWS];
+    __shared__ float so[WAVES][16][DH + 4];
+    __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int split = blockIdx.x % p.nsplit, item = blockIdx.x / p.nsplit;
@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
         w.init_row(i, qw[i], p.scale);
     }
     const int *table = p.block_table + (int64_t)b * p.max_blocks;
-    constexpr int kStep = kWaves * kTile;
+    constexpr int kStep = WAVES * kTile;
     int t = start + wave * kTile;
     if (t < end) {
         // K of the next tile is loaded when the scores have used this one's, V
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
             sl[wave][16 * i + m] = w.l[i];
         }
     }
-    const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;
+    const int jr = threadIdx.x >> 4 & 15, jc = threadIdx.x & 15;
     constexpr int CH = DH / 16;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -547,13 +547,15 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
                     *(float4 *)&so[wave][m][(g * 4 + k) * CH + j] = make_float4(o[0][k], o[1][k], o[2][k], o[3][k]);
                 }
             __syncthreads();
+            if (WAVES > kWaves && threadIdx.x >= 256)
+                continue;  // 256 threads join
             float mm = sm[0][16 * i + jr];
 #pragma unroll
-            for (int k = 1; k < kWaves; ++k)
+            for (int k = 1; k < WAVES; ++k)
                 mm = fmaxf(mm, sm[k][16 * i + jr]);
             float l = 0.0f, acc[CH] = {};
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) {
+            for (int k = 0; k < WAVES; ++k) {
                 const float f = __builtin_amdgcn_exp2f(sm[k][16 * i + jr] - mm);
                 l += f * sl[k][16 * i + jr];
 #pragma unroll
@@ -561,7 +563,7 @@ __global__ __launch_bounds__(kThreads) void attn_kv4_kernel(const AttnKv4Args p)
                     acc[j] += f * so[k][jr][jc * CH + j];
             }
             if (orow < r.rows) {
-                if (p.nsplit == 1) {
+                if (WAVES > kWaves || p.nsplit == 1) {
                     uint16_t *dst = (uint16_t *)p.out + orow_at * D + c * DH + jc * CH;
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                     uint32_t y[CH / 2];
@@ -648,13 +650,26 @@ __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
     }
 }
 
+// Sequences that are not split, one workgroup a CU at most, are walked by eight
+// wavefronts a workgroup: 1 sequence of 700 keys, 8 kv heads of 128, 9.0 us
+// against 10.3 with four; 32 of 1024 12.6 against 14.6; 64 of them (512
+// workgroups) 24.0 against 20.7.  Not where a wavefront holds more than 128
+// channels of 16 rows, whose join outlasts the gain (D = 256: 40 keys 7.6
+// against 6.4, 700 keys 14.0 against 13.4).
+bool many_waves(int D, int rt, int64_t items) { return D * rt <= 128 && items <= 256; }
+
 template <typename T, int D, int RT>
 hipError_t launch_t(const AttnKv4Args &p, hipStream_t s)
 {
     const int64_t items = (int64_t)p.batch * p.hkv * p.row_tiles;
-    if (!grid_fits(items * p.nsplit, kThreads) || !grid_fits(items * p.join_rows, 256))
+    if (!grid_fits(items * p.nsplit, 64 * kWaves) || !grid_fits(items * p.join_rows, 256))
         return kGridTooLarge;
-    attn_kv4_kernel<T, D, RT><<<dim3((unsigned)(items * p.nsplit)), kThreads, 0, s>>>(p);
+    if constexpr (D * RT <= 128)
+        if (p.nsplit == 1 && many_waves(D, RT, items)) {
+            attn_kv4_kernel<T, D, RT, kMany><<<dim3((unsigned)items), 64 * kMany, 0, s>>>(p);
+            return hipGetLastError();
+        }
+    attn_kv4_kernel<T, D, RT, kWaves><<<dim3((unsigned)(items * p.nsplit)), 64 * kWaves, 0, s>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.nsplit == 1)
         return e;
@@ -694,10 +709,14 @@ AttnKv4Plan attn_kv4_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_
     // 1536, 89 with 576).
     const int64_t slots = 256 * (D == 256 || (D == 128 && rt == 2) ? 2 : D == 64 && rt == 1 ? 4 : 3);
     // Up to 1024 keys are not split: the second kernel costs what the shorter
-    // first one gains (1 sequence of 700, 8 kv heads: 10.3 us against 5.7 + 3.9),
-    // and a caller its launch.
+    // first one gains (8 kv heads of 128: 1 sequence of 700 keys 9.0 us against
+    // 10.2 in four, of 1024 10.2 against 9.3 in eight, of 1500 13.5 against 10.5),
+    // and a caller its launch.  Where eight wavefronts a workgroup fill half of
+    // the CUs, up to 2048 keys (16 sequences of 2048 18.1 us either way, 32 20.7
+    // against 25.6; 16 of 4096 33.1 against 26.7).
+    const int64_t whole = many_waves(D, rt, items) && items >= 128 ? 2048 : 1024;
     const int64_t step = kTile * kWaves;
-    const int64_t want = items > 0 && max_len > 1024 ? slots / items : 1, most = (max_len + step - 1) / step;
+    const int64_t want = items > 0 && max_len > whole ? slots / items : 1, most = (max_len + step - 1) / step;
     const int64_t n = want < most ? want : most;
     a.nsplit = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
     a.part_rows = a.nsplit > 1 ? items * a.nsplit * 16 * rt : 0;

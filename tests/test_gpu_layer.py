@@ -423,6 +423,23 @@ def test_attn_kv4_many_short_one_long(bq, dev, T, ws):
 
 
 @pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("batch,top,hq,hkv,d,window", [(40, 333, 16, 8, 64, 0), (33, 290, 8, 8, 128, 50), (17, 1400, 16, 8, 128, 0),
+                                                       (65, 150, 40, 5, 64, 0)])
+def test_attn_kv4_many_workgroups(bq, dev, T, batch, top, hq, hkv, d, window):
+    """Enough sequences and heads that every one of them is one workgroup's."""
+    banner(f"attn: many workgroups {batch} {top} {hq} {hkv} {d} {window} {T}")
+    g = gen(batch + top)
+    page = 16
+    lens = [(37 * i + 1) % (top // 4) for i in range(batch - 1)] + [top]
+    pages = sum(-(-n // page) for n in lens) + 2
+    cache = make_cache(g, pages, hkv, d, page, T)
+    tab = tables(g, lens, page, pages)
+    q = (torch.randn(len(lens), hq, d, generator=g) * 1.5).to(T)
+    got = run_attn(bq, dev, q, cache, tab, lens, hkv, page, window=window)
+    check_attn(got, q, cache, tab, lens, list(range(len(lens) + 1)), window, what="many workgroups")
+
+
+@pytest.mark.parametrize("T", TYPES)
 def test_attn_kv4_bad_pages_and_lengths(bq, dev, T):
     """Pages outside the cache are not attended to; lengths are taken within
     the block table; max_q_len and the queries' range bound what is written."""
