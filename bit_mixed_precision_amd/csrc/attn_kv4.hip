@@ -32,6 +32,7 @@
 //
 // Long sequences are split over workgroups (and over a workgroup's
 // wavefronts, joined through LDS); a second kernel joins the parts in order.
+#include "attn_rows.h"
 #include "bq_internal.h"
 #include "dtype16.h"
 
@@ -56,13 +57,11 @@ struct Rows {
 // First query of sequence b, and its query rows per kv head.
 __device__ __forceinline__ void query_rows(const AttnKv4Args &p, int b, int &q0, int &rows)
 {
-    int qlen = p.max_q_len;
-    q0 = b * p.max_q_len;
-    if (p.q_start) {
-        q0 = max(p.q_start[b], 0);
-        qlen = min(max(min(p.q_start[b + 1], p.total_q) - q0, 0), p.max_q_len);
-    }
-    rows = qlen * p.group;
+    QueryRows r = {b * p.max_q_len, p.max_q_len};
+    if (p.q_start)
+        r = query_rows_of(p.q_start[b], p.q_start[b + 1], p.total_q, p.max_q_len);
+    q0 = r.first;
+    rows = r.count * p.group;
 }
 
 // Rows `tile` * ROWS on of sequence b.  Every split takes `chunk` keys, the

@@ -735,3 +735,28 @@ def test_layer_workspaces_from_the_graphs_pool(bq, dev):
             torch.cuda.synchronize()
             for a, b in zip(got, want):
                 assert torch.equal(a, b), f"replay {rep}"
+
+
+# ---------------------------------------------------------------- index arrays that hold anything
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("keys", [40, 1500])
+def test_attn_kv4_query_starts_anywhere(bq, dev, T, keys):
+    """q_start values at the ends of 32 bits: the queries taken within
+    [0, total_q) are computed, every other row stays as it was.  With 1500
+    keys the sequences are split."""
+    banner(f"attn: q_start at the ends of 32 bits, {keys} keys {T}")
+    hq, hkv, d, page = 4, 2, 128, 16
+    big, small = 2**31 - 1, -(2**31)
+    g = gen(21)
+    cache = make_cache(g, -(-keys // page), hkv, d, page, T)
+    tab = torch.arange(-(-keys // page), dtype=torch.int32)[None]
+    q = torch.randn(6, hq, d, generator=g).to(T)
+    for starts, used in (([big, -2], (0, 0)), ([5, small], (0, 0)), ([small, big], (0, 6)), ([small, 2], (0, 2)),
+                         ([4, big], (4, 6)), ([6, 9], (0, 0)), ([-1, -2], (0, 0)), ([big, small], (0, 0))):
+        out, lse = run_attn(bq, dev, q, cache, tab, [keys], hkv, page, starts, 6)
+        lo, hi = used
+        if hi > lo:
+            check_attn((out[lo:hi], lse[lo:hi]), q[lo:hi], cache, tab, [keys], [0, hi - lo], what=f"starts {starts}")
+        for t in (out, lse):
+            assert (t[:lo] == 7.0).all() and (t[hi:] == 7.0).all(), f"starts {starts}"
