@@ -671,8 +671,9 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
     a token) over the 4-bit cache: sequence b's queries stand at the end of
     its seq_lens[b] cached keys (int32 [batch]), found through block_table
     int32 [batch, max_blocks]; causal, within the last `window` keys if
-    window > 0.  q_start int32 [batch + 1] gives each sequence's queries, at
-    most max_q_len; None: total_q / batch each.  scale None: head_dim ** -0.5.
+    window > 0.  q_start int32 [batch + 1] gives each sequence's queries, of
+    which the first max_q_len are computed (the others' outputs are not
+    written); None: total_q / batch each.  scale None: head_dim ** -0.5.
 
     -> out, of q's shape and type; (out, lse) with return_lse or lse given:
     lse fp32 [total_q, q_heads].  A row with no keys gives zeros (lse -inf).

@@ -47,21 +47,19 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // What one tile of 16 query rows attends to.
 struct Rows {
     int q0;          // first row of the sequence's queries in q / out
-    int rows;        // query rows of the sequence and kv head (q_len * group)
+    int rows;        // query rows of the sequence and kv head (computed queries * group)
     int base;        // position of the first query
     int pos_min, pos_max;
     int lo, hi;      // keys [lo, hi), lo a multiple of kTile
     int chunk;       // keys of one split
 };
 
-// First query of sequence b, and its query rows per kv head.
-__device__ __forceinline__ void query_rows(const AttnKv4Args &p, int b, int &q0, int &rows)
+// Queries of sequence b.
+__device__ __forceinline__ QueryRows query_rows(const AttnKv4Args &p, int b)
 {
-    QueryRows r = {b * p.max_q_len, p.max_q_len};
     if (p.q_start)
-        r = query_rows_of(p.q_start[b], p.q_start[b + 1], p.total_q, p.max_q_len);
-    q0 = r.first;
-    rows = r.count * p.group;
+        return query_rows_of(p.q_start[b], p.q_start[b + 1], p.total_q, p.max_q_len);
+    return {b * p.max_q_len, p.max_q_len, p.max_q_len};
 }
 
 // Rows `tile` * ROWS on of sequence b.  Every split takes `chunk` keys, the
@@ -71,9 +69,11 @@ template <int ROWS>
 __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
 {
     Rows r;
-    query_rows(p, b, r.q0, r.rows);
+    const QueryRows q = query_rows(p, b);
+    r.q0 = q.first;
+    r.rows = q.count * p.group;
     const int len = min(max(p.seq_lens[b], 0), p.max_blocks << p.page_shift);
-    r.base = len - r.rows / p.group;
+    r.base = len - q.len;
     const int first = tile * ROWS / p.group, last = min(tile * ROWS + ROWS - 1, r.rows - 1) / p.group;
     r.pos_min = r.base + first;
     r.pos_max = r.base + last;
@@ -449,8 +449,8 @@ __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args 
     const int tile = item % p.row_tiles;
     const int head = item / p.row_tiles % p.hkv;
     const int b = item / p.row_tiles / p.hkv;
-    int q0, rows;
-    query_rows(p, b, q0, rows);
+    const QueryRows qr = query_rows(p, b);
+    const int q0 = qr.first, rows = qr.count * p.group;
     if (tile * ROWS >= rows)
         return;
     // the queries are on their way while the keys are found

@@ -152,9 +152,11 @@ int bq_kv4_read(const void *cache, int64_t num_pages, int page_size, int kv_head
  *                the end; each is taken within [0, total_q], and a sequence
  *                whose end is not past its start has none; NULL: max_q_len
  *                queries each (total_q = batch * max_q_len)
- *   max_q_len    the most queries of one sequence; further ones of a sequence
- *                are left out: their outputs stay as they were, like rows
- *                behind the last sequence
+ *   max_q_len    the most queries of one sequence that are computed, its first
+ *                ones; further ones of a sequence are left out: their outputs
+ *                stay as they were, like rows behind the last sequence, and
+ *                the positions of the others do not depend on it (q_len counts
+ *                all of a sequence's queries)
  *   seq_lens     [batch] int32, keys in the cache with the new ones; taken
  *                within [0, max_blocks * page_size]
  *   block_table  [batch, max_blocks] int32; tokens of a page outside

@@ -760,3 +760,29 @@ def test_attn_kv4_query_starts_anywhere(bq, dev, T, keys):
             check_attn((out[lo:hi], lse[lo:hi]), q[lo:hi], cache, tab, [keys], [0, hi - lo], what=f"starts {starts}")
         for t in (out, lse):
             assert (t[:lo] == 7.0).all() and (t[hi:] == 7.0).all(), f"starts {starts}"
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("longest", [50, 1500])
+def test_attn_kv4_sequences_longer_than_max_q_len(bq, dev, T, longest):
+    """Of sequences with more queries than max_q_len the first max_q_len are
+    computed, each at its own position; the others stay as they were.  With
+    1500 keys the sequences are split."""
+    banner(f"attn: more queries than max_q_len, {longest} keys {T}")
+    lens, starts, most, hq, hkv, d, page = [longest, 30, 21], [0, 12, 14, 23], 5, 4, 2, 64, 16
+    g = gen(22)
+    pages = sum(-(-n // page) for n in lens)
+    cache = make_cache(g, pages, hkv, d, page, T)
+    tab = tables(g, lens, page, pages)
+    q = torch.randn(23, hq, d, generator=g).to(T)
+    out, lse = run_attn(bq, dev, q, cache, tab, lens, hkv, page, starts, most)
+    want, wlse = run_attn(bq, dev, q, cache, tab, lens, hkv, page, starts, 12)
+    check_attn((want, wlse), q, cache, tab, lens, starts, what="all queries")
+    for b in range(3):
+        n = starts[b + 1] - starts[b]
+        # the sequence's computed queries alone, at the end of a shorter cache
+        k = min(n, most)
+        part = slice(starts[b], starts[b] + k)
+        check_attn((out[part], lse[part]), q[part], cache, tab[b: b + 1], [lens[b] - n + k], [0, k], what=f"sequence {b}")
+        left = slice(starts[b] + k, starts[b + 1])
+        assert (out[left] == 7.0).all() and (lse[left] == 7.0).all(), f"sequence {b}: queries left out"

@@ -29,11 +29,12 @@ extern "C" void rows(int start, int end, int total, int most, int *out)
     const bq::QueryRows r = bq::query_rows_of(start, end, total, most);
     out[0] = r.first;
     out[1] = r.count;
+    out[2] = r.len;
 }
 """)
 
     def call(*a):
-        out = (ctypes.c_int * 2)()
+        out = (ctypes.c_int * 3)()
         lib.rows(*a, out)
         return tuple(out)
 
@@ -52,8 +53,16 @@ def test_query_rows_stay_inside_the_queries(rows):
     """Whatever the starts hold, the rows lie in [0, total_q) and are those of
     the range taken within it."""
     for start, end, total, most in _cases():
-        first, count = rows(start, end, total, most)
+        first, count, _ = rows(start, end, total, most)
         lo, hi = min(max(start, 0), total), min(max(end, 0), total)
         assert 0 <= first and 0 <= count and first + count <= total, (start, end, total, most, first, count)
         assert count == min(max(hi - lo, 0), most), (start, end, total, most)
         assert count == 0 or first == lo
+
+
+def test_query_positions_do_not_depend_on_the_most_computed(rows):
+    """The length that positions are counted from is the whole range's."""
+    for start, end, total, most in _cases():
+        first, count, length = rows(start, end, total, most)
+        lo, hi = min(max(start, 0), total), min(max(end, 0), total)
+        assert length == max(hi - lo, 0) and count == min(length, most), (start, end, total, most)
