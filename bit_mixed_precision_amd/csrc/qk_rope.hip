@@ -195,9 +195,10 @@ __device__ __forceinline__ void store_kv4(const uint16_t x16[8], bool isV, uint8
         lo = fminf(lo, __shfl_xor(lo, off, 64));
         hi = fmaxf(hi, __shfl_xor(hi, off, 64));
     }
-    // the stored parameters are fp16: bf16 values past its range are held at its ends
+    // the stored parameters are fp16: bf16 values past its range are held at its
+    // ends, and a row below it (max x < min) takes the scale 0
     const float mn = (float)(_Float16)fminf(fmaxf(lo, -65504.0f), 65504.0f);
-    const float sc = (float)(_Float16)fminf((hi - mn) / 15.0f, 65504.0f);
+    const float sc = (float)(_Float16)fminf(fmaxf((hi - mn) / 15.0f, 0.0f), 65504.0f);
     // The correctly rounded quotient from the scale's correctly rounded
     // reciprocal: one correction of d r by its exact remainder (Markstein).
     // A scale of 0 (or no number) makes codes 0.

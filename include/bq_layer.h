@@ -112,7 +112,9 @@ int64_t bq_kv4_page_bytes(int kv_heads, int head_dim, int page_size);
  * and head, in fp32 with correctly rounded quotients:
  *   min = fp16(min x), scale = fp16((max x - min) / 15)
  *   code = nearest((x - min) / scale), ties to even, in 0..15; 0 if scale = 0
- * (bf16 values outside fp16's range are stored as its ends allow.)
+ * min is held within [-65504, 65504] and scale within [0, 65504], so that
+ * finite bf16 values outside fp16's range give finite ones: a row below the
+ * range reads back as -65504, values more than 15 * 65504 above min as that.
  *
  *   v       tokens x kv_heads x head_dim, v_stride between tokens
  *   cache   num_pages pages, 16-byte aligned

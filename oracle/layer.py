@@ -76,10 +76,11 @@ def round_to(x, dtype):
 
 def kv4_codes(x):
     """Codes, scale, min of the rows of x (16-bit values), in the fp32 steps
-    of the definition: min = fp16(min x), scale = fp16((max - min) / 15)."""
+    of the definition: min = fp16(min x), scale = fp16((max - min) / 15), both
+    held at the ends of fp16's range and the scale at 0."""
     x = x.to(torch.float32)
     lo = x.amin(-1, keepdim=True).clamp(-65504, 65504).half().float()
-    s = ((x.amax(-1, keepdim=True) - lo) / 15).clamp(max=65504).half().float()
+    s = ((x.amax(-1, keepdim=True) - lo) / 15).clamp(0, 65504).half().float()
     q = torch.where(s > 0, ((x - lo) / torch.where(s > 0, s, torch.ones_like(s))).round(), torch.zeros_like(x))
     return q.clamp(0, 15).to(torch.uint8), s.half(), lo.half()
 

@@ -786,3 +786,46 @@ def test_attn_kv4_sequences_longer_than_max_q_len(bq, dev, T, longest):
         check_attn((out[part], lse[part]), q[part], cache, tab[b: b + 1], [lens[b] - n + k], [0, k], what=f"sequence {b}")
         left = slice(starts[b] + k, starts[b + 1])
         assert (out[left] == 7.0).all() and (lse[left] == 7.0).all(), f"sequence {b}: queries left out"
+
+
+# ---------------------------------------------------------------- the cache at the ends of fp16's range
+
+def test_kv4_values_outside_fp16s_range(bq, dev):
+    """Finite bf16 rows wholly below fp16's range, wholly above it, across its
+    ends, and constant: finite parameters, a scale of at least 0, values held
+    at what they can express; attention over them stays finite."""
+    banner("cache, bf16 values outside fp16's range")
+    T, d, page = torch.bfloat16, 128, 16
+    g = gen(31)
+    u = torch.rand(14, d, generator=g)
+    rows = torch.stack([-2e6 - 0 * u[0], -2e6 * (1 + u[1]), -65504 * (1 + u[2]), -1e38 * (0.5 + u[3]), 2e6 + 0 * u[4],
+                        7e4 * (1 + u[5]), 1e38 * (0.5 + u[6]), (u[7] - 0.5) * 4e5, (u[8] - 0.5) * 2e38, -1e6 + 0 * u[9],
+                        1e-6 + 0 * u[10], -1e-6 - 0 * u[11], 1e-40 * u[12], (u[13] - 0.5) * 1e-6]).to(T)
+    n = rows.shape[0]
+    cache = torch.full((1, bq.kv4_page_bytes(1, d, page)), 0xA5, dtype=torch.uint8, device=dev)
+    x = rows[:, None].to(dev)
+    bq.qk_norm_rope_kv4(None, x, x, None, None, None, cache, torch.arange(n, device=dev), page)
+    k, v = bq.kv4_read(cache, torch.arange(n, device=dev), page, 1, d, T)
+    torch.cuda.synchronize()
+    ref = layer.Cache(1, 1, d, page, 0xA5)
+    for t in range(n):
+        ref.write(t, rows[t][None], rows[t][None])
+    assert torch.equal(cache.cpu(), ref.flat())
+    x = rows.to(F64)
+    for t in range(n):
+        (q, s, m), _ = ref.read(t)
+        assert torch.isfinite(s).all() and torch.isfinite(m).all() and float(s) >= 0
+        # the nearest code's value, where the parameters reach the value: half a
+        # step, the parameters' own roundings (15 codes of the scale's, the
+        # minimum's) and bf16's on reading
+        want = x[t].clamp(-65504, float(m) + 15 * 65504)
+        tol = float(s) * (0.5 + 15 * 2.0 ** -11) + 15 * 2.0 ** -25 + abs(float(m)) * 2.0 ** -11 + 2.0 ** -25
+        for got in (k, v):
+            got = got[t, 0].cpu().to(F64)
+            assert torch.isfinite(got).all()
+            assert ((got - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8).all(), f"row {t}"
+    q = torch.zeros(1, 2, d, dtype=T)
+    q[0, 0, 0] = 1e-3
+    out, lse = run_attn(bq, dev, q, ref, torch.zeros(1, 1, dtype=torch.int32), [n], 1, page)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    check_attn((out, lse), q, ref, torch.zeros(1, 1, dtype=torch.int32), [n], [0, 1], what="ends of the range")
