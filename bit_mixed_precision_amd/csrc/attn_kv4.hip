@@ -28,7 +28,8 @@
 // output: one rounding of it alone would weigh as much as the output's own;
 // with a bf16 output the high part is enough.
 // The reference maximum is raised only when a score passes it by 2^8, and
-// then for all lanes of the row; sums and accumulators are fp32.
+// then for all lanes of the row; sums and accumulators are fp32.  p sv is
+// brought into fp16's range by the largest V scale that the row has seen.
 //
 // Long sequences are split over workgroups (and over a workgroup's
 // wavefronts, joined through LDS); a second kernel joins the parts in order.
@@ -215,7 +216,7 @@ struct Wave {
     float a1[RT], b1[RT];
     float mt[RT], mref[RT];  // reference maximum of score / a1, and what is subtracted: mt a1 - shift
     float l[RT], z[RT];
-    float cap, shift;        // largest V scale that p sv 2^shift takes in fp16's range
+    float cap[RT];           // largest V scale that p sv 2^shift takes in fp16's range: 2^(6 - shift), or 0 (shift 0)
     int pos[RT];
     u4 ph[RT], pl[RT];       // p sv of the tile, high and low parts
     f4 o[RT][kMT];
@@ -262,7 +263,7 @@ struct Wave {
         a1[r] = fmaxf(back * 0x1p20f * (fabsf(scale) * kLog2e), 0x1p-120f);  // a masked score is -inf a1
         b1[r] = sum * f * 0x1p-20f;
         mt[r] = mref[r] = kNoMax;
-        l[r] = z[r] = 0.0f;
+        l[r] = z[r] = cap[r] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
             o[r][i] = (f4){0, 0, 0, 0};
@@ -331,7 +332,7 @@ struct Wave {
 #pragma unroll
         for (int j = 1; j < 8; ++j)
             vtop = fmaxf(vtop, sv[j]);
-        bool raise = vtop > cap;
+        bool raise = false;
         float top[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -339,24 +340,30 @@ struct Wave {
 #pragma unroll
             for (int j = 1; j < 8; ++j)
                 top[r] = fmaxf(top[r], s[r][j]);
-            raise |= top[r] * a1[r] - mref[r] > 8.0f + shift;
+            raise |= vtop > cap[r] || top[r] * a1[r] > mt[r] + 8.0f;
         }
         if (__builtin_expect(__any(raise), 0)) {
-#pragma unroll
-            for (int off = 16; off < 64; off <<= 1)
-                vtop = fmaxf(vtop, __shfl_xor(vtop, off, 64));
-            if (vtop > cap) {
-                const int e = (int)((__float_as_uint(fminf(vtop, 65504.0f)) >> 23) & 255u) - 125;
-                cap = ldexpf(1.0f, e);
-                shift = (float)(6 - e);
-            }
+            // Each row by the keys that it sees (the others' scores are -inf): no
+            // other key, and nothing that another row needs, changes a bit of it.
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
+                float seen = 0.0f;
 #pragma unroll
-                for (int off = 16; off < 64; off <<= 1)
+                for (int j = 0; j < 8; ++j)
+                    seen = fmaxf(seen, s[r][j] > -__builtin_inff() ? sv[j] : 0.0f);
+#pragma unroll
+                for (int off = 16; off < 64; off <<= 1) {
                     top[r] = fmaxf(top[r], __shfl_xor(top[r], off, 64));
-                mt[r] = fmaxf(mt[r], top[r] * a1[r]);
-                const float now = mt[r] - shift, f = __builtin_amdgcn_exp2f(mref[r] - now);
+                    seen = fmaxf(seen, __shfl_xor(seen, off, 64));
+                }
+                const bool wider = seen > cap[r];
+                if (wider || top[r] * a1[r] > mt[r] + 8.0f)
+                    mt[r] = fmaxf(mt[r], top[r] * a1[r]);
+                // 2 to 4 times the scale
+                const uint32_t e = (__float_as_uint(fminf(seen, 65504.0f)) >> 23) + 2u;
+                cap[r] = wider ? __uint_as_float(e << 23) : cap[r];
+                const float shift = cap[r] > 0.0f ? 133.0f - (float)(__float_as_uint(cap[r]) >> 23) : 0.0f;
+                const float now = mt[r] - shift, f = __builtin_amdgcn_exp2f(mref[r] - now);  // 1 for a row that needs nothing
                 mref[r] = now;
                 l[r] *= f;
                 z[r] *= f;
@@ -470,7 +477,6 @@ __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args 
         return;
 
     Wave<T, D, RT> w;
-    w.cap = w.shift = 0.0f;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int row = tile * ROWS + 16 * i + (lane & 15);

@@ -170,8 +170,11 @@ int bq_kv4_read(const void *cache, int64_t num_pages, int page_size, int kv_head
  *                no particular contents; NULL with 0 bytes, or fewer than
  *                bq_attn_kv4_workspace_bytes, for none (sequences are not
  *                split).  Calls that share one must not overlap.
- * The cache's values are used exactly, the products and sums are fp32; p is
- * held in 22 bits for fp16 outputs and 11 for bf16.
+ * The cache's values are used exactly, the products and sums are fp32; p times
+ * a key's V scale is held in 22 bits for fp16 outputs and 11 for bf16, and to
+ * 2^-29 of the row's largest p times the largest V scale that the row sees.
+ * Keys that a row does not see change no bit of its result, whatever their
+ * codes and parameters are.
  * q_heads a multiple of kv_heads, max_blocks * page_size <= 2^30, total_q <=
  * 2^30 (BQ_ERR_SHAPE).
  */

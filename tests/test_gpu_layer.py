@@ -829,3 +829,59 @@ def test_kv4_values_outside_fp16s_range(bq, dev):
     out, lse = run_attn(bq, dev, q, ref, torch.zeros(1, 1, dtype=torch.int32), [n], 1, page)
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     check_attn((out, lse), q, ref, torch.zeros(1, 1, dtype=torch.int32), [n], [0, 1], what="ends of the range")
+
+
+# ---------------------------------------------------------------- keys that a row does not see
+
+def _set_params(cache, tokens, k, v, page):
+    """fp16 (scale, min) of K and of V at the tokens of pages 0, 1, ..."""
+    for t in tokens:
+        _, _, ak, av = cache._places(t % page)
+        for at, par in ((ak, k), (av, v)):
+            cache.bytes[t // page][:, at] = torch.tensor(par).half().view(torch.uint8)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("hq,d", [(2, 64), (8, 128), (64, 64), (2, 256)])
+@pytest.mark.parametrize("k,v", [([65504.0, 65504.0], [65504.0, 65504.0]), ([0.0, -65504.0], [65504.0, -65504.0]),
+                                 ([0.0, 0.0], [1000.0, 0.0])])
+def test_attn_kv4_unseen_keys_change_no_bit(bq, dev, T, hq, d, k, v):
+    """Large finite parameters of keys before every window, and of the last
+    keys, which only the last rows see: the other rows, whose own V scales are
+    small, keep every bit."""
+    banner(f"attn: unseen keys of large scale {hq} {d} {k} {v} {T}")
+    n, ql, hkv, page = 150, 8, 1, 16
+    g = gen(41)
+    q = torch.randn(ql, hq, d, generator=g).to(T)
+    for window, last in ((40, 1), (0, 4)):
+        cache = make_cache(g, 10, hkv, d, page, T, v_mul=1e-2)
+        tab = torch.arange(10, dtype=torch.int32)[None]
+        want = run_attn(bq, dev, q, cache, tab, [n], hkv, page, window=window)
+        check_attn(want, q, cache, tab, [n], [0, ql], window, what="clean")
+        before = list(range(0, n - ql - window + 1)) if window else []
+        _set_params(cache, before + list(range(n - last, n)), k, v, page)
+        out, lse = run_attn(bq, dev, q, cache, tab, [n], hkv, page, window=window)
+        assert torch.equal(out[:-last], want[0][:-last]) and torch.equal(lse[:-last], want[1][:-last])
+        assert not torch.equal(out[-last:], want[0][-last:])
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("spread", [2.0 ** 8, 2.0 ** 14])
+def test_attn_kv4_one_large_v_scale(bq, dev, T, spread):
+    """A key that every row sees, of a V scale far above the others' and of
+    small weight: p times a scale is also held to 2^-29 of the row's largest p
+    times that scale, which is then the larger error (centred codes of
+    magnitude at most 8, n keys)."""
+    banner(f"attn: one V scale {spread} times the others {T}")
+    n, hq, hkv, d, page = 300, 4, 1, 128, 16
+    g = gen(42)
+    cache = make_cache(g, 19, hkv, d, page, T, k_off=0.0, v_mul=1e-2)
+    tab = torch.arange(19, dtype=torch.int32)[None]
+    s = 1e-2 * 5 / 15 * spread
+    _set_params(cache, [77], [0.0, 0.0], [s, -8 * s], page)
+    q = torch.randn(1, hq, d, generator=g).to(T) * 4
+    out, lse = run_attn(bq, dev, q, cache, tab, [n], hkv, page)
+    want, wlse, size, delta = layer.attention(q, cache, tab, [n], [0, 1], d ** -0.5)
+    r = (2.0 ** -20 if T == torch.float16 else 2.0 ** -10 + 2.0 ** -20) + n * U
+    tol = half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25 + n * 8 * s * 2.0 ** -29
+    within(out, want, tol, "one large V scale")
