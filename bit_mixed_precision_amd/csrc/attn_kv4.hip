@@ -216,7 +216,7 @@ struct Wave {
     float a1[RT], b1[RT];
     float mt[RT], mref[RT];  // reference maximum of score / a1, and what is subtracted: mt a1 - shift
     float l[RT], z[RT];
-    float cap[RT];           // largest V scale that p sv 2^shift takes in fp16's range: 2^(6 - shift), or 0 (shift 0)
+    float cap[RT];           // largest V scale (its size) that p sv 2^shift takes in fp16's range: 2^(6 - shift), or 0 (shift 0)
     int pos[RT];
     u4 ph[RT], pl[RT];       // p sv of the tile, high and low parts
     f4 o[RT][kMT];
@@ -328,10 +328,10 @@ struct Wave {
                 mv[j] = there && number ? mv[j] : 0.0f;
             }
         }
-        float vtop = sv[0];
+        float vtop = fabsf(sv[0]);
 #pragma unroll
         for (int j = 1; j < 8; ++j)
-            vtop = fmaxf(vtop, sv[j]);
+            vtop = fmaxf(vtop, fabsf(sv[j]));
         bool raise = false;
         float top[RT];
 #pragma unroll
@@ -350,7 +350,7 @@ struct Wave {
                 float seen = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    seen = fmaxf(seen, s[r][j] > -__builtin_inff() ? sv[j] : 0.0f);
+                    seen = fmaxf(seen, s[r][j] > -__builtin_inff() ? fabsf(sv[j]) : 0.0f);
 #pragma unroll
                 for (int off = 16; off < 64; off <<= 1) {
                     top[r] = fmaxf(top[r], __shfl_xor(top[r], off, 64));

@@ -27,7 +27,9 @@
  *                                       2Uu + 2U - 1, packed as for K
  *   K params [page_size][2] fp16        scale, min
  *   V params [page_size][2] fp16
- * and the value of a code is code * scale + min.  Token t of a sequence lies
+ * and the value of a code is code * scale + min (bq_qk_norm_rope_kv4 stores
+ * scales of at least 0; a cache laid out by other means may hold negative
+ * ones).  Token t of a sequence lies
  * in page block_table[t / page_size] at t % page_size; a slot is
  * page * page_size + offset.
  */

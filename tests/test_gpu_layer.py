@@ -885,3 +885,39 @@ def test_attn_kv4_one_large_v_scale(bq, dev, T, spread):
     r = (2.0 ** -20 if T == torch.float16 else 2.0 ** -10 + 2.0 ** -20) + n * U
     tol = half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25 + n * 8 * s * 2.0 ** -29
     within(out, want, tol, "one large V scale")
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("d,ql", [(64, 20), (128, 1), (256, 3)])
+@pytest.mark.parametrize("v_mul", [1.0, 3000.0])
+def test_attn_kv4_negative_scales(bq, dev, T, d, ql, v_mul):
+    """A page may hold negative scales: all of V's, or every third one, and
+    half of K's."""
+    banner(f"attn: negative scales d={d} q={ql} {v_mul} {T}")
+    n, hq, hkv, page = 200, 4, 2, 16
+    g = gen(43)
+    for every in (1, 3):
+        cache = make_cache(g, 13, hkv, d, page, T, v_mul=v_mul)
+        plain = layer.Cache(13, hkv, d, page)
+        for t in range(n):
+            _, _, ak, av = cache._places(t % page)
+            if t % 2:
+                cache.bytes[t // page][:, ak[1]] ^= 128
+        plain.bytes = cache.bytes.clone()
+        for t in range(0, n, every):
+            _, _, ak, av = cache._places(t % page)
+            cache.bytes[t // page][:, av[1]] ^= 128
+        tab = torch.arange(13, dtype=torch.int32)[None]
+        q = torch.randn(ql, hq, d, generator=g).to(T)
+        out, lse = run_attn(bq, dev, q, cache, tab, [n], hkv, page)
+        want, wlse, _, delta = layer.attention(q, cache, tab, [n], [0, ql], d ** -0.5)
+        _, _, size, _ = layer.attention(q, plain, tab, [n], [0, ql], d ** -0.5)  # the terms' magnitudes
+        # K's scales of either sign: the score's bound takes their sizes
+        for t in range(n):
+            _, _, ak, _ = plain._places(t % page)
+            plain.bytes[t // page][:, ak[1]] &= 127
+        _, _, _, delta = layer.attention(q, plain, tab, [n], [0, ql], d ** -0.5)
+        r = (2.0 ** -20 if T == torch.float16 else 2.0 ** -10 + 2.0 ** -20) + n * U
+        within(out, want, half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25, f"every {every}")
+        off = (lse.cpu().to(F64) - wlse).abs() - (delta + 2.0 ** -20 * (1 + wlse.abs()))
+        assert (off <= 0).all()
