@@ -246,7 +246,7 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
                 int head_dim, const void *cache, int64_t num_pages, int page_size, int64_t max_blocks, float softmax_scale,
                 int64_t window, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream)
 {
-    if (dtype != BQ_F16 && dtype != BQ_BF16)
+    if ((dtype != BQ_F16 && dtype != BQ_BF16) || !__builtin_isfinite(softmax_scale))
         return BQ_ERR_ARG;
     if (!page_size_ok(page_size) || max_blocks < 0 || max_blocks > BQ_MAX_DIM || num_pages < 0 || num_pages > BQ_MAX_DIM ||
         total_q < 0 || total_q > BQ_MAX_DIM || window < 0 || window > BQ_MAX_DIM || workspace_bytes < 0)

@@ -178,7 +178,7 @@ int bq_kv4_read(const void *cache, int64_t num_pages, int page_size, int kv_head
  * Keys that a row does not see change no bit of its result, whatever their
  * codes and parameters are.
  * q_heads a multiple of kv_heads, max_blocks * page_size <= 2^30, total_q <=
- * 2^30 (BQ_ERR_SHAPE).
+ * 2^30 (BQ_ERR_SHAPE); softmax_scale finite, of any sign (BQ_ERR_ARG).
  */
 int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
                 const int32_t *block_table, int64_t batch, int64_t total_q, int64_t max_q_len, int q_heads, int kv_heads,

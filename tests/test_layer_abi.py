@@ -169,3 +169,10 @@ def test_python_arguments_are_checked(bq):
     with pytest.raises(ValueError):
         bq.attn_kv4(x, torch.zeros(2, 2 * 16 * 136, dtype=torch.uint8), torch.zeros(3, 2, dtype=torch.int32),
                     torch.zeros(3, dtype=torch.int32), 16, 2)
+
+
+def test_attn_kv4_refuses_scales_that_are_no_numbers(bq):
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        assert _attn(bq, scale=bad) == bq.BQ_ERR_ARG, bad
+        assert _attn(bq, scale=bad, batch=0, total=0) == bq.BQ_ERR_ARG, bad
+    assert _attn(bq, scale=3e38, batch=0, total=0) == bq.BQ_OK
