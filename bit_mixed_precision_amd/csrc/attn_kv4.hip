@@ -667,7 +667,7 @@ template <typename T, int D, int RT>
 hipError_t launch_t(const AttnKv4Args &p, hipStream_t s)
 {
     const int64_t items = (int64_t)p.batch * p.hkv * p.row_tiles;
-    if (!grid_fits(items * p.nsplit, 64 * kWaves) || !grid_fits(items * p.join_rows, 256))
+    if (!grid_fits(items * p.nsplit, 64 * kWaves) || (p.nsplit > 1 && !grid_fits(items * p.join_rows, 256)))
         return kGridTooLarge;
     if constexpr (D * RT <= 128)
         if (p.nsplit == 1 && many_waves(D, RT, items)) {

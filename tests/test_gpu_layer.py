@@ -921,3 +921,17 @@ def test_attn_kv4_negative_scales(bq, dev, T, d, ql, v_mul):
         within(out, want, half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25, f"every {every}")
         off = (lse.cpu().to(F64) - wlse).abs() - (delta + 2.0 ** -20 * (1 + wlse.abs()))
         assert (off <= 0).all()
+
+
+def test_attn_kv4_room_for_many_queries(bq, dev):
+    """max_q_len far above the queries that there are: 2^24 query rows of room
+    on 2^19 workgroups, none split."""
+    banner("attn: room for 2^24 query rows")
+    T, B, most, hkv, d, page = torch.float16, 8, 2**18, 8, 64, 16
+    g = gen(51)
+    lens, starts = [20] * B, list(range(B + 1))
+    cache = make_cache(g, 2 * B, hkv, d, page, T)
+    tab = tables(g, lens, page, 2 * B)
+    q = torch.randn(B, hkv, d, generator=g).to(T)
+    got = run_attn(bq, dev, q, cache, tab, lens, hkv, page, starts, most)
+    check_attn(got, q, cache, tab, lens, starts, what="room")
