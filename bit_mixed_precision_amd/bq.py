@@ -693,11 +693,12 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
     pages = _cache_ptr(cache, kv_heads, dim, page_size, dev)
     starts = None
     if q_start is None:
-        if batch == 0 or total % batch:
+        if total % batch if batch else total:
             raise ValueError("without q_start every sequence has total_q / batch queries")
-        if max_q_len is not None and max_q_len != total // batch:
+        each = total // batch if batch else 0
+        if max_q_len is not None and max_q_len != each:
             raise ValueError("max_q_len must be total_q / batch without q_start")
-        max_q_len = total // batch
+        max_q_len = each
     else:
         if max_q_len is None:
             raise ValueError("q_start needs max_q_len")

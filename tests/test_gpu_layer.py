@@ -935,3 +935,33 @@ def test_attn_kv4_room_for_many_queries(bq, dev):
     q = torch.randn(B, hkv, d, generator=g).to(T)
     got = run_attn(bq, dev, q, cache, tab, lens, hkv, page, starts, most)
     check_attn(got, q, cache, tab, lens, starts, what="room")
+
+
+@pytest.mark.parametrize("T", TYPES)
+def test_layer_empty_calls(bq, dev, T):
+    """A batch of no sequences, sequences of no queries, no tokens: empty
+    results, nothing launched, nothing written."""
+    banner(f"empty calls {T}")
+    hq, hkv, d, page = 4, 2, 128, 16
+    cache = torch.full((3, bq.kv4_page_bytes(hkv, d, page)), 0xA5, dtype=torch.uint8, device=dev)
+    q = torch.empty(0, hq, d, dtype=T, device=dev)
+    k = torch.empty(0, hkv, d, dtype=T, device=dev)
+    ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    for batch in (0, 2):
+        out, lse = bq.attn_kv4(q, cache, ints(batch, 3), ints(batch), page, hkv, return_lse=True)
+        assert out.shape == q.shape and lse.shape == (0, hq)
+        out = bq.attn_kv4(q, cache, ints(batch, 3), ints(batch), page, hkv, q_start=ints(batch + 1), max_q_len=4)
+        assert out.shape == q.shape
+    with pytest.raises(ValueError):
+        bq.attn_kv4(torch.empty(1, hq, d, dtype=T, device=dev), cache, ints(0, 3), ints(0), page, hkv)
+    assert bq.qk_norm_rope_kv4(q, k, k, None, None, None, cache, torch.empty(0, dtype=torch.int64, device=dev), page).shape == q.shape
+    a, b = bq.qk_norm_rope(q, k, None, None, None)
+    assert a.shape == q.shape and b.shape == k.shape
+    a, b = bq.kv4_read(cache, torch.empty(0, dtype=torch.int64, device=dev), page, hkv, d, T)
+    assert a.shape == k.shape and b.shape == k.shape
+    w = torch.zeros(8, 64, dtype=torch.uint8, device=dev)
+    s = torch.ones(8, 1, dtype=torch.float16, device=dev)
+    assert bq.gemm_w4g_a16(torch.empty(0, 128, dtype=T, device=dev), w, s).shape == (0, 8)
+    assert bq.gemm_w4g_a16(torch.zeros(3, 128, dtype=T, device=dev), w[:0], s[:0]).shape == (3, 0)
+    torch.cuda.synchronize()
+    assert (cache == 0xA5).all()
