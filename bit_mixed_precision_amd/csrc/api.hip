@@ -13,7 +13,7 @@
 #include <mutex>
 
 #include "../../include/bq.h"
-#include "bq_internal.h"
+#include "bq_layer_internal.h"
 
 namespace {
 

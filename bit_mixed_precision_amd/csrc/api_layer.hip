@@ -4,7 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/bq_layer.h"
-#include "bq_internal.h"
+#include "bq_layer_internal.h"
 
 namespace {
 

@@ -34,7 +34,7 @@
 // Long sequences are split over workgroups (and over a workgroup's
 // wavefronts, joined through LDS); a second kernel joins the parts in order.
 #include "attn_rows.h"
-#include "bq_internal.h"
+#include "bq_layer_internal.h"
 #include "dtype16.h"
 
 namespace bq {

@@ -10,7 +10,7 @@
 //    instructions, K in parts over workgroups where tiles are few.
 // The first two keep scale and zero point outside the sums:
 //   sum_g s_g (sum_k a u - (8 + z_g) sum_k a).
-#include "bq_internal.h"
+#include "bq_layer_internal.h"
 #include "dtype16.h"
 #include "lds_dma.h"
 

@@ -16,7 +16,7 @@
 // the fp32 rate on this chip): a code turns over at a border between two
 // values, and with 53 bits the rounded key, hence the code, is the
 // definition's.  Queries (and keys without a cache) take fp32.
-#include "bq_internal.h"
+#include "bq_layer_internal.h"
 #include "dtype16.h"
 
 namespace bq {

@@ -84,3 +84,10 @@ def test_trace_durations_pairs_labels_with_bench_dispatches(tmp_path):
         b.trace_durations(str(p), ["quantize_rows", "gemm_w4a8_m1"])
     st = b.stats([1.0, 2.0, 3.0, 4.0, 100.0])
     assert st["us"] == 3.0 and st["n"] == 5 and st["us_min"] == 1.0
+
+
+def test_traffic_summary_is_of_these_sources():
+    """The committed summary was taken from the tiled GEMM as it stands, so
+    the bench reports its bytes."""
+    got = _bench().measured_traffic()
+    assert isinstance(got, int) and got >= 4096 * 4096 + 4096 * 2048 + 2 * 4096 + 2 * 4096 * 4096
