@@ -45,6 +45,80 @@ def quantize_w4g(w, group, zero=True):
     return (c[:, 0::2] | (c[:, 1::2] << 4)).to(torch.uint8), s.half(), None if z is None else z.half()
 
 
+def round_once(x, dtype):
+    """float64 -> dtype (as float64) in one rounding, ties to even; no overflow."""
+    bits, least = (11, -24) if dtype == torch.float16 else (8, -133)
+    step = torch.ldexp(torch.ones_like(x), (torch.frexp(x)[1] - bits).clamp(min=least))
+    return (x / step).round() * step
+
+
+def w4g_bound(A, Bp, scale, zero, group):
+    """The product S [M, N] and the bound of an output of A's type, for A whose
+    rows are independent of the weights (random signs: partial sums stay within
+    seven times the root of their terms' squares, or the terms' sum if smaller).
+
+    u = 2^-23 is a whole step of fp32 below the largest of what an addition
+    takes in: 32 products and the accumulator, 34 of them with the result, per
+    matrix step of 32 k; all errors of one output are added up.
+
+    M <= 16: the weights are exact.  Steps sum a (c + b) and a by themselves and
+    in groups, b = 8 (fp16) or 136 (bf16); what a step takes in is at most a
+    code's alignment times |a| (bf16: 144; fp16 codes are subnormal and aligned
+    as 2^-14: 64, times 2 for the product's own carry, in matrix steps, and
+    1024 in the dot products of M = 1, which a lane takes 32 at a time) or the
+    group's sum so far.  The group's end and the sum over groups: eight
+    roundings of both parts, and one a group, and 16 in joins, of the sum.
+
+    M > 16: S is of the weights rounded once to A's type, each step takes in
+    products and the sum so far.  (c - z) s is formed in fp32, with one rounding
+    (c s and z s are exact in it), on its way to the type, or with none where the
+    multiply-add rounds to the type itself: the two differ only where fp32 rounds
+    onto a tie, and the bound takes in their difference there.
+    """
+    M, K = A.shape
+    u, e = 2.0 ** -23, torch.finfo(A.dtype).eps / 2
+    bf16 = A.dtype == torch.bfloat16
+    a, W = A.to(F64), weights_w4g(Bp, scale, zero, group)
+    floor = 0.0 if bf16 else 2.0 ** -25  # half a step of fp16 subnormals
+    either = 0.0
+    if M > 16:
+        twice = W.to(torch.float32).to(A.dtype).to(F64)
+        W = round_once(W, A.dtype)
+        if not torch.equal(W, twice):
+            either = a.abs() @ (W - twice).abs().t()
+    S = a @ W.t()
+    sums = torch.minimum(7 * ((a * a) @ (W * W).t()).sqrt(), a.abs() @ W.abs().t())
+    if M > 16:
+        term = a.abs().amax(1, keepdim=True) * W.abs().amax(1)
+        return S, e * S.abs() * (1 + 2.0 ** -10) + u * (34 * (K // 32) * torch.maximum(term, sums) + 20 * sums) + floor + either
+    n, blocks, per = Bp.shape[0], K // 32, group // 32
+    s = scale.to(F64).repeat_interleave(per, 1)                                       # [N, blocks]
+    z = torch.zeros_like(s) if zero is None else zero.to(F64).repeat_interleave(per, 1)
+    b = 136.0 if bf16 else 8.0
+    codes = weights_w4g(Bp, torch.ones_like(scale), None, group) + b
+    x = a.view(M, blocks, 32)
+    part = torch.einsum("mbk,nbk->mnb", x, codes.view(n, blocks, 32))                 # a step's own sums
+    ones = x.sum(2)
+
+    def running(t):  # sums of a group at each of its steps
+        return t.unflatten(-1, (blocks // per, per)).cumsum(-1).flatten(-2)
+
+    def taken(first, t):  # the most that a step takes in: terms, the sum before, the sum after
+        r = running(t)
+        return torch.maximum(torch.maximum(first, r.abs()), (r - t).abs())
+
+    if M == 1:
+        size = x.abs().sum(2)
+        top = torch.maximum(size * (144.0 if bf16 else 15.0), x.abs().amax(2) * (0.0 if bf16 else 1024.0))
+    else:
+        size = x.abs().amax(2)
+        top = size * (144.0 if bf16 else 128.0)
+    step = taken(top[:, None], part) + taken(size, ones)[:, None] * (b + z.abs())
+    ends = running(part).abs() + running(ones).abs()[:, None] * (b + z.abs())
+    err = 34 * (step * s).sum(2) + 8 * (ends * s)[..., per - 1:: per].sum(2) + (K // group + 16) * sums
+    return S, e * S.abs() * (1 + 2.0 ** -10) + u * err + floor
+
+
 # ---- norm and rotation ----
 
 def norm_rope(x, w, eps, cos, sin, pos, interleaved):

@@ -28,6 +28,7 @@ import pytest
 import torch
 
 from gpu_util import banner, need_gpu
+from layer_cases import W4G_ALL, W4G_LARGE, W4G_TALL, w4g_inputs, w4g_windows
 from oracle import layer
 
 pytestmark = pytest.mark.gpu
@@ -965,3 +966,91 @@ def test_layer_empty_calls(bq, dev, T):
     assert bq.gemm_w4g_a16(torch.zeros(3, 128, dtype=T, device=dev), w[:0], s[:0]).shape == (3, 0)
     torch.cuda.synchronize()
     assert (cache == 0xA5).all()
+
+
+# ---------------------------------------------------------------- w4g, to the sums' own bound
+
+def run_w4g(bq, dev, A, B, s, z, **kw):
+    return bq.gemm_w4g_a16(A.to(dev), B.to(dev), s.to(dev), None if z is None else z.to(dev), **kw)
+
+
+@pytest.mark.parametrize("shape", W4G_ALL)
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("zero", [False, True])
+def test_w4g_closely(bq, dev, shape, T, zero):
+    """Every kernel and tile to oracle.layer.w4g_bound, which notices a lost
+    step of K or another group's scale; twice the same bits; and without a
+    workspace."""
+    M, N, K, group = shape
+    banner(f"w4g closely M={M} N={N} K={K} group={group} zero={zero} {T}")
+    A, B, s, z = w4g_inputs(M, N, K, group, zero, T)
+    S, tol = layer.w4g_bound(A, B, s, z, group)
+    out = run_w4g(bq, dev, A, B, s, z)
+    torch.cuda.synchronize()
+    within(out, S, tol, f"w4g {shape} {T}")
+    again = run_w4g(bq, dev, A, B, s, z)
+    alone = run_w4g(bq, dev, A, B, s, z, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+    within(alone, S, tol, f"w4g {shape} {T} without a workspace")
+
+
+@pytest.mark.parametrize("shape", W4G_ALL)
+@pytest.mark.parametrize("T", TYPES)
+def test_w4g_windows(bq, dev, shape, T):
+    """Rows of A that are zero but for 32 k, the first and the last among them:
+    the codes, scales and zero points of exactly those."""
+    M, N, K, group = shape
+    banner(f"w4g windows M={M} N={N} K={K} group={group} {T}")
+    _, B, s, z = w4g_inputs(M, N, K, group, True, T)
+    for A, _ in w4g_windows(M, K, T):
+        S, tol = layer.w4g_bound(A, B, s, z, group)
+        out = run_w4g(bq, dev, A, B, s, z)
+        torch.cuda.synchronize()
+        within(out, S, tol, f"w4g windows {shape} {T}")
+
+
+@pytest.mark.parametrize("shape", W4G_LARGE + W4G_TALL)
+def test_w4g_large_tiles_write_their_outputs_only(bq, dev, shape):
+    """Ragged edges of the large tiles: nothing before or behind the output."""
+    M, N, K, group = shape
+    banner(f"w4g large tiles' edges M={M} N={N} K={K}")
+    A, B, s, z = w4g_inputs(M, N, K, group, True, torch.float16)
+    whole = torch.full((M * N + 512,), 7.0, dtype=torch.float16, device=dev)
+    out = whole[256: 256 + M * N].view(M, N)
+    run_w4g(bq, dev, A, B, s, z, out=out)
+    torch.cuda.synchronize()
+    assert (whole[:256] == 7.0).all() and (whole[256 + M * N:] == 7.0).all()
+    S, tol = layer.w4g_bound(A, B, s, z, group)
+    within(out, S, tol, f"w4g {shape}")
+
+
+# ---------------------------------------------------------------- attention: splits of two row tiles, and of ragged queries
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("ws", ["auto", "none", "full"])
+@pytest.mark.parametrize("lens,ql,hq,hkv,d,page,window", [([1300], 20, 2, 2, 64, 16, 0), ([1100, 70, 1537], 9, 4, 1, 64, 32, 0),
+                                                          ([2100, 3], 17, 2, 2, 64, 64, 1500), ([1400, 1200], 40, 2, 2, 128, 16, 0)])
+def test_attn_kv4_split_row_tiles(bq, dev, T, ws, lens, ql, hq, hkv, d, page, window):
+    """More than 16 query rows a kv head over sequences that are split."""
+    banner(f"attn: split, two row tiles {lens} {ql} {d} {window} {T} {ws}")
+    test_attn_kv4(bq, dev, (lens, ql, hq, hkv, d, page, window), T, ws)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("d,hkv", [(64, 1), (128, 2), (256, 1)])
+@pytest.mark.parametrize("window", [0, 1100])
+def test_attn_kv4_split_ragged_queries(bq, dev, T, d, hkv, window):
+    """q_start over sequences that are split: of 0, 1, 13 and 3 queries, one
+    of more queries than keys, rows behind the last left as they were."""
+    banner(f"attn: split, ragged queries d={d} {window} {T}")
+    lens, starts, hq, page = [1500, 1203, 1300, 0, 5, 40], [0, 1, 1, 14, 17, 26, 29], 4, 32
+    g = gen(61)
+    pages = sum(-(-n // page) for n in lens)
+    cache = make_cache(g, pages, hkv, d, page, T)
+    tab = tables(g, lens, page, pages)
+    rows = torch.randn(33, hq + 2, d, generator=g).to(T)
+    x = rows.to(dev)
+    for ws in ("auto", "none"):
+        got = run_attn(bq, dev, rows[:, :hq], cache, tab, lens, hkv, page, starts, 13, window=window, ws=ws, q_dev=x[:, :hq])
+        check_attn(got, rows[:, :hq], cache, tab, lens, starts, window, what="split, ragged")
