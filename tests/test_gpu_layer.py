@@ -1054,3 +1054,32 @@ def test_attn_kv4_split_ragged_queries(bq, dev, T, d, hkv, window):
     for ws in ("auto", "none"):
         got = run_attn(bq, dev, rows[:, :hq], cache, tab, lens, hkv, page, starts, 13, window=window, ws=ws, q_dev=x[:, :hq])
         check_attn(got, rows[:, :hq], cache, tab, lens, starts, window, what="split, ragged")
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attn_kv4_large_scales_and_rising_scores(bq, dev, T, sign):
+    """V scales of about 2000, of either sign, and scores that rise along the
+    sequence by just less than what raises the reference maximum (2^7.5 of
+    2^8): p times the scale stays within fp16's range."""
+    banner(f"attn: rising scores over large V scales of sign {sign} {T}")
+    n, hq, hkv, d, page = 700, 2, 1, 64, 16
+    g = gen(44)
+    cache = make_cache(g, 44, hkv, d, page, T, v_mul=6000.0)
+    tab = torch.arange(44, dtype=torch.int32)[None]
+    for t in range(n):
+        _, _, ak, av = cache._places(t % page)
+        rise = 7.5 * math.log(2) * (t >= 256)  # of the score: 1/8 per unit of q's sum, which is 8
+        cache.bytes[t // page][:, ak] = torch.tensor([0.0, rise]).half().view(torch.uint8)
+        if sign < 0:
+            cache.bytes[t // page][:, av[1]] ^= 128
+    q = torch.full((1, hq, d), 0.125).to(T)
+    out, lse = run_attn(bq, dev, q, cache, tab, [n], hkv, page)
+    want, wlse, size, delta = layer.attention(q, cache, tab, [n], [0, 1], d ** -0.5)
+    if sign < 0:  # the terms' magnitudes: |scale|
+        for t in range(n):
+            cache.bytes[t // page][:, cache._places(t % page)[3][1]] &= 127
+        _, _, size, delta = layer.attention(q, cache, tab, [n], [0, 1], d ** -0.5)
+    r = (2.0 ** -20 if T == torch.float16 else 2.0 ** -10 + 2.0 ** -20) + n * U
+    within(out, want, half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25, "rising")
+    assert ((lse.cpu().to(F64) - wlse).abs() <= delta + 2.0 ** -20 * (1 + wlse.abs())).all()
