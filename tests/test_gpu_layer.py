@@ -1083,3 +1083,42 @@ def test_attn_kv4_large_scales_and_rising_scores(bq, dev, T, sign):
     r = (2.0 ** -20 if T == torch.float16 else 2.0 ** -10 + 2.0 ** -20) + n * U
     within(out, want, half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25, "rising")
     assert ((lse.cpu().to(F64) - wlse).abs() <= delta + 2.0 ** -20 * (1 + wlse.abs())).all()
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("c", [(40, 4, 2, 128, 16), (2600, 8, 8, 64, 32), (33, 0, 3, 256, 64)])
+def test_qk_norm_rope_kv4_positions_outside_the_table(bq, dev, T, c):
+    """A token left out for its position writes neither its query nor the
+    cache; slots at the ends of 64 bits are not followed; the others are
+    written as alone."""
+    banner(f"cache, positions outside the table {c} {T}")
+    tokens, hq, hkv, d, page = c
+    g = gen(71 + tokens)
+    rows = (torch.randn(tokens, hq + 2 * hkv, d, generator=g) * 2).to(T)
+    cos, sin = table(64, d)
+    pos = torch.randint(0, 64, (tokens,), generator=g, dtype=torch.int32)
+    slots = torch.randperm(tokens + 9, generator=g)[:tokens].contiguous()
+    bad = {1: -1, 2: 64, 5: 2**31 - 1, 30: -(2**31)}
+    for t, p in bad.items():
+        pos[t] = p
+    slots[3], slots[7], slots[20] = 2**63 - 1, -(2**63), 1 << 40
+    pages = -(-(tokens + 9) // page)
+    out = []
+    for keep in (None, [t for t in range(tokens) if t not in bad and t not in (3, 7, 20)]):
+        x, p, s = (rows, pos, slots) if keep is None else (rows[keep], pos[keep], slots[keep])
+        x = x.to(dev)
+        cache = torch.full((pages, bq.kv4_page_bytes(hkv, d, page)), 0xA5, dtype=torch.uint8, device=dev)
+        q = torch.full((x.shape[0], hq, d), 7.0, dtype=T, device=dev) if hq else None
+        bq.qk_norm_rope_kv4(x[:, :hq] if hq else None, x[:, hq: hq + hkv], x[:, hq + hkv:], cos.to(dev), sin.to(dev), p.to(dev),
+                            cache, s.to(dev), page, q_out=q)
+        torch.cuda.synchronize()
+        out.append((cache, q))
+    assert torch.equal(out[0][0], out[1][0])
+    if hq:
+        assert torch.equal(out[0][1][keep], out[1][1])
+        assert (out[0][1][list(bad)] == 7.0).all()
+        assert (out[0][1][[3, 7, 20]] != 7.0).any(-1).all()  # their queries are written
+    k, v = bq.kv4_read(out[0][0], torch.tensor([2**63 - 1, -(2**63), -1, 1 << 40], device=dev), page, hkv, d, T,
+                       *(torch.full((4, hkv, d), 7.0, dtype=T, device=dev) for _ in range(2)))
+    torch.cuda.synchronize()
+    assert (k == 7.0).all() and (v == 7.0).all()
