@@ -26,7 +26,8 @@
 //
 // p sv is split in two fp16 values (high part and remainder) for an fp16
 // output: one rounding of it alone would weigh as much as the output's own;
-// with a bf16 output the high part is enough.
+// with a bf16 output the high part, three bits more than the output has, is
+// enough (its error against 64 bits grows by under 1 %).
 // The reference maximum is raised only when a score passes it by 2^8, and
 // then for all lanes of the row; sums and accumulators are fp32.  p sv is
 // brought into fp16's range by the largest V scale that the row has seen.
@@ -714,11 +715,13 @@ AttnKv4Plan attn_kv4_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_
     // 1536, 89 with 576).
     const int64_t slots = 256 * (D == 256 || (D == 128 && rt == 2) ? 2 : D == 64 && rt == 1 ? 4 : 3);
     // Up to 1024 keys are not split: the second kernel costs what the shorter
-    // first one gains (8 kv heads of 128: 1 sequence of 700 keys 9.0 us against
-    // 10.2 in four, of 1024 10.2 against 9.3 in eight, of 1500 13.5 against 10.5),
-    // and a caller its launch.  Where eight wavefronts a workgroup fill half of
-    // the CUs, up to 2048 keys (16 sequences of 2048 18.1 us either way, 32 20.7
-    // against 25.6; 16 of 4096 33.1 against 26.7).
+    // first one gains, or nearly, and its launch costs a caller more (8 kv heads
+    // of 128, in a graph: 1 sequence of 700 keys 8.9 us, split 9.1, of 1024 9.9
+    // and 9.0, 8 of 1024 11.4 and 12.3; called from Python 9.2 and 12.1, 10.1 and
+    // 12.2, 11.2 and 12.2; of 1500 in a graph 13.5 and 10.5).  Where eight
+    // wavefronts a workgroup fill half of the CUs, up to 2048 keys (16 sequences
+    // of 2048 18.1 us either way, 32 20.7 against 25.6; 16 of 4096 33.1 against
+    // 26.7).
     const int64_t whole = many_waves(D, rt, items) && items >= 128 ? 2048 : 1024;
     const int64_t step = kTile * kWaves;
     const int64_t want = items > 0 && max_len > whole ? slots / items : 1, most = (max_len + step - 1) / step;

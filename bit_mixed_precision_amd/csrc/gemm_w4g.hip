@@ -7,7 +7,11 @@
 //  * skinny (M <= 16): matrix instructions on the bare codes, K split over a
 //    workgroup's wavefronts;
 //  * tiled: the weights rounded once to T between LDS and the matrix
-//    instructions, K in parts over workgroups where tiles are few.
+//    instructions, K in parts over workgroups where tiles are few.  A choice:
+//    the rounding is as large as the output's own, so the error against 64 bits
+//    is 1.35 times it (bf16 2.3e-3 for 1.7e-3, fp16 2.8e-4 for 2.1e-4); bare
+//    codes would take the scale to every accumulator at the end of each group,
+//    32 to 128 k, in the issue slots that bound this kernel.
 // The first two keep scale and zero point outside the sums:
 //   sum_g s_g (sum_k a u - (8 + z_g) sum_k a).
 #include "bq_layer_internal.h"
@@ -18,8 +22,8 @@ namespace bq {
 namespace {
 
 // M up to which the skinny kernel is taken: 16 weight rows a workgroup and all
-// of A's (M = 16, N = K = 4096: 7.4 us, tiled 12.6; M = 20, N = 11008: 26.4,
-// tiled 13.6).
+// of A's (M = 16, N = K = 4096, fp16: 6.8 us, tiled 12.3; bf16 with zero points
+// 7.9, 17.2).
 constexpr int kSkinnyM = 16;
 
 constexpr uint32_t kFlip = 0x88888888u;  // two's complement nibble -> c + 8
@@ -661,12 +665,11 @@ template <typename T>
 hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale, const uint16_t *zero, int gshift,
                       uint16_t *C, int M, int N, int K, float *ws, int64_t wsBytes, hipStream_t s)
 {
-    // M = 1: a row of B a wavefront (N = K = 4096 5.1 us, the skinny kernel
-    // 5.6; N = 11008 9.4, 11.2).  Above, the skinny kernel with as many loads
-    // of A as it has rows; with few tiles of N the wavefronts share them out
-    // further and hold more in flight (M = 4, N = 4096, K = 4096: eight
-    // wavefronts, four steps 5.9 us, four wavefronts 6.6; N = 11008: 16.5,
-    // 14.1).
+    // M = 1: a row of B a wavefront (fp16, K = 4096: N = 4096 5.2 us, the skinny
+    // kernel 5.6; N = 11008 9.6, 10.9).  Above, the skinny kernel with as many
+    // loads of A as it has rows; with few tiles of N the wavefronts share them
+    // out further and hold more in flight (M = 4, K = 4096, bf16 with zero
+    // points: N = 4096 eight wavefronts 6.7 us, four 7.8; N = 11008 16.3, 14.1).
     if (M == 1)
         return launch_gemv_t<T>(A, B, scale, zero, gshift, C, N, K, s);
     if (M <= 4)
@@ -678,8 +681,11 @@ hipError_t launch_any(const uint16_t *A, const uint8_t *B, const uint16_t *scale
         return launch_skinny_t<T, 4, 8, 1>(A, B, scale, zero, gshift, C, M, N, K, s);
     // Larger tiles move less, but there have to be enough of them (M = 2048, N =
     // K = 4096: 128 x 128 80 us, 128 x 64 106; M = 256, N = 11008, 172 tiles of
-    // 128 x 128: 46, 59, 64 x 64 58; M = 512, N = 4096, K = 11008, 128 tiles: 113,
-    // 78, 100; M = 200, N = K = 4096: 64 x 64 21.9, 128 x 64 in two parts 25.9).
+    // 128 x 128: 39, 53, 64 x 64 51; M = 512, N = 4096, K = 11008, 128 tiles: 113,
+    // 78, 100; M = 200, N = K = 4096: 64 x 64 21.9, 128 x 64 in two parts 25.9;
+    // M = 128, N = 28672: 49, 62, 78).  The rule does not ask how many of a tile's
+    // rows there are: from N = 20480 on it takes 128 x 128 for few rows too (M =
+    // 20, N = 28672: 42 us, 32 x 64 29; M = 64: 44, 64 x 64 41).
     if (tiles_of(M, N, 128, 128) >= 160)
         return launch_tiled_t<T, 128, 128, 2>(A, B, scale, zero, gshift, C, M, N, K, nullptr, 1, s);
     if (tiles_of(M, N, 128, 64) >= 256)

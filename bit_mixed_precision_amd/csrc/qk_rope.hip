@@ -10,7 +10,10 @@
 // wavefront covers 512 channels with one load instruction; the norm's sum and
 // the quantizer's range are butterfly reductions inside the row's lanes, and
 // a rotation pair in halves is a lane rot_dim/16 away.  Bound by moving the
-// rows (and by launch latency at decode sizes).
+// rows (and by launch latency at decode sizes); with a cache, by latency: 4097
+// tokens of 16 + 16 heads of 64 take 16.9 us, of which the VALU issues for 7,
+// in six wavefronts a SIMD.  Scattered slots write 19.4 MB there, neighbouring
+// ones 12.8, and take 0.8 us more.
 //
 // Keys that go to the cache are normalized and rotated in fp64 (fp64 runs at
 // the fp32 rate on this chip): a code turns over at a border between two
@@ -312,7 +315,10 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkRopeArgs
 // Eight channels a lane of K or V of one token: codes and parameters to the
 // 16-bit type, T(fp32(code * scale) + min): the product is exact.
 // Wavefronts are laid out as the writer's (4097 tokens, 16 heads of 64: 8.3 us
-// with rows of one token's heads, so 7.1).
+// with rows of one token's heads, so 7.4).  Bound by latency: a wavefront lives
+// for three accesses, each after the last (slot, codes and parameters, outputs),
+// and moves 1 KB; its VALU is busy 8 % of that time.  Neighbouring slots gain
+// little (7.2 us; 16388 tokens 28, scattered 30: 3 TB/s).
 template <typename T, int LPR>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(const uint8_t *cache, int64_t num_pages, int page_shift, int hkv,
                                                             const int64_t *slots, int64_t tokens, uint16_t *k, uint16_t *v)

@@ -65,7 +65,9 @@ enum bq_dtype {
  *              bq_gemm_w4g_workspace_bytes, for none (K is not split, the sums
  *              are taken in another order).  Calls that share one must not
  *              overlap.
- * M > 16 rounds each weight once to dtype; smaller M uses the exact weights.
+ * M > 16 rounds each weight once to dtype (in fp16, one past 65504 becomes
+ * infinite); smaller M uses the exact weights.  A row's low bits therefore
+ * depend on M, and on whether K is split.
  * 0 <= M, N <= BQ_MAX_DIM, M * N <= BQ_MAX_OUT, 0 <= K <= BQ_MAX_K, K a
  * multiple of 64 and of group (BQ_ERR_SHAPE); pointers 16-byte aligned.
  * K == 0 writes zeros.
@@ -87,7 +89,10 @@ int64_t bq_gemm_w4g_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *
  *   q, k          tokens x q_heads x head_dim and tokens x kv_heads x
  *                 head_dim, q_stride / k_stride elements between tokens
- *                 (at least a token's size, multiples of 8); finite values
+ *                 (at least a token's size, multiples of 8); finite values.
+ *                 With weights, bf16 values lie below 2^60 in magnitude, and
+ *                 mean(x^2) + eps above 2^-100: squares and the product with
+ *                 the weight are fp32
  *   q_weight, k_weight  [head_dim] of dtype; both or neither (BQ_ERR_NULL)
  *   cos, sin      [max_pos, rot_dim/2] fp32
  *   positions     [tokens] int32; a token whose position is outside
@@ -151,7 +156,8 @@ int bq_kv4_read(const void *cache, int64_t num_pages, int page_size, int kv_head
  * p = seq_len - q_len + i.  q_heads / kv_heads query heads share a kv head.
  * A row with no keys gives zeros (lse -infinity).
  *
- *   q            total_q x q_heads x head_dim, q_stride between tokens
+ *   q            total_q x q_heads x head_dim, q_stride between tokens; bf16
+ *                values of magnitude below 2^100
  *   q_start      [batch + 1] int32, the first query of each sequence, then
  *                the end; each is taken within [0, total_q], and a sequence
  *                whose end is not past its start has none; NULL: max_q_len
@@ -176,7 +182,9 @@ int bq_kv4_read(const void *cache, int64_t num_pages, int page_size, int kv_head
  * a key's V scale is held in 22 bits for fp16 outputs and 11 for bf16, and to
  * 2^-29 of the row's largest p times the largest V scale that the row sees.
  * Keys that a row does not see change no bit of its result, whatever their
- * codes and parameters are.
+ * codes and parameters are.  Where sequences are split, the length of the
+ * parts follows from the call's sizes and its longest sequence, and with it the
+ * order of the sums: a sequence's low bits can differ between batches.
  * q_heads a multiple of kv_heads, max_blocks * page_size <= 2^30, total_q <=
  * 2^30 (BQ_ERR_SHAPE); softmax_scale finite, of any sign (BQ_ERR_ARG).
  */
