@@ -215,9 +215,9 @@ struct Wave {
     u4 q0[RT][kQ], q4[RT][kQ];
     // score = a1 (sk (16 s0 + s4) + b1 mk), in powers of two; a1 >= 0
     float a1[RT], b1[RT];
-    float mt[RT], mref[RT];  // reference maximum of score / a1, and what is subtracted: mt a1 - shift
+    float mt[RT], mref[RT];  // the scores' reference maximum, and what is subtracted of them: mt - shift
     float l[RT], z[RT];
-    float cap[RT];           // largest V scale (its size) that p sv 2^shift takes in fp16's range: 2^(6 - shift), or 0 (shift 0)
+    float cap[RT];           // V scales up to cap = 2^(6 - shift) leave p sv 2^shift within fp16; 0 at first, with shift 0
     int pos[RT];
     u4 ph[RT], pl[RT];       // p sv of the tile, high and low parts
     f4 o[RT][kMT];
