@@ -63,9 +63,21 @@ LAYER_SIGNATURES = {
                     _I64, _P],
     "bq_attn_kv4_workspace_bytes": [_I64, _I64, _I, _I, _I, _I64],
 }
+# the same for include/bq_decode.h
+DECODE_SIGNATURES = {
+    "bq_tree_mask": [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P],
+    "bq_attn_kv4_tree": [_P, _I64, _I, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _I, _I64, _P, _I64, _F32, _I64,
+                         _P, _P, _P, _I64, _P],
+    "bq_attn_kv4_tree_workspace_bytes": [_I64, _I64, _I, _I, _I, _I64],
+    "bq_sample": [_P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
+    "bq_sample_workspace_bytes": [_I64, _I64, _I],
+    "bq_tree_accept": [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P],
+    "bq_kv4_compact": [_P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _P],
+}
 _RESTYPES = {"bq_status_string": ctypes.c_char_p, "bq_gemm_splitk_workspace_bytes": ctypes.c_int64,
              "bq_gemm_w4g_workspace_bytes": ctypes.c_int64, "bq_kv4_page_bytes": ctypes.c_int64,
-             "bq_attn_kv4_workspace_bytes": ctypes.c_int64}
+             "bq_attn_kv4_workspace_bytes": ctypes.c_int64, "bq_attn_kv4_tree_workspace_bytes": ctypes.c_int64,
+             "bq_sample_workspace_bytes": ctypes.c_int64}
 
 
 class BQError(RuntimeError):
@@ -86,7 +98,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build the HIP library first "
                 "(python -c 'import __graft_entry__ as g; g.build()')")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, args in {**SIGNATURES, **LAYER_SIGNATURES}.items():
+        for name, args in {**SIGNATURES, **LAYER_SIGNATURES, **DECODE_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = _RESTYPES.get(name, ctypes.c_int)
@@ -679,6 +691,12 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
     lse fp32 [total_q, q_heads].  A row with no keys gives zeros (lse -inf).
     A workspace is allocated for the call when it needs one and none is
     given."""
+    return _attn(q, cache, block_table, seq_lens, page_size, kv_heads, None, scale, q_start, max_q_len, window, out, lse, return_lse,
+                 workspace)
+
+
+def _attn(q, cache, block_table, seq_lens, page_size, kv_heads, mask, scale, q_start, max_q_len, window, out, lse, return_lse,
+          workspace):
     dt = _dtype16(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be 3-D [total_q, q_heads, head_dim]")
@@ -707,7 +725,213 @@ def attn_kv4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, se
     e = None
     if lse is not None or return_lse:
         lse, e = _output(lse, "lse", torch.float32, (total, hq), dev)
-    ws, wp, wn = _workspace(workspace, attn_kv4_workspace_bytes(batch, max_q_len, hq, kv_heads, dim, blocks * page_size), dev)
-    _enqueue("bq_attn_kv4", dev, q.data_ptr(), qs, dt, starts, lens, tab, batch, total, max_q_len, hq, kv_heads, dim, pages,
-             cache.shape[0], page_size, blocks, dim ** -0.5 if scale is None else scale, window, o, e, wp, wn)
+    name, seen = "bq_attn_kv4", ()
+    if mask is not None:
+        name, seen = "bq_attn_kv4_tree", _tree_mask_ptr(mask, total, dev)
+    ws, wp, wn = _workspace(workspace, _host_bytes(name + "_workspace_bytes", batch, max_q_len, hq, kv_heads, dim,
+                                                   blocks * page_size), dev)
+    _enqueue(name, dev, q.data_ptr(), qs, dt, starts, lens, tab, batch, total, max_q_len, hq, kv_heads, dim, pages,
+             cache.shape[0], page_size, blocks, *seen, dim ** -0.5 if scale is None else scale, window, o, e, wp, wn)
     return out if lse is None else (out, lse)
+
+
+# --------------------------------------------------------------------------
+# decoding: sampling, and trees of drafted tokens (include/bq_decode.h)
+# --------------------------------------------------------------------------
+
+TREE_MAX = 1024
+
+
+def _tree_mask_ptr(mask, total, dev):
+    if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+        raise ValueError("tree_mask must be a 2-D tensor [total_q, words]")
+    return _dense(mask, "tree_mask", torch.int32, (total, mask.shape[1]), dev), mask.shape[1]
+
+
+def _tree_nodes(t: torch.Tensor, name: str, q_start: Optional[torch.Tensor], max_q_len: Optional[int]):
+    """(device, batch, total_q, max_q_len, address of q_start) of trees whose
+    nodes a tensor `t` lists: [batch, nodes], or [total_q] with q_start."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.device
+    if q_start is None:
+        if t.dim() != 2:
+            raise ValueError(f"{name} must be 2-D [batch, nodes] without q_start")
+        batch, each = t.shape
+        if max_q_len is not None and max_q_len != each:
+            raise ValueError("max_q_len must be the nodes of a tree without q_start")
+        return dev, batch, batch * each, each, None
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be 1-D [total_q] with q_start")
+    if max_q_len is None:
+        raise ValueError("q_start needs max_q_len")
+    starts = _dense(q_start, "q_start", torch.int32, None, dev)
+    if q_start.dim() != 1 or q_start.shape[0] < 1:
+        raise ValueError("q_start must be 1-D [batch + 1]")
+    return dev, q_start.shape[0] - 1, t.shape[0], max_q_len, starts
+
+
+def tree_mask(parents: torch.Tensor, seq_lens: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+              max_q_len: Optional[int] = None, mask: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None):
+    """What the nodes of drafted trees see, and their positions: parents int32
+    [batch, nodes] (or [total_q] with q_start int32 [batch + 1] and max_q_len),
+    each the number of an earlier node of the tree, -1 for a root -> (mask
+    int32 [total_q, ceil(max_q_len / 32)], positions int32 [total_q]).  Bit j %
+    32 of word j / 32 of a row: the node sees node j, itself or an ancestor of
+    its.  position = seq_len - q_len + depth with seq_lens int32 [batch], the
+    keys in the cache with the nodes, else the depth."""
+    dev, batch, total, most, starts = _tree_nodes(parents, "parents", q_start, max_q_len)
+    par = _dense(parents, "parents", torch.int32, None, dev)
+    lens = None if seq_lens is None else _dense(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    if mask is not None and mask.dim() != 2:
+        raise ValueError("mask must be 2-D [total_q, words]")
+    words = max(1, -(-most // 32)) if mask is None else mask.shape[1]
+    mask, m = _output(mask, "mask", torch.int32, (total, words), dev)
+    positions, at = _output(positions, "positions", torch.int32, (total,), dev)
+    _enqueue("bq_tree_mask", dev, par, starts, lens, batch, total, most, words, m, at)
+    return mask, positions
+
+
+def attn_kv4_tree_workspace_bytes(batch: int, max_q_len: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
+    """Device workspace bytes with which attn_kv4_tree splits sequences of up
+    to max_len keys (0: it does not)."""
+    return _host_bytes("bq_attn_kv4_tree_workspace_bytes", batch, max_q_len, q_heads, kv_heads, head_dim, max_len)
+
+
+def attn_kv4_tree(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int,
+                  kv_heads: int, tree_mask: torch.Tensor, scale: Optional[float] = None, q_start: Optional[torch.Tensor] = None,
+                  max_q_len: Optional[int] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """attn_kv4 for the nodes of drafted trees, the last keys of each cache:
+    a row attends to all keys before the tree and to the nodes of its row of
+    tree_mask int32 [total_q, words] (tree_mask() gives them; any bits are
+    allowed), with window > 0 to the last `window` of these.  The other
+    arguments and the results are attn_kv4's; at most 1024 nodes a sequence."""
+    if tree_mask is None:
+        raise ValueError("tree_mask is required")
+    return _attn(q, cache, block_table, seq_lens, page_size, kv_heads, tree_mask, scale, q_start, max_q_len, window, out, lse,
+                 return_lse, workspace)
+
+
+_LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def sample_workspace_bytes(rows: int, vocab: int, dtype: torch.dtype) -> int:
+    """Device workspace bytes with which sample shares rows between workgroups
+    (0: it does not)."""
+    if dtype not in _LOGITS:
+        raise ValueError("dtype must be float16, bfloat16 or float32")
+    return _host_bytes("bq_sample_workspace_bytes", rows, vocab, _LOGITS[dtype])
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+           tokens: Optional[torch.Tensor] = None, logprobs: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None):
+    """One token per row of logits [rows, vocab] (fp16, bf16 or fp32, dense
+    within a row) from the random numbers u fp32 [rows] in [0, 1) -> (tokens
+    int32 [rows], logprobs fp32 [rows], the log of the probability with which
+    each was drawn).
+
+    Each row's settings, fp32 [rows] (top_k int32), None for off: temperature
+    (not above 0: the first of the greatest logits), then of the tokens in
+    descending order, equal ones by index, the first top_k (if above 0), of
+    these the first whose predecessors' probabilities sum to less than top_p
+    (if below 1), and those of at least min_p of the greatest probability (if
+    above 0).  The token is where the kept probabilities, summed up in the order
+    of indices, pass u.  A row of -inf and NaN alone gives token -1.  A workspace
+    is allocated for the call when it needs one and none is given."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in _LOGITS:
+        raise ValueError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [rows, vocab]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
+    rows, vocab = logits.shape
+    stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits must be dense within a row")
+    dev = logits.device
+    pu = _dense(u, "u", torch.float32, (rows,), dev)
+    pt = None if temperature is None else _dense(temperature, "temperature", torch.float32, (rows,), dev)
+    pk = None if top_k is None else _dense(top_k, "top_k", torch.int32, (rows,), dev)
+    pp = None if top_p is None else _dense(top_p, "top_p", torch.float32, (rows,), dev)
+    pm = None if min_p is None else _dense(min_p, "min_p", torch.float32, (rows,), dev)
+    tokens, tok = _output(tokens, "tokens", torch.int32, (rows,), dev)
+    logprobs, lp = _output(logprobs, "logprobs", torch.float32, (rows,), dev)
+    kind = _LOGITS[logits.dtype]
+    ws, wp, wn = _workspace(workspace, _host_bytes("bq_sample_workspace_bytes", rows, vocab, kind), dev)
+    _enqueue("bq_sample", dev, logits.data_ptr(), stride if rows > 1 else vocab, kind, rows, vocab, pu, pt, pk, pp, pm, tok, lp,
+             wp, wn)
+    return tokens, logprobs
+
+
+def tree_accept(tokens: torch.Tensor, parents: torch.Tensor, sampled: torch.Tensor, q_start: Optional[torch.Tensor] = None,
+                max_q_len: Optional[int] = None, max_path: Optional[int] = None, path: Optional[torch.Tensor] = None,
+                count: Optional[torch.Tensor] = None, next_token: Optional[torch.Tensor] = None):
+    """The path of drafted tokens that the sampled ones agree with: tokens,
+    parents int32 [batch, nodes] (or [total_q] with q_start and max_q_len),
+    sampled int32, as many, the model's token at each node -> (path int32
+    [batch, max_path]: node 0, then node after node the first child whose token
+    was sampled at its parent, then -1; count int32 [batch]; next_token int32
+    [batch], what was sampled at the path's last node).  max_path None: the most
+    nodes of a tree."""
+    dev, batch, total, most, starts = _tree_nodes(tokens, "tokens", q_start, max_q_len)
+    tok = _dense(tokens, "tokens", torch.int32, None, dev)
+    par = _dense(parents, "parents", torch.int32, tokens.shape, dev)
+    if not isinstance(sampled, torch.Tensor):
+        raise TypeError("sampled must be a torch.Tensor")
+    drawn = _dense(sampled, "sampled", torch.int32, tokens.shape if sampled.dim() == tokens.dim() else (total,), dev)
+    if max_path is None:
+        max_path = max(1, most) if path is None else path.shape[-1]
+    path, pp = _output(path, "path", torch.int32, (batch, max_path), dev)
+    count, pc = _output(count, "count", torch.int32, (batch,), dev)
+    next_token, pn = _output(next_token, "next_token", torch.int32, (batch,), dev)
+    _enqueue("bq_tree_accept", dev, tok, par, drawn, starts, batch, total, most, max_path, pp, pc, pn)
+    return path, count, next_token
+
+
+def kv4_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, path: torch.Tensor, count: torch.Tensor,
+                page_size: int, kv_heads: int, head_dim: int, q_start: Optional[torch.Tensor] = None,
+                max_q_len: Optional[int] = None, total_q: Optional[int] = None) -> torch.Tensor:
+    """Moves the keys and values of the accepted nodes behind the prefix, for
+    all kv heads: key prefix + path[b, j] to prefix + j for the first count[b]
+    entries, prefix = seq_lens[b] (with the nodes) less the sequence's nodes:
+    max_q_len each, or by q_start int32 [batch + 1] over total_q nodes.  cache
+    [num_pages, page bytes], or [layers, num_pages, page bytes] for all layers
+    in one call (its layers may lie apart) -> cache, changed in place."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() not in (2, 3):
+        raise ValueError("cache must be a tensor [num_pages, page bytes] or [layers, num_pages, page bytes]")
+    dev = cache.device
+    layers, stride = 1, 0
+    if cache.dim() == 3:
+        layers, stride = cache.shape[0], cache.stride(0)
+    pages = cache.shape[-2]
+    if layers:
+        at = _cache_ptr(cache if cache.dim() == 2 else cache[0], kv_heads, head_dim, page_size, dev)
+    else:
+        at = cache.data_ptr()
+    if block_table.dim() != 2 or path.dim() != 2:
+        raise ValueError("block_table and path must be 2-D [batch, ...]")
+    batch, blocks = block_table.shape
+    tab = _dense(block_table, "block_table", torch.int32, None, dev)
+    lens = _dense(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    pp = _dense(path, "path", torch.int32, (batch, path.shape[1]), dev)
+    pc = _dense(count, "count", torch.int32, (batch,), dev)
+    starts = None
+    if q_start is None:
+        if max_q_len is None:
+            raise ValueError("kv4_compact needs max_q_len, or q_start and total_q")
+        if total_q is not None and total_q != batch * max_q_len:
+            raise ValueError("total_q must be batch * max_q_len without q_start")
+        total_q = batch * max_q_len
+    else:
+        if total_q is None:
+            raise ValueError("q_start needs total_q")
+        starts = _dense(q_start, "q_start", torch.int32, (batch + 1,), dev)
+        max_q_len = min(total_q, TREE_MAX) if max_q_len is None else max_q_len
+    _enqueue("bq_kv4_compact", dev, at, layers, stride, pages, page_size, kv_heads, head_dim, tab, blocks, starts, lens, batch,
+             total_q, max_q_len, pp, pc, path.shape[1])
+    return cache

@@ -1,8 +1,10 @@
-// C ABI of the decoder-layer operators (declared in include/bq_layer.h):
-// host-side validation, then the launchers.  Every check runs before
-// anything is enqueued.
+// C ABI of the decoder-layer operators (declared in include/bq_layer.h) and of
+// bq_attn_kv4_tree (include/bq_decode.h), which shares bq_attn_kv4's:
+// host-side validation, then the launchers.  Every check runs before anything
+// is enqueued.
 #include <hip/hip_runtime.h>
 
+#include "../../include/bq_decode.h"
 #include "../../include/bq_layer.h"
 #include "bq_layer_internal.h"
 
@@ -241,10 +243,12 @@ int64_t bq_attn_kv4_workspace_bytes(int64_t batch, int64_t max_q_len, int q_head
     return bq::attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, head_dim, max_len).part_rows * (head_dim + 2) * 4;
 }
 
-int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
-                const int32_t *block_table, int64_t batch, int64_t total_q, int64_t max_q_len, int q_heads, int kv_heads,
-                int head_dim, const void *cache, int64_t num_pages, int page_size, int64_t max_blocks, float softmax_scale,
-                int64_t window, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream)
+// bq_attn_kv4, and bq_attn_kv4_tree where the queries are a tree's nodes.
+static int attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
+                    const int32_t *block_table, int64_t batch, int64_t total_q, int64_t max_q_len, int q_heads, int kv_heads,
+                    int head_dim, const void *cache, int64_t num_pages, int page_size, int64_t max_blocks, bool tree,
+                    const uint32_t *mask, int64_t mask_words, float softmax_scale, int64_t window, void *out, float *lse,
+                    void *workspace, int64_t workspace_bytes, void *stream)
 {
     if ((dtype != BQ_F16 && dtype != BQ_BF16) || !__builtin_isfinite(softmax_scale))
         return BQ_ERR_ARG;
@@ -271,6 +275,10 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
     if (!aligned(out, 16) || !aligned(cache, 16) || !aligned(workspace, 16) || !aligned(q_start, 4) ||
         !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(lse, 4))
         return BQ_ERR_ALIGN;
+    if (tree && !mask)
+        return BQ_ERR_NULL;
+    if (!aligned(mask, 4))
+        return BQ_ERR_ALIGN;
     const int dev = bq::device_status();
     if (dev != BQ_OK)
         return dev;
@@ -294,12 +302,44 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
     a.window = (int)window;
     a.out = out;
     a.lse = lse;
+    a.tree_mask = mask;
+    a.mask_words = (int)mask_words;
     const bq::AttnKv4Plan plan = bq::attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, head_dim, max_len);
     a.row_tiles = (int)plan.row_tiles;
     a.nsplit = plan.part_rows > 0 && workspace && workspace_bytes >= plan.part_rows * (head_dim + 2) * 4 ? plan.nsplit : 1;
     a.part = (float *)workspace;
     a.part_ml = a.part + plan.part_rows * head_dim;
     return bq::launch_status(bq::launch_attn_kv4(a, head_dim, plan.rt, dtype == BQ_BF16, (hipStream_t)stream));
+}
+
+int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
+                const int32_t *block_table, int64_t batch, int64_t total_q, int64_t max_q_len, int q_heads, int kv_heads,
+                int head_dim, const void *cache, int64_t num_pages, int page_size, int64_t max_blocks, float softmax_scale,
+                int64_t window, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return attn_kv4(q, q_stride, dtype, q_start, seq_lens, block_table, batch, total_q, max_q_len, q_heads, kv_heads, head_dim,
+                    cache, num_pages, page_size, max_blocks, false, nullptr, 0, softmax_scale, window, out, lse, workspace,
+                    workspace_bytes, stream);
+}
+
+int64_t bq_attn_kv4_tree_workspace_bytes(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int head_dim,
+                                         int64_t max_len)
+{
+    return max_q_len > BQ_TREE_MAX ? -BQ_ERR_SHAPE
+                                   : bq_attn_kv4_workspace_bytes(batch, max_q_len, q_heads, kv_heads, head_dim, max_len);
+}
+
+int bq_attn_kv4_tree(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
+                     const int32_t *block_table, int64_t batch, int64_t total_q, int64_t max_q_len, int q_heads,
+                     int kv_heads, int head_dim, const void *cache, int64_t num_pages, int page_size, int64_t max_blocks,
+                     const uint32_t *mask, int64_t mask_words, float softmax_scale, int64_t window, void *out, float *lse,
+                     void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (mask_words < 1 || mask_words > BQ_TREE_MAX / 32 || max_q_len > BQ_TREE_MAX)
+        return BQ_ERR_SHAPE;
+    return attn_kv4(q, q_stride, dtype, q_start, seq_lens, block_table, batch, total_q, max_q_len, q_heads, kv_heads, head_dim,
+                    cache, num_pages, page_size, max_blocks, true, mask, mask_words, softmax_scale, window, out, lse,
+                    workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

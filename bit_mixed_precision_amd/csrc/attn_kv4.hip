@@ -66,8 +66,10 @@ __device__ __forceinline__ QueryRows query_rows(const AttnKv4Args &p, int b)
 
 // Rows `tile` * ROWS on of sequence b.  Every split takes `chunk` keys, the
 // same for all sequences: workgroups then last equally long, and the shorter
-// sequences' last splits are empty.
-template <int ROWS>
+// sequences' last splits are empty.  TREE: the queries are a tree's nodes, key
+// base + i for node i, and see all keys before base; pos_min is the last of
+// those that every row sees.
+template <int ROWS, bool TREE>
 __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
 {
     Rows r;
@@ -79,6 +81,10 @@ __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
     const int first = tile * ROWS / p.group, last = min(tile * ROWS + ROWS - 1, r.rows - 1) / p.group;
     r.pos_min = r.base + first;
     r.pos_max = r.base + last;
+    if constexpr (TREE) {
+        r.pos_min = r.base - 1;
+        r.pos_max = min(len, r.base + 32 * p.mask_words) - 1;
+    }
     r.lo = p.window > 0 ? max(0, r.pos_min - p.window + 1) & ~(kTile - 1) : 0;
     r.hi = max(r.pos_max + 1, r.lo);
     r.chunk = r.hi - r.lo;
@@ -90,8 +96,8 @@ __device__ __forceinline__ Rows rows_of(const AttnKv4Args &p, int b, int tile)
         for (int off = 32; off > 0; off >>= 1)
             most = max(most, __shfl_xor(most, off, 64));
         most = min(most, p.max_blocks << p.page_shift);
-        if (p.window > 0)  // keys of ROWS rows: their positions, the window, lo's alignment
-            most = min(most, p.window + (ROWS - 1) / p.group + 1 + kTile);
+        if (p.window > 0)  // keys of ROWS rows: their positions (or the nodes), the window, lo's alignment
+            most = min(most, p.window + (TREE ? 32 * p.mask_words : (ROWS - 1) / p.group + 1) + kTile);
         constexpr int step = kTile * kWaves;
         r.chunk = __builtin_amdgcn_readfirstlane(((most + p.nsplit - 1) / p.nsplit + step - 1) / step * step);
     }
@@ -112,6 +118,75 @@ struct Place {
     uint32_t in[2];          // first token in the page
     int lim[2];              // tokens at or past lim are not there
 };
+
+// What one row of a tree's mask says.
+struct TreeRow {
+    const uint32_t *words;
+    int low, high;    // its nodes are [low, high): those that are keys, and have a bit
+    int first;        // first key of the prefix that it sees
+    int nodes;        // nodes that it sees, with a window at most that many
+
+    __device__ __forceinline__ uint32_t word(int k) const
+    {
+        if (32 * k >= high || 32 * k + 32 <= low || k < 0)
+            return 0;
+        uint32_t w = words[k];
+        if (32 * k + 32 > high)
+            w &= ~0u >> (32 * k + 32 - high);
+        if (32 * k < low)
+            w &= ~0u << (low - 32 * k);
+        return w;
+    }
+    // The nodes of word k that lie in the window: the last `nodes` of the row's.
+    __device__ __forceinline__ uint32_t seen(int k) const
+    {
+        uint32_t w = word(k);
+        if (nodes < high - low) {
+            int left = nodes;
+            for (int i = (high - 1) >> 5; i > k; --i)
+                left -= __popc(word(i));
+            for (int over = __popc(w) - max(left, 0); over > 0; --over)
+                w &= w - 1;
+        }
+        return w;
+    }
+    // Bits of the keys t .. t + 31 that the row sees.
+    __device__ __forceinline__ uint32_t keys(int t, int base) const
+    {
+        const int at = t - base;  // node of key t
+        uint32_t on = 0;
+        if (at < 0) {
+            on = at > -32 ? ~0u >> (32 + at) : ~0u;
+            if (first > t)
+                on = first < t + 32 ? on & (~0u << (first - t)) : 0;
+            if (at > -32)
+                on |= seen(0) << -at;
+        } else {
+            on = seen(at >> 5) >> (at & 31);
+            if (at & 31)
+                on |= seen((at >> 5) + 1) << (32 - (at & 31));
+        }
+        return on;
+    }
+};
+
+__device__ __forceinline__ TreeRow tree_row(const AttnKv4Args &p, const Rows &r, int len, int qi)
+{
+    TreeRow x;
+    x.words = p.tree_mask + (int64_t)(r.q0 + qi) * p.mask_words;
+    x.low = max(-r.base, 0);
+    x.high = min(len, 32 * p.mask_words);
+    x.first = 0;
+    x.nodes = x.high;
+    if (p.window > 0) {
+        int n = 0;
+        for (int k = 0; 32 * k < x.high; ++k)
+            n += __popc(x.word(k));
+        x.nodes = min(n, p.window);
+        x.first = r.base - (p.window - x.nodes);
+    }
+    return x;
+}
 
 template <int N>
 __device__ __forceinline__ void load_dwords(uint32_t *dst, const uint8_t *src)
@@ -218,7 +293,7 @@ struct Wave {
     float mt[RT], mref[RT];  // the scores' reference maximum, and what is subtracted of them: mt - shift
     float l[RT], z[RT];
     float cap[RT];           // V scales up to cap = 2^(6 - shift) leave p sv 2^shift within fp16; 0 at first, with shift 0
-    int pos[RT];
+    int pos[RT];             // the rows' positions (or nodes)
     u4 ph[RT], pl[RT];       // p sv of the tile, high and low parts
     f4 o[RT][kMT];
 
@@ -301,8 +376,10 @@ struct Wave {
     }
 
     // p of a tile and its V parameters; masked if not every row sees every key.
+    // TREE: `sees` has a bit for each key of the tile and row.
+    template <bool TREE>
     __device__ __forceinline__ void values(const Tile<D> &x, float (&s)[RT][8], bool masked, int t, const int (&lim)[2],
-                                           int window, int lane)
+                                           int window, int lane, const uint32_t (&sees)[RT])
     {
         float sv[8], mv[8];
 #pragma unroll
@@ -322,7 +399,8 @@ struct Wave {
                 const bool number = __builtin_isfinite(mv[j]) && __builtin_isfinite(sv[j]);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const bool on = there && tok <= pos[r] && (window <= 0 || tok > pos[r] - window);
+                    const bool on = there && (TREE ? (sees[r] >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1
+                                                   : tok <= pos[r] && (window <= 0 || tok > pos[r] - window));
                     s[r][j] = on ? (number ? s[r][j] : __builtin_nanf("")) : -__builtin_inff();
                 }
                 sv[j] = there && number ? sv[j] : 0.0f;
@@ -444,7 +522,7 @@ struct Wave {
 };
 
 // WAVES: kWaves, or kMany where `many_waves` says so.
-template <typename T, int D, int RT, int WAVES>
+template <typename T, int D, int RT, int WAVES, bool TREE>
 __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args p)
 {
     constexpr int DH = D > 128 ? 128 : D;  // channels joined at a time
@@ -472,7 +550,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args 
         for (int k = 0; k < D / 32; ++k)
             load_dwords<4>(qw[i] + 4 * k, (const uint8_t *)(q + (lane >> 4) * (D / 4) + 8 * k));
     }
-    const Rows r = rows_of<ROWS>(p, b, tile);
+    const Rows r = rows_of<ROWS, TREE>(p, b, tile);
     const int start = r.lo + split * r.chunk, end = min(start + r.chunk, r.hi);
     if (split > 0 && start >= r.hi)
         return;
@@ -481,7 +559,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args 
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int row = tile * ROWS + 16 * i + (lane & 15);
-        w.pos[i] = row < r.rows ? r.base + row / p.group : r.pos_max;
+        w.pos[i] = TREE ? min(row, r.rows - 1) / p.group : row < r.rows ? r.base + row / p.group : r.pos_max;
         w.init_row(i, qw[i], p.scale);
     }
     const int *table = p.block_table + (int64_t)b * p.max_blocks;
@@ -514,7 +592,13 @@ __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args 
                 load_pages(pages, p, table, min(u + kStep, end - 1), end);
             }
             const bool whole = t + kTile <= min(min(lim[0], lim[1]), r.pos_min + 1) && (p.window <= 0 || t > r.pos_max - p.window);
-            w.values(v, s, !whole, t, lim, p.window, lane);
+            uint32_t sees[RT] = {};
+            if constexpr (TREE)
+                if (!whole)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        sees[i] = tree_row(p, r, qr.len, w.pos[i]).keys(t, r.base);
+            w.template values<TREE>(v, s, !whole, t, lim, p.window, lane, sees);
             w.products(v, bias);
             if (u >= end)
                 break;
@@ -596,7 +680,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_kv4_kernel(const AttnKv4Args 
 }
 
 // Joins the splits of one query row: D/4 threads a split, blockDim.x of them.
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, bool TREE>
 __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
 {
     constexpr int TPS = D / 4, ROWS = 16 * RT;
@@ -605,7 +689,7 @@ __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
     const int tile = item % p.row_tiles;
     const int head = item / p.row_tiles % p.hkv;
     const int b = item / p.row_tiles / p.hkv;
-    const Rows r = rows_of<ROWS>(p, b, tile);
+    const Rows r = rows_of<ROWS, TREE>(p, b, tile);
     const int row = tile * ROWS + jr;
     if (row >= r.rows)
         return;
@@ -664,7 +748,7 @@ __global__ __launch_bounds__(256) void attn_kv4_join(const AttnKv4Args p)
 // against 6.4, 700 keys 14.0 against 13.4).
 bool many_waves(int D, int rt, int64_t items) { return D * rt <= 128 && items <= 256; }
 
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, bool TREE>
 hipError_t launch_t(const AttnKv4Args &p, hipStream_t s)
 {
     const int64_t items = (int64_t)p.batch * p.hkv * p.row_tiles;
@@ -672,28 +756,28 @@ hipError_t launch_t(const AttnKv4Args &p, hipStream_t s)
         return kGridTooLarge;
     if constexpr (D * RT <= 128)
         if (p.nsplit == 1 && many_waves(D, RT, items)) {
-            attn_kv4_kernel<T, D, RT, kMany><<<dim3((unsigned)items), 64 * kMany, 0, s>>>(p);
+            attn_kv4_kernel<T, D, RT, kMany, TREE><<<dim3((unsigned)items), 64 * kMany, 0, s>>>(p);
             return hipGetLastError();
         }
-    attn_kv4_kernel<T, D, RT, kWaves><<<dim3((unsigned)(items * p.nsplit)), 64 * kWaves, 0, s>>>(p);
+    attn_kv4_kernel<T, D, RT, kWaves, TREE><<<dim3((unsigned)(items * p.nsplit)), 64 * kWaves, 0, s>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.nsplit == 1)
         return e;
     int groups = 1;  // splits joined side by side: whole wavefronts, up to 256 threads
     while (groups * (D / 4) < 256 && (groups < p.nsplit || groups * (D / 4) < 64))
         groups *= 2;
-    attn_kv4_join<T, D, RT><<<dim3((unsigned)(items * p.join_rows)), groups * (D / 4), 0, s>>>(p);
+    attn_kv4_join<T, D, RT, TREE><<<dim3((unsigned)(items * p.join_rows)), groups * (D / 4), 0, s>>>(p);
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool TREE>
 hipError_t launch_d(const AttnKv4Args &p, int D, int rt, hipStream_t s)
 {
     if (D == 64)
-        return rt == 2 ? launch_t<T, 64, 2>(p, s) : launch_t<T, 64, 1>(p, s);
+        return rt == 2 ? launch_t<T, 64, 2, TREE>(p, s) : launch_t<T, 64, 1, TREE>(p, s);
     if (D == 128)
-        return rt == 2 ? launch_t<T, 128, 2>(p, s) : launch_t<T, 128, 1>(p, s);
-    return launch_t<T, 256, 1>(p, s);
+        return rt == 2 ? launch_t<T, 128, 2, TREE>(p, s) : launch_t<T, 128, 1, TREE>(p, s);
+    return launch_t<T, 256, 1, TREE>(p, s);
 }
 
 }  // namespace
@@ -735,7 +819,9 @@ hipError_t launch_attn_kv4(AttnKv4Args &p, int D, int rt, bool bf16, hipStream_t
 {
     const int64_t rows = (int64_t)p.max_q_len * p.group;
     p.join_rows = (int)(rows < 16 * rt ? rows : 16 * rt);
-    return bf16 ? launch_d<BF16>(p, D, rt, s) : launch_d<F16>(p, D, rt, s);
+    if (p.tree_mask)
+        return bf16 ? launch_d<BF16, true>(p, D, rt, s) : launch_d<F16, true>(p, D, rt, s);
+    return bf16 ? launch_d<BF16, false>(p, D, rt, s) : launch_d<F16, false>(p, D, rt, s);
 }
 
 }  // namespace bq

@@ -51,6 +51,8 @@ struct AttnKv4Args {
     float *lse;
     int row_tiles, nsplit, join_rows;
     float *part, *part_ml;
+    const uint32_t *tree_mask;  // or nullptr: causal
+    int mask_words;
 };
 // How a call is split: rt tiles of 16 query rows a workgroup, row_tiles
 // workgroups per sequence and kv head, times nsplit parts of the keys, whose

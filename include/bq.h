@@ -383,7 +383,9 @@ int bq_gemm_select_path(int64_t M, int64_t N, int64_t K, int bits);
 }
 #endif
 
-/* The operators of a low-bit decoder layer around these products. */
+/* The operators of a low-bit decoder layer around these products, and of
+ * decoding. */
 #include "bq_layer.h"
+#include "bq_decode.h"
 
 #endif /* BQ_H */
