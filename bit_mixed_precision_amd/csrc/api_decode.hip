@@ -155,8 +155,8 @@ int bq_sample(const void *logits, int64_t row_stride, int dtype, int64_t rows, i
     a.row_stride = row_stride;
     a.rows = (int)rows;
     a.vocab = (int)vocab;
-    a.frac = 61;  // sums of vocab weights stay within 2^61
-    while (1ll << (61 - a.frac) < vocab)
+    a.frac = 61;  // sums of vocab weights stay within 2^61; 48 octaves below the greatest nothing is a unit
+    while (a.frac > 46 || 1ll << (61 - a.frac) < vocab)
         --a.frac;
     a.u = u;
     a.temperature = temperature;
