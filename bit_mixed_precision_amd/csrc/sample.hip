@@ -9,25 +9,26 @@
 // between tokens that weigh 2^-17 of the whole).
 //
 // What is kept is a limit in the order of the tokens (key descending, index
-// ascending): its last token's key and index.  Top-k finds it where a count
-// is reached, top-p where a sum of units is, the drawn token where a sum in the
-// order of indices is: all three are one radix select, a histogram of eight
-// more bits at a time.
+// ascending): its last token's key and index.
 //
-// Three kernels, each once over the logits, the first from memory and the others
-// from the caches:
+// Four kernels:
 //   greatest   the greatest logit of every group of a row's lanes;
 //   weigh      a row with a top_k of at most as many as there are groups: no
-//              token below the top_k-th greatest group can be kept, those above
-//              it are written out, a few more than top_k.  Another row: the
-//              units of each quarter of an octave of weight, per workgroup;
-//   draw       one workgroup a row.  Few tokens written out: all from these, in
-//              LDS.  Units per quarter octave: the limit lies in one of them,
-//              whose tokens are gathered into LDS; the sums over the others give
-//              the part of the row that the drawn token is in, which is read
-//              again.  If more must be gathered than LDS holds (a row of equal
-//              logits), all selects run over the row itself.
-// Without a workspace the last form is used alone.
+//              token below the top_k-th greatest group can be kept, those from
+//              it on, a few more than top_k, are listed.  Another row: the units
+//              of each eighth of an octave of weight, per workgroup and row;
+//   gather     lists the tokens of the eighth of an octave in which such a row's limit
+//              lies;
+//   draw       one workgroup a row: ends the kept ones of the listed tokens; the
+//              sums over the others give the part of the row that the drawn token
+//              is in, which is read again.
+// Without a workspace, where a list is too short (a row of equal logits), and for
+// a greater top_k, one workgroup selects over the row itself, eight bits of key at
+// a time.
+//
+// Most of a draw's time is one workgroup's way through code and dependent loads:
+// code that runs once costs the instructions' way from memory, so loops are not
+// unrolled there.
 #include "bq_decode_internal.h"
 #include "dtype16.h"
 
@@ -39,10 +40,10 @@ typedef unsigned long long u64;
 constexpr int kThreads = 1024, kWaves = kThreads / 64;  // of a workgroup that has a row
 constexpr int kPart = 4;                                // wavefronts of one that has a part of a row
 constexpr uint32_t kNone = 0x007fffffu;                 // keys up to that of -infinity are no tokens
-constexpr int kOct = 192;                               // quarter octaves of weight: 48 octaves, past which nothing is a unit
+constexpr int kOct = 384;                               // eighths of octaves of weight: 48 octaves, past which nothing is a unit
 constexpr int kGroups = 256;                            // groups of a row, at most
-constexpr int kRowList = 2048;                          // tokens of a row that are written out, at most
-constexpr int kList = 6144;                             // tokens gathered in LDS, at most
+constexpr int kList = 6144;                             // tokens of a row that are listed, at most
+constexpr int kFound = 1024;                            // of them by one workgroup
 
 // The order of the numbers as unsigned integers; -0 as 0, NaN below all.
 __device__ __forceinline__ uint32_t key_of(float x)
@@ -54,6 +55,10 @@ __device__ __forceinline__ float value_of(uint32_t key)
 {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
+// A token as one number, in the order of tokens the greater the earlier.
+__device__ __forceinline__ u64 order_of(uint32_t key, int index) { return (u64)key << 32 | ~(uint32_t)index; }
+__device__ __forceinline__ uint32_t key_in(u64 order) { return (uint32_t)(order >> 32); }
+__device__ __forceinline__ int index_in(u64 order) { return (int)~(uint32_t)order; }
 
 // A row of logits, as vectors of 16 bytes from the aligned address at or before
 // its start; of the first and last one only what lies in the row is read.
@@ -79,30 +84,6 @@ struct Row {
         else
             return TYPE == 1 ? BF16::to_f32(bits & 0xffffu) : F16::to_f32(bits & 0xffffu);
     }
-    // Raw vector v; what is not in the row is -infinity.
-    __device__ __forceinline__ u4 load(int v) const
-    {
-        const int first = v * kE - lead;
-        if (first >= 0 && first + kE <= vocab)
-            return *(const u4 *)(base + (int64_t)v * 16);
-        u4 x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (TYPE == 2) {
-                const int at = first + i;
-                x[i] = at >= 0 && at < vocab ? ((const uint32_t *)base)[v * 4 + i] : 0xff800000u;
-            } else {
-                uint32_t h[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int at = first + 2 * i + j;
-                    h[j] = at >= 0 && at < vocab ? ((const uint16_t *)base)[v * 8 + 2 * i + j] : (TYPE == 1 ? 0xff80u : 0xfc00u);
-                }
-                x[i] = h[0] | h[1] << 16;
-            }
-        }
-        return x;
-    }
     __device__ __forceinline__ static float value(const u4 &x, int e)
     {
         if constexpr (TYPE == 2)
@@ -110,94 +91,162 @@ struct Row {
         else
             return value(x[e >> 1] >> (16 * (e & 1)));
     }
-    // f(index, key) for the tokens of vectors [first, last), as the wavefront's
-    // parts of them: 64 neighbouring vectors a step, all lanes at the same step
-    // and token of their vector (key 0 past the end).
-    template <typename F>
-    __device__ __forceinline__ void each(int first, int last, F f) const
+    // Drops the first token of a vector; `next` becomes its last.
+    __device__ __forceinline__ static void shift(u4 &x, uint32_t next)
     {
-        const int part = (last - first + kThreads - 1) / kThreads * 64, lane = threadIdx.x & 63;
-        const int v0 = first + (int)(threadIdx.x >> 6) * part, v1 = min(v0 + part, last);
-        for (int v = v0; v < v1; v += 64) {
-            u4 x = {};
-            const bool in = v + lane < v1;
-            if (in)
-                x = load(v + lane);
+        if constexpr (TYPE == 2) {
+            x[0] = x[1];
+            x[1] = x[2];
+            x[2] = x[3];
+            x[3] = next;
+        } else {
+            x[0] = __builtin_amdgcn_alignbit(x[1], x[0], 16);
+            x[1] = __builtin_amdgcn_alignbit(x[2], x[1], 16);
+            x[2] = __builtin_amdgcn_alignbit(x[3], x[2], 16);
+            x[3] = __builtin_amdgcn_alignbit(next, x[3], 16);
+        }
+    }
+    // Raw vector v; what is not in the row is -infinity.
+    __device__ __forceinline__ u4 load(int v) const
+    {
+        const int first = v * kE - lead;
+        if (first >= 0 && first + kE <= vocab)
+            return *(const u4 *)(base + (int64_t)v * 16);
+        u4 x = {};
+#pragma unroll 1
+        for (int i = 0; i < kE; ++i) {
+            const bool in = first + i >= 0 && first + i < vocab;
+            if constexpr (TYPE == 2)
+                shift(x, in ? ((const uint32_t *)base)[v * kE + i] : 0xff800000u);
+            else
+                shift(x, in ? ((const uint16_t *)base)[v * kE + i] : TYPE == 1 ? 0xff80u : 0xfc00u);
+        }
+        return x;
+    }
+    // f(index, key) for the tokens of vector v.
+    template <typename F>
+    __device__ __forceinline__ void each_token(int v, u4 x, F f) const
+    {
+        int at = v * kE - lead;
+#pragma unroll 1
+        for (int i = 0; i < kE; ++i, ++at) {
+            f(at, key_of(value(x[0])));
+            shift(x, 0);
+        }
+    }
+    // The same for the whole row, by a workgroup of kThreads.
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        const int n = vectors();
+        for (int v = threadIdx.x; v < n; v += 4 * kThreads) {
+            u4 x[4];
 #pragma unroll
-            for (int e = 0; e < kE; ++e)
-                f((v + lane) * kE + e - lead, in ? key_of(value(x, e)) : 0u);
+            for (int i = 0; i < 4; ++i)
+                if (v + kThreads * i < n)
+                    x[i] = load(v + kThreads * i);
+#pragma unroll 1
+            for (int at = v; at < min(v + 4 * kThreads, n); at += kThreads) {
+                each_token(at, x[0], f);
+                x[0] = x[1];
+                x[1] = x[2];
+                x[2] = x[3];
+            }
         }
     }
 };
 
 // Weights of a row's tokens.
 struct Scale {
-    uint32_t top;     // greatest key
-    double max, c;    // y = (max - x) c
+    uint32_t top;       // greatest key
+    double max, c;      // y = (max - x) c / 8: c counts eighths of octaves
     int frac;
+    const double *mid;  // [kOct] weight of the middle of each eighth of an octave, in units
 
-    __device__ __forceinline__ double octaves(uint32_t key) const
+    // Eighths of octaves below the greatest.
+    __device__ __forceinline__ double eighths(uint32_t key) const
     {
         return key == top ? 0.0 : (max - (double)value_of(key)) * c;
     }
-    __device__ __forceinline__ static int bin(double y) { return y < 0.25 * kOct ? (int)(y * 4.0) : kOct; }
-    // 2^-y in units, to the nearest: 2^r by its series, whose remainder is below
-    // 2^-47, |r| <= 1/2.
-    __device__ __forceinline__ u64 units(double y) const
+    // 2^-(q / 8) in units, to the nearest: from the middle of the eighth of an octave
+    // `bin` = floor(q) on by the series, whose remainder is below 2^-50.
+    __device__ __forceinline__ u64 units(double q, int bin) const
     {
-        constexpr double l = 0.693147180559945309417;
-        constexpr double c1 = l, c2 = c1 * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5, c6 = c5 * l / 6,
-                         c7 = c6 * l / 7, c8 = c7 * l / 8, c9 = c8 * l / 9, c10 = c9 * l / 10, c11 = c10 * l / 11;
-        if (!(y < 0.25 * kOct))
-            return 0;
-        const double n = __builtin_rint(y), r = n - y;
-        double p = c11;
-        p = __builtin_fma(p, r, c10);
-        p = __builtin_fma(p, r, c9);
-        p = __builtin_fma(p, r, c8);
-        p = __builtin_fma(p, r, c7);
-        p = __builtin_fma(p, r, c6);
-        p = __builtin_fma(p, r, c5);
-        p = __builtin_fma(p, r, c4);
-        p = __builtin_fma(p, r, c3);
-        p = __builtin_fma(p, r, c2);
-        p = __builtin_fma(p, r, c1);
-        p = __builtin_fma(p, r, 1.0);
+        constexpr double l = 0.693147180559945309417 / 8;
+        constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5, c6 = c5 * l / 6, c7 = c6 * l / 7;
+        const double r = ((double)bin + 0.5) - q;
+        double s = c7;
+        s = __builtin_fma(s, r, c6);
+        s = __builtin_fma(s, r, c5);
+        s = __builtin_fma(s, r, c4);
+        s = __builtin_fma(s, r, c3);
+        s = __builtin_fma(s, r, c2);
+        s = __builtin_fma(s, r, l);
+        s = __builtin_fma(s, r, 1.0);
         // with 2^52 added, the number's low bits are the rounded integer
-        const double scale = __hiloint2double((1023 + frac - (int)n) << 20, 0);
-        return (u64)__double_as_longlong(__builtin_fma(p, scale, 0x1p52)) & 0xfffffffffffffull;
+        const u64 n = (u64)__double_as_longlong(__builtin_fma(s, mid[bin], 0x1p52)) & 0xfffffffffffffull;
+        return q == 0.0 ? 1ull << frac : n;
     }
-    __device__ __forceinline__ u64 units_of(uint32_t key) const { return units(octaves(key)); }
+    __device__ __forceinline__ u64 units(double q) const { return q < kOct ? units(q, (int)q) : 0; }
+    __device__ __forceinline__ u64 units_of(uint32_t key) const { return units(eighths(key)); }
 };
+
+// Fills Scale::mid.
+__device__ __forceinline__ void fill_mid(double *mid, int frac)
+{
+    for (int i = threadIdx.x; i < kOct; i += blockDim.x) {
+        // 2^-1/16, and half, quarter and eighth of an octave from there
+        double x = 0.957603280698573646936;
+        x *= i & 4 ? 0.707106781186547524401 : 1.0;
+        x *= i & 2 ? 0.840896415253714543031 : 1.0;
+        x *= i & 1 ? 0.917004043204671231744 : 1.0;
+        mid[i] = x * __hiloint2double((1023 + frac - (i >> 3)) << 20, 0);
+    }
+}
 
 // A row's settings.
 struct Settings {
-    bool greedy;
-    int top_k;             // 0: off
-    bool has_p;
-    double top_p, far, u;  // far: octaves within which min-p keeps tokens
+    bool greedy, has_p;
+    int top_k;  // 0: off
+    float top_p, min_p, u;
 
-    __device__ __forceinline__ Settings(const SampleArgs &p, int b, Scale &s)
+    __device__ __forceinline__ Settings(const SampleArgs &p, int b)
     {
         const float t = p.temperature ? p.temperature[b] : 1.0f;
-        greedy = !(t > 0.0f);
-        s.max = value_of(s.top);
-        s.c = 1.4426950408889634074 / (double)fminf(t, 3.402823466e38f);
-        s.frac = p.frac;
         const int k = p.top_k ? p.top_k[b] : 0;
-        top_k = k > 0 && k < p.vocab ? k : 0;
-        const float tp = p.top_p ? p.top_p[b] : 1.0f, mp = p.min_p ? p.min_p[b] : 0.0f;
-        has_p = tp < 1.0f;
-        top_p = fmaxf(tp, 0.0f);
-        far = mp > 0.0f ? -log2(fmin((double)mp, 1.0)) + 0x1p-53 : 1e300;
+        top_p = p.top_p ? p.top_p[b] : 1.0f;
+        min_p = p.min_p ? p.min_p[b] : 0.0f;
         u = p.u[b];
+        temperature = fminf(t, 3.402823466e38f);
+        greedy = !(t > 0.0f);
+        top_k = k > 0 && k < p.vocab ? k : 0;
+        has_p = top_p < 1.0f;
+    }
+    __device__ __forceinline__ Scale scale(uint32_t top, int frac, const double *mid) const
+    {
+        return {top, value_of(top), 8 * 1.4426950408889634074 / (double)temperature, frac, mid};
+    }
+    // Eighths of octaves within which min-p keeps tokens.
+    __device__ __forceinline__ double far() const
+    {
+        return min_p > 0.0f ? 8 * (0x1p-53 - log2(fmin((double)min_p, 1.0))) : 1e300;
     }
     // The sum that top-p must reach, and the one that the drawn token must pass.
-    __device__ __forceinline__ u64 reach(u64 total) const { return max((u64)ceil(top_p * (double)total), 1ull); }
+    __device__ __forceinline__ u64 reach(u64 total) const
+    {
+        return max((u64)ceil((double)fmaxf(top_p, 0.0f) * (double)total), 1ull);
+    }
     __device__ __forceinline__ u64 pass(u64 total) const
     {
-        return u < 1.0 ? min(total - 1, (u64)floor(fmax(u, 0.0) * (double)total)) : total - 1;
+        return u < 1.0f ? min(total - 1, (u64)floor((double)fmaxf(u, 0.0f) * (double)total)) : total - 1;
     }
+    // Whether weigh lists the tokens from the top_k-th greatest group on, or sums up
+    // the units; else the row itself is selected over.
+    __device__ __forceinline__ bool lists(int groups) const { return top_k && top_k <= groups; }
+    __device__ __forceinline__ bool sums() const { return !top_k; }
+
+private:
+    float temperature;
 };
 
 // Kept: keys above `key`, and those that equal it up to index `last`.
@@ -210,32 +259,53 @@ struct Limit {
 struct Shared {
     u64 hist[256];
     u64 sums[kWaves];
-    uint32_t keys[kWaves];
-    int places[kWaves];
     u64 before;
     uint32_t bin;
     int count;
+    double mid[kOct];
 };
 
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v)
+__device__ __forceinline__ u64 wave_sum(u64 v)
 {
-#pragma unroll
+#pragma unroll 1
     for (int off = 32; off > 0; off >>= 1)
         v += __shfl_xor(v, off, 64);
     return v;
 }
+__device__ __forceinline__ u64 wave_max(u64 v)
+{
+#pragma unroll 1
+    for (int off = 32; off > 0; off >>= 1)
+        v = max(v, __shfl_xor(v, off, 64));
+    return v;
+}
 __device__ __forceinline__ u64 wave_scan(u64 v)  // sums over the lanes up to each
 {
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 64; off <<= 1) {
         const u64 x = __shfl_up(v, off, 64);
-        v += (threadIdx.x & 63) >= off ? x : 0;
+        v += (int)(threadIdx.x & 63) >= off ? x : 0;
     }
     return v;
 }
 
-// Sum over the workgroup, in every thread; sh.sums has each wavefront's.
+// Sums over the threads up to each, and over all of them.
+__device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 &total)
+{
+    const u64 upto = wave_scan(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63)
+        sh.sums[threadIdx.x >> 6] = upto;
+    __syncthreads();
+    u64 before = 0;
+    total = 0;
+#pragma unroll 4
+    for (int w = 0; w < kWaves; ++w) {
+        before += w < (int)(threadIdx.x >> 6) ? sh.sums[w] : 0;
+        total += sh.sums[w];
+    }
+    return before + upto;
+}
 __device__ __forceinline__ u64 block_sum(Shared &sh, u64 v)
 {
     v = wave_sum(v);
@@ -244,36 +314,51 @@ __device__ __forceinline__ u64 block_sum(Shared &sh, u64 v)
         sh.sums[threadIdx.x >> 6] = v;
     __syncthreads();
     u64 total = 0;
+#pragma unroll 4
     for (int w = 0; w < kWaves; ++w)
         total += sh.sums[w];
     return total;
 }
 
-// First of n amounts, four a lane in the first wavefront, at which their sum
-// reaches `stop`: sh.bin, and sh.before what lies before it; n if none does.
-__device__ __forceinline__ void find(Shared &sh, const u64 *amount, int n, bool backwards, u64 stop)
+// Sorts n <= kThreads different numbers in LDS, the greatest first, by counting
+// the greater ones of each.
+__device__ __forceinline__ void sort_few(u64 *x, int n)
 {
-    if (threadIdx.x < 64) {
-        u64 a[4], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = 4 * threadIdx.x + i;
-            a[i] = at < n ? amount[backwards ? n - 1 - at : at] : 0;
-            mine += a[i];
-        }
-        const u64 upto = wave_scan(mine);
-        const u64 there = __ballot(upto >= stop);
-        if (there ? (int)threadIdx.x == __ffsll(there) - 1 : threadIdx.x == 63) {
-            u64 sum = upto - mine;
-            int i = 0;
-            for (; i < 4 && sum + a[i] < stop; ++i)
-                sum += a[i];
-            const int at = there ? 4 * (int)threadIdx.x + i : n;
-            sh.bin = backwards && at < n ? n - 1 - at : at;
-            sh.before = sum;
-        }
+    const u64 mine = (int)threadIdx.x < n ? x[threadIdx.x] : 0;
+    int rank = 0;
+    if ((int)threadIdx.x < n) {
+#pragma unroll 8
+        for (int i = 0; i < n; ++i)
+            rank += x[i] > mine;
     }
     __syncthreads();
+    if ((int)threadIdx.x < n)
+        x[rank] = mine;
+    __syncthreads();
+}
+
+// First of N x 64 amounts, N a lane, at which their sum reaches `stop` (one
+// does), and what lies before it.
+template <int N>
+__device__ __forceinline__ int wave_find(const u64 (&a)[N], u64 stop, u64 &before)
+{
+    u64 mine = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        mine += a[i];
+    const u64 upto = wave_scan(mine);
+    const int lane = __ffsll((u64)__ballot(upto >= stop)) - 1;
+    u64 sum = upto - mine;
+    int at = 0;
+    bool past = false;
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i) {
+        past |= sum + a[i] >= stop;
+        sum += past ? 0 : a[i];
+        at += !past;
+    }
+    before = __shfl(sum, lane, 64);
+    return N * lane + __shfl(at, lane, 64);
 }
 
 // The greatest 32-bit number at which the amounts of the items that have it, or
@@ -285,21 +370,35 @@ __device__ bool select(Shared &sh, Items items, u64 stop, uint32_t &number, u64 
 {
     number = 0;
     before = 0;
+#pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
         __syncthreads();
-        for (int i = threadIdx.x; i < 256; i += kThreads)
-            sh.hist[i] = 0;
+        if (threadIdx.x < 256)
+            sh.hist[threadIdx.x] = 0;
         __syncthreads();
         const uint32_t high = shift == 24 ? 0u : ~0u << (shift + 8);
         items([&](uint32_t x, u64 amount) {
             if ((x & high) == number)
-                atomicAdd(&sh.hist[x >> shift & 255], amount);
+                atomicAdd(&sh.hist[255 - (x >> shift & 255)], amount);
         });
         __syncthreads();
-        find(sh, sh.hist, 256, true, stop - before);
+        if (threadIdx.x < 64) {
+            u64 a[4], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum += a[i] = sh.hist[4 * threadIdx.x + i];
+            sum = wave_sum(sum);
+            u64 less = 0;
+            const int bin = sum >= stop - before ? wave_find(a, stop - before, less) : 256;
+            if (threadIdx.x == 0) {
+                sh.bin = bin;
+                sh.before = less;
+            }
+        }
+        __syncthreads();
         if (sh.bin == 256)
             return false;
-        number |= sh.bin << shift;
+        number |= (255 - sh.bin) << shift;
         before += sh.before;
     }
     return true;
@@ -320,73 +419,64 @@ __device__ bool limit_at(Shared &sh, Tokens tokens, Amount amount, u64 stop, Lim
     return true;
 }
 
-__device__ __forceinline__ void answer(const SampleArgs &p, int b, int token, double logprob)
+__device__ __forceinline__ void answer(const SampleArgs &p, int b, int token, float logprob)
 {
     p.tokens[b] = token;
     if (p.logprobs)
-        p.logprobs[b] = (float)logprob;
+        p.logprobs[b] = logprob;
+}
+__device__ __forceinline__ void answer_first(const SampleArgs &p, int b, u64 first)
+{
+    const bool none = key_in(first) <= kNone;
+    answer(p, b, none ? -1 : index_in(first), none ? -__builtin_inff() : 0.0f);
+}
+// With n of `total` units: by the smaller of the token and the others, so that
+// its rounding is one of the logarithm.
+__device__ __forceinline__ void answer_units(const SampleArgs &p, int b, int token, u64 n, u64 total)
+{
+    const bool most = n > total - n;
+    const float x = (float)((double)(most ? total - n : n) / (double)total);
+    answer(p, b, token, most ? log1pf(-x) : logf(x));
 }
 
-// Draws the token whose units, in the order of indices, pass `want` of the kept
-// units of vectors [first, last), of which `sum` lie before the first.
+// Draws the token at which the kept units, in the order of indices, pass `want`,
+// among vectors [first, last), before which `sum` of them lie.
 template <int TYPE, typename Kept>
-__device__ void draw_from(Shared &sh, const SampleArgs &p, int b, const Row<TYPE> &row, int first, int last, Kept kept, u64 want,
-                          u64 before, u64 total)
+__device__ __forceinline__ void draw_from(Shared &sh, const SampleArgs &p, int b, const Row<TYPE> &row, int first, int last,
+                                          Kept kept, u64 want, u64 sum, u64 total)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    u64 mine = 0;
-    row.each(first, last, [&](int i, uint32_t k) { mine += kept(i, k); });
-    block_sum(sh, mine);
-    u64 sum = before;
-    for (int w = 0; w < wave; ++w)
-        sum += sh.sums[w];
-    if (sum > want || sum + sh.sums[wave] <= want)
-        return;
-    // this wavefront's part has it: one step after another, a step's tokens lane by lane
-    constexpr int E = Row<TYPE>::kE;
-    const int part = (last - first + kThreads - 1) / kThreads * 64;
-    const int v0 = first + wave * part, v1 = min(v0 + part, last);
-    for (int v = v0; v < v1; v += 64) {
-        u64 n[E], lane_sum = 0;
+    for (int v0 = first; v0 < last; v0 += kThreads) {
+        const int v = v0 + threadIdx.x;
+        u64 here = 0, step;
         u4 x = {};
-        const bool in = v + lane < v1;
-        if (in)
-            x = row.load(v + lane);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            n[e] = in ? kept((v + lane) * E + e - row.lead, key_of(row.value(x, e))) : 0;
-            lane_sum += n[e];
+        if (v < last) {
+            x = row.load(v);
+            row.each_token(v, x, [&](int i, uint32_t k) { here += kept(i, k); });
         }
-        const u64 upto = wave_scan(lane_sum) + sum;
-        const u64 past = __ballot(upto > want);
-        if (past) {
-            if (lane == __ffsll(past) - 1) {
-                u64 s = upto - lane_sum;
-                bool done = false;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    s += n[e];
-                    if (!done && s > want) {
-                        done = true;
-                        answer(p, b, (v + lane) * E + e - row.lead, log((double)n[e] / (double)total));
-                    }
-                }
-            }
+        u64 upto = sum + block_scan(sh, here, step);
+        if (upto > want && upto - here <= want) {
+            upto -= here;
+            row.each_token(v, x, [&](int i, uint32_t k) {
+                const u64 n = kept(i, k);
+                if (upto <= want && upto + n > want)
+                    answer_units(p, b, i, n, total);
+                upto += n;
+            });
+        }
+        sum += step;
+        if (sum > want)
             return;
-        }
-        sum = __shfl(upto, 63, 64);
     }
 }
 
-// All of a row's work over the row itself; s.top is known.
+// All of a row's work over the row itself.
 template <int TYPE>
-__device__ __noinline__ void draw_slowly(Shared &sh, const SampleArgs &p, int b, const Row<TYPE> &row, const Scale &s, const Settings &set)
+__device__ __forceinline__ void draw_slowly(Shared &sh, const SampleArgs &p, int b, const Row<TYPE> &row, const Scale &s,
+                                            const Settings &set)
 {
-    const int n = row.vectors();
     Limit limit = {kNone, 0};
-    // zero units are no tokens here: they are not drawn, and add to no sum
     auto tokens = [&](auto f) {
-        row.each(0, n, [&](int i, uint32_t k) {
+        row.each([&](int i, uint32_t k) {
             if (k > kNone && limit.keeps(i, k))
                 f(i, k);
         });
@@ -396,77 +486,57 @@ __device__ __noinline__ void draw_slowly(Shared &sh, const SampleArgs &p, int b,
         if (limit_at(sh, tokens, [](uint32_t) { return (u64)1; }, (u64)set.top_k, to))
             limit = to;
     }
-    if (set.has_p) {
+    const double far = set.far();
+    u64 total = 0;
+#pragma unroll 1
+    for (int pass = set.has_p ? 0 : 1; pass < 2; ++pass) {
         u64 mine = 0;
-        tokens([&](int, uint32_t k) { mine += s.units_of(k); });
-        const u64 stop = set.reach(block_sum(sh, mine));
+        tokens([&](int, uint32_t k) {
+            const double q = s.eighths(k);
+            mine += pass == 0 || q <= far ? s.units(q) : 0;
+        });
+        total = block_sum(sh, mine);
         Limit to;
-        if (limit_at(sh, tokens, [&](uint32_t k) { return s.units_of(k); }, stop, to))
+        if (pass == 0 && limit_at(sh, tokens, [&](uint32_t k) { return s.units_of(k); }, set.reach(total), to))
             limit = to;
     }
     auto kept = [&](int i, uint32_t k) {
         if (k <= kNone || !limit.keeps(i, k))
             return (u64)0;
-        const double y = s.octaves(k);
-        return y <= set.far ? s.units(y) : 0;
+        const double q = s.eighths(k);
+        return q <= far ? s.units(q) : 0;
     };
-    u64 mine = 0;
-    row.each(0, n, [&](int i, uint32_t k) { mine += kept(i, k); });
-    const u64 total = block_sum(sh, mine);
-    draw_from(sh, p, b, row, 0, n, kept, set.pass(total), 0, total);
+    draw_from(sh, p, b, row, 0, row.vectors(), kept, set.pass(total), 0, total);
 }
 
-// The greatest key, of the lowest index, of pairs over the workgroup; in every thread.
-template <int WAVES>
-__device__ __forceinline__ void block_greatest(uint32_t *keys, int *places, uint32_t &key, int &place)
+// A row without what other kernels found.
+template <int TYPE>
+__device__ __noinline__ void draw_row(Shared &sh, const SampleArgs &p, int b)
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const uint32_t k = __shfl_xor(key, off, 64);
-        const int i = __shfl_xor(place, off, 64);
-        if (k > key || (k == key && i < place)) {
-            key = k;
-            place = i;
-        }
-    }
+    const Row<TYPE> row(p, b);
+    u64 first = 0;
+    row.each([&](int i, uint32_t k) { first = max(first, order_of(k, i)); });
+    first = wave_max(first);
+    if ((threadIdx.x & 63) == 0)
+        sh.sums[threadIdx.x >> 6] = first;
+    fill_mid(sh.mid, p.frac);
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-        keys[threadIdx.x >> 6] = key;
-        places[threadIdx.x >> 6] = place;
+    for (int w = 0; w < kWaves; ++w)
+        first = max(first, sh.sums[w]);
+    const Settings set(p, b);
+    if (key_in(first) <= kNone || set.greedy) {
+        if (threadIdx.x == 0)
+            answer_first(p, b, first);
+        return;
     }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-        if (keys[w] > key || (keys[w] == key && places[w] < place)) {
-            key = keys[w];
-            place = places[w];
-        }
+    draw_slowly(sh, p, b, row, set.scale(key_in(first), p.frac, sh.mid), set);
 }
 
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs p)
 {
     __shared__ Shared sh;
-    const int b = blockIdx.x;
-    const Row<TYPE> row(p, b);
-    uint32_t key = 0;
-    int place = p.vocab;
-    row.each(0, row.vectors(), [&](int i, uint32_t k) {
-        if (k > key) {
-            key = k;
-            place = i;
-        }
-    });
-    block_greatest<kWaves>(sh.keys, sh.places, key, place);
-    Scale s;
-    s.top = key;
-    const Settings set(p, b, s);
-    if (key <= kNone || set.greedy) {
-        if (threadIdx.x == 0)
-            answer(p, b, key <= kNone ? -1 : place, key <= kNone ? -__builtin_inf() : 0.0);
-        return;
-    }
-    draw_slowly(sh, p, b, row, s, set);
+    draw_row<TYPE>(sh, p, blockIdx.x);
 }
 
 // How rows are shared between workgroups, and where what they find is kept.
@@ -475,59 +545,97 @@ struct Parts {
     int waves;    // a row, a multiple of kPart
     int lanes;    // of a group: 16 or 64
     int groups;
-    int64_t row_bytes;   // of lists or histograms
     uint32_t *greatest;  // [rows][groups]
-    uint2 *first;        // [rows][waves / kPart]: greatest key and its first place
-    uint8_t *found;      // [rows][row_bytes]
+    u64 *first;          // [rows][waves / kPart]: greatest key and its first place (order_of)
+    u64 *list;           // [rows][kList]: tokens (order_of)
+    uint32_t *length;    // [rows]
+    u64 *sums;           // [rows][kOct]: units per eighth of an octave
+    u64 *units;          // [rows][waves / kPart][kOct]: the same of each part
 
     __host__ __device__ int parts() const { return waves / kPart; }
-    // a row's list and its length, or its histograms [parts][kOct] of units, then
-    // of tokens
-    __device__ uint2 *list(int b) const { return (uint2 *)(found + b * row_bytes); }
-    __device__ uint32_t *length(int b) const { return (uint32_t *)(list(b) + kRowList); }
-    __device__ u64 *units(int b) const { return (u64 *)(found + b * row_bytes); }
-    __device__ uint32_t *tokens(int b) const { return (uint32_t *)(units(b) + parts() * kOct); }
 };
 
 template <int TYPE>
 __global__ __launch_bounds__(64 * kPart) void greatest_kernel(const SampleArgs p, const Parts q)
 {
     constexpr int E = Row<TYPE>::kE;
-    __shared__ uint32_t keys[kPart];
-    __shared__ int places[kPart];
+    __shared__ u64 firsts[kPart];
     const int b = blockIdx.x / q.parts(), part = blockIdx.x % q.parts(), lane = threadIdx.x & 63;
     const int wave = part * kPart + (threadIdx.x >> 6);
     const Row<TYPE> row(p, b);
-    const int n = row.vectors(), first = wave * q.steps * 64;
+    const int n = row.vectors(), first = wave * q.steps * 64 + lane;
     uint32_t key = 0;
-    int place = p.vocab;
-#pragma unroll 4
-    for (int s = 0; s < q.steps; ++s) {
-        const int v = first + s * 64 + lane;
-        if (v >= n)
-            continue;
-        const u4 x = row.load(v);
+    int place = 0;
+    for (int st = 0; st < q.steps; st += 4) {
+        u4 x[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t k = key_of(row.value(x, e));
-            if (k > key) {
-                key = k;
-                place = v * E + e - row.lead;
-            }
-        }
+        for (int i = 0; i < 4; ++i)
+            if (st + i < q.steps && first + (st + i) * 64 < n)
+                x[i] = row.load(first + (st + i) * 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (st + i < q.steps && first + (st + i) * 64 < n)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const uint32_t k = key_of(row.value(x[i], e));
+                    if (k > key) {
+                        key = k;
+                        place = (first + (st + i) * 64) * E + e - row.lead;
+                    }
+                }
     }
     uint32_t g = key;
+#pragma unroll 1
     for (int off = 1; off < q.lanes; off <<= 1)
         g = max(g, (uint32_t)__shfl_xor(g, off, 64));
     if (lane % q.lanes == 0)
         q.greatest[(int64_t)b * q.groups + wave * (64 / q.lanes) + lane / q.lanes] = g;
-    block_greatest<kPart>(keys, places, key, place);
-    if (threadIdx.x == 0) {
-        q.first[(int64_t)b * q.parts() + part] = make_uint2(key, (uint32_t)place);
-        if (part == 0)
-            *q.length(b) = 0;
+    const u64 f = wave_max(order_of(key, place));
+    if (lane == 0)
+        firsts[threadIdx.x >> 6] = f;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        q.first[(int64_t)b * q.parts() + part] = max(max(firsts[0], firsts[1]), max(firsts[2], firsts[3]));
+    if (part == 0) {  // what the next kernels count up
+        for (int i = threadIdx.x; i < kOct; i += 64 * kPart)
+            q.sums[(int64_t)b * kOct + i] = 0;
+        if (threadIdx.x == 0)
+            q.length[b] = 0;
     }
 }
+
+// The tokens that a workgroup lists, in any order: what is drawn from a row's list
+// does not depend on it.
+struct Found {
+    u64 token[kFound];
+    int count, at;
+
+    // The tokens of vector v whose bits are set, by one lane.
+    template <int TYPE>
+    __device__ __forceinline__ void add(const Row<TYPE> &row, int v, const u4 &x, uint32_t on)
+    {
+        int to = atomicAdd(&count, __popc(on));
+        row.each_token(v, x, [&](int index, uint32_t k) {
+            if ((on & 1) && to < kFound)
+                token[to] = order_of(k, index);
+            to += on & 1;
+            on >>= 1;
+        });
+    }
+    // To the row's list; more than there is room for make the list too long.
+    __device__ __forceinline__ void list(const Parts &q, int b)
+    {
+        __syncthreads();
+        const int n = count;
+        if (n == 0)
+            return;
+        if (threadIdx.x == 0)
+            at = (int)atomicAdd(&q.length[b], n > kFound ? kList + 1u : (uint32_t)n);
+        __syncthreads();
+        for (int i = threadIdx.x; i < min(n, kFound) && at + i < kList; i += 64 * kPart)
+            q.list[(int64_t)b * kList + at + i] = token[i];
+    }
+};
 
 template <int TYPE>
 __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, const Parts q)
@@ -535,89 +643,204 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
     constexpr int E = Row<TYPE>::kE;
     static_assert(kGroups == 64 * kPart, "a thread a group");
     __shared__ uint32_t groups[kGroups];
-    __shared__ uint32_t keys[kPart];
-    __shared__ int places[kPart];
     __shared__ uint32_t low;
-    __shared__ u64 units[kOct];
-    __shared__ uint32_t tokens[kOct];
+    __shared__ Found found;
+    u64 *const units = found.token;  // of one of which there is need
+    static_assert(kOct <= kFound, "units share the list's place");
+    __shared__ double mid[kOct];
     const int b = blockIdx.x / q.parts(), part = blockIdx.x % q.parts(), lane = threadIdx.x & 63;
     const int wave = part * kPart + (threadIdx.x >> 6);
-    const uint32_t mine = (int)threadIdx.x < q.groups ? q.greatest[(int64_t)b * q.groups + threadIdx.x] : 0u;
-    groups[threadIdx.x] = mine;
-    uint32_t key = mine;
-    int place = 0;
-    block_greatest<kPart>(keys, places, key, place);
-    Scale s;
-    s.top = key;
-    const Settings set(p, b, s);
-    if (key <= kNone || set.greedy)
+    const Settings set(p, b);
+    const bool lists = set.lists(q.groups);
+    if (set.greedy || (!lists && !set.sums()))
         return;
     const Row<TYPE> row(p, b);
-    const int n = row.vectors(), first = wave * q.steps * 64;
-    if (set.top_k && set.top_k <= q.groups) {
+    const int n = row.vectors(), first = wave * q.steps * 64 + lane;
+    u4 x[4];
+    auto load = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (st + i < q.steps && first + (st + i) * 64 < n)
+                x[i] = row.load(first + (st + i) * 64);
+    };
+    auto each = [&](auto f) {
+        for (int st = 0;;) {
+#pragma unroll 1
+            for (int i = st; i < min(st + 4, q.steps); ++i) {
+                f(first + i * 64);
+                x[0] = x[1];
+                x[1] = x[2];
+                x[2] = x[3];
+            }
+            st += 4;
+            if (st >= q.steps)
+                break;
+            load(st);
+        }
+    };
+    load(0);
+    if (lists) {
         // the top_k-th greatest group: at least top_k tokens are as great
+        const uint32_t mine = (int)threadIdx.x < q.groups ? q.greatest[(int64_t)b * q.groups + threadIdx.x] : 0u;
+        groups[threadIdx.x] = mine;
+        if (threadIdx.x == 0)
+            found.count = 0;
+        __syncthreads();
         int rank = 0;
+#pragma unroll 8
         for (int i = 0; i < q.groups; ++i)
             rank += groups[i] > mine || (groups[i] == mine && i < (int)threadIdx.x);
         if ((int)threadIdx.x < q.groups && rank == set.top_k - 1)
             low = mine;
         __syncthreads();
         const uint32_t least = max(low, kNone + 1);
-        uint2 *list = q.list(b);
-        for (int st = 0; st < q.steps; ++st) {
-            const int v = first + st * 64 + lane;
-            u4 x = {};
+        each([&](int v) {
             uint32_t on = 0;
             if (v < n) {
-                x = row.load(v);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    on |= (uint32_t)(key_of(row.value(x, e)) >= least) << e;
+                    on |= (uint32_t)(key_of(row.value(x[0], e)) >= least) << e;
             }
-            if (!__any(on))
-                continue;
-            // in any order: what is drawn from the list does not depend on it
-            uint32_t at = 0;
-            const uint32_t upto = (uint32_t)wave_scan(__popc(on));
-            if (lane == 63)
-                at = atomicAdd(q.length(b), upto);
-            at = __shfl(at, 63, 64) + upto - __popc(on);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (on >> e & 1) {
-                    if (at < kRowList)
-                        list[at] = make_uint2(key_of(row.value(x, e)), (uint32_t)(v * E + e - row.lead));
-                    ++at;
-                }
-        }
+            if (on)
+                found.add(row, v, x[0], on);
+        });
+        found.list(q, b);
         return;
     }
-    if (threadIdx.x < kOct) {
-        units[threadIdx.x] = 0;
-        tokens[threadIdx.x] = 0;
+    const u64 top = wave_max(lane < q.parts() ? q.first[(int64_t)b * q.parts() + lane] : 0);
+    if (key_in(top) <= kNone)
+        return;
+    const Scale s = set.scale(key_in(top), p.frac, mid);
+    for (int i = threadIdx.x; i < kOct; i += 64 * kPart)
+        units[i] = 0;
+    fill_mid(mid, p.frac);
+    __syncthreads();
+    each([&](int v) {
+        if (v < n) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float a = row.value(x[0], e);
+                const double eighths = a == (float)s.max ? 0.0 : (s.max - (double)a) * s.c;
+                if (eighths < kOct) {  // no NaN, and no -infinity
+                    const int bin = (int)eighths;
+                    atomicAdd(&units[bin], s.units(eighths, bin));
+                }
+            }
+        }
+    });
+    __syncthreads();
+    for (int i = threadIdx.x; i < kOct; i += 64 * kPart) {
+        const u64 sum = units[i];
+        q.units[((int64_t)b * q.parts() + part) * kOct + i] = sum;
+        if (sum)
+            atomicAdd(&q.sums[(int64_t)b * kOct + i], sum);
     }
+}
+
+// Where a row that was summed up ends what it keeps.
+struct Edge {
+    int bin;     // heavier eighths of octaves are kept; kOct: all are
+    u64 stop;    // units up to which the tokens of this one are, 0: all
+    double far;  // eighths of octaves within which tokens are kept
+};
+
+// Computed by every wavefront, of the row's sums.
+__device__ __forceinline__ Edge edge_of(const u64 *sums, const Settings &set)
+{
+    Edge x = {kOct, 0, set.far()};
+    if (set.has_p) {
+        constexpr int N = kOct / 64;
+        u64 a[N], total = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            total += a[i] = sums[N * (threadIdx.x & 63) + i];
+        const u64 stop = set.reach(wave_sum(total));
+        u64 before;
+        x.bin = wave_find(a, stop, before);
+        x.stop = stop - before;
+    }
+    if (x.far < x.bin) {
+        x.bin = (int)x.far;
+        x.stop = 0;
+    }
+    return x;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(64 * kPart) void gather_kernel(const SampleArgs p, const Parts q)
+{
+    constexpr int E = Row<TYPE>::kE;
+    __shared__ Found found;
+    const int b = blockIdx.x / q.parts(), part = blockIdx.x % q.parts(), lane = threadIdx.x & 63;
+    const int wave = part * kPart + (threadIdx.x >> 6);
+    const Settings set(p, b);
+    if (set.greedy || !set.sums() || !(set.has_p || set.min_p > 0.0f))
+        return;
+    const Row<TYPE> row(p, b);
+    const int n = row.vectors(), first = wave * q.steps * 64 + lane;
+    const u64 top = wave_max(lane < q.parts() ? q.first[(int64_t)b * q.parts() + lane] : 0);
+    if (key_in(top) <= kNone)
+        return;
+    const Scale s = set.scale(key_in(top), p.frac, nullptr);
+    const int bin = edge_of(q.sums + (int64_t)b * kOct, set).bin;
+    if (bin >= kOct)
+        return;
+    if (threadIdx.x == 0)
+        found.count = 0;
     __syncthreads();
     for (int st = 0; st < q.steps; ++st) {
-        const int v = first + st * 64 + lane;
+        const int v = first + st * 64;
         if (v >= n)
             continue;
         const u4 x = row.load(v);
+        uint32_t on = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const uint32_t k = key_of(row.value(x, e));
-            const double y = s.octaves(k);
-            if (k > kNone && y < 0.25 * kOct) {
-                atomicAdd(&units[s.bin(y)], s.units(y));
-                if (set.top_k)
-                    atomicAdd(&tokens[s.bin(y)], 1u);
-            }
+            const float a = row.value(x, e);
+            const double eighths = a == (float)s.max ? 0.0 : (s.max - (double)a) * s.c;
+            on |= (uint32_t)(eighths < kOct && (int)eighths == bin) << e;
         }
+        if (on)
+            found.add(row, v, x, on);
     }
-    __syncthreads();
-    if (threadIdx.x < kOct) {
-        q.units(b)[part * kOct + threadIdx.x] = units[threadIdx.x];
-        if (set.top_k)
-            q.tokens(b)[part * kOct + threadIdx.x] = tokens[threadIdx.x];
+    found.list(q, b);
+}
+
+// Draws from n <= kThreads tokens, among which all that are kept are: sorts them,
+// ends the kept ones, sorts these by index.
+__device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b, u64 *few, u64 *units, int n, const Scale &s,
+                                         const Settings &set)
+{
+    const int i = threadIdx.x;
+    int place = 0;
+    u64 mine = 0, total;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+        sort_few(few, n);
+        const u64 x = i < n ? few[i] : 0;
+        u64 sum;
+        if (pass == 0) {
+            double eighths = 0.0;
+            if (i < min(n, set.top_k)) {
+                place = index_in(x);
+                eighths = s.eighths(key_in(x));
+                mine = s.units(eighths);
+            }
+            sum = block_scan(sh, mine, total);
+            if ((set.has_p && sum - mine >= set.reach(total)) || eighths > set.far())
+                mine = 0;
+            units[i] = mine;
+            n = __syncthreads_count(mine > 0);  // the kept ones are the first
+            few[i] = mine ? order_of(~(uint32_t)place, i) : 0;
+            __syncthreads();
+        } else {
+            mine = i < n ? units[index_in(x)] : 0;
+            sum = block_scan(sh, mine, total);
+            const u64 want = set.pass(total);
+            if (sum > want && sum - mine <= want)
+                answer_units(p, b, (int)~key_in(x), mine, total);
+            return;
+        }
     }
 }
 
@@ -625,191 +848,121 @@ template <int TYPE>
 __global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs p, const Parts q)
 {
     __shared__ Shared sh;
-    __shared__ uint2 list[kList];
-    __shared__ u64 units[kOct], amount[kGroups];
-    const int b = blockIdx.x, parts = q.parts();
-    uint32_t key = 0;
-    int place = p.vocab;
-    for (int i = threadIdx.x; i < parts; i += kThreads) {
-        const uint2 x = q.first[(int64_t)b * parts + i];
-        if (x.x > key) {
-            key = x.x;
-            place = (int)x.y;
-        }
-    }
-    block_greatest<kWaves>(sh.keys, sh.places, key, place);
-    Scale s;
-    s.top = key;
-    const Settings set(p, b, s);
-    if (key <= kNone || set.greedy) {
+    __shared__ u64 few[kThreads], amount[kThreads];
+    const int b = blockIdx.x, parts = q.parts(), lane = threadIdx.x & 63;
+    const Settings set(p, b);
+    const uint32_t length = q.length[b];
+    const u64 first = wave_max(lane < parts ? q.first[(int64_t)b * parts + lane] : 0);
+    if (key_in(first) <= kNone || set.greedy) {
         if (threadIdx.x == 0)
-            answer(p, b, key <= kNone ? -1 : place, key <= kNone ? -__builtin_inf() : 0.0);
+            answer_first(p, b, first);
         return;
     }
-    const Row<TYPE> row(p, b);
+    const bool lists = set.lists(q.groups);
+    if ((!lists && !set.sums()) || length > (lists ? kThreads : kList)) {
+        draw_row<TYPE>(sh, p, b);
+        return;
+    }
+    const Scale s = set.scale(key_in(first), p.frac, sh.mid);
+    const u64 *list = q.list + (int64_t)b * kList;
+    fill_mid(sh.mid, p.frac);
+    if (lists) {
+        if (threadIdx.x < length)
+            few[threadIdx.x] = list[threadIdx.x];
+        __syncthreads();
+        draw_few(sh, p, b, few, amount, (int)length, s, set);
+        return;
+    }
+
+    const Edge edge = edge_of(q.sums + (int64_t)b * kOct, set);
     Limit limit = {kNone, 0};
-    int n = 0;  // of the list
+    u64 mine[kList / kThreads];
+#pragma unroll
+    for (int i = 0; i < kList / kThreads; ++i)
+        mine[i] = threadIdx.x + i * kThreads < length ? list[threadIdx.x + i * kThreads] : 0;
     auto tokens = [&](auto f) {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const uint2 x = list[i];
-            if (limit.keeps((int)x.y, x.x))
-                f((int)x.y, x.x);
+        u64 x[kList / kThreads];
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i)
+            x[i] = mine[i];
+#pragma unroll 1
+        for (uint32_t at = threadIdx.x; at < length; at += kThreads) {
+            f(index_in(x[0]), key_in(x[0]));
+#pragma unroll
+            for (int i = 1; i < kList / kThreads; ++i)
+                x[i - 1] = x[i];
         }
     };
-    auto by_units = [&](uint32_t k) { return s.units_of(k); };
-    auto by_count = [](uint32_t) { return (u64)1; };
-
-    if (set.top_k && set.top_k <= q.groups) {
-        n = (int)min(*q.length(b), (uint32_t)kRowList + 1);
-        if (n > kRowList) {
-            draw_slowly(sh, p, b, row, s, set);
-            return;
-        }
-        for (int i = threadIdx.x; i < n; i += kThreads)
-            list[i] = q.list(b)[i];
+    if (threadIdx.x < 256)
+        sh.hist[threadIdx.x] = 0;
+    if (threadIdx.x == 0)
+        sh.count = 0;
+    __syncthreads();
+    if (edge.stop) {
+        // a 256th of the eighth of an octave, then its tokens in order
+        auto piece = [&](uint32_t k) { return min((int)((s.eighths(k) - edge.bin) * 256.0), 255); };
+        tokens([&](int, uint32_t k) { atomicAdd(&sh.hist[piece(k)], s.units_of(k)); });
         __syncthreads();
-        Limit to;
-        if (limit_at(sh, tokens, by_count, (u64)set.top_k, to))
-            limit = to;
-        if (set.has_p) {
-            u64 mine = 0;
-            tokens([&](int, uint32_t k) { mine += s.units_of(k); });
-            const u64 stop = set.reach(block_sum(sh, mine));
-            if (limit_at(sh, tokens, by_units, stop, to))
-                limit = to;
-        }
-        auto kept = [&](uint32_t k) {
-            const double y = s.octaves(k);
-            return y <= set.far ? s.units(y) : 0;
-        };
-        u64 mine = 0;
-        tokens([&](int, uint32_t k) { mine += kept(k); });
-        const u64 total = block_sum(sh, mine);
-        uint32_t at;
-        u64 before;
-        select(sh, [&](auto f) { tokens([&](int i, uint32_t k) { f(~(uint32_t)i, kept(k)); }); }, set.pass(total) + 1, at, before);
+        u64 a[4], before;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            a[i] = sh.hist[4 * lane + i];
+        const int at = wave_find(a, edge.stop, before);
         tokens([&](int i, uint32_t k) {
-            if (i == (int)~at)
-                answer(p, b, i, log((double)kept(k) / (double)total));
-        });
-        return;
-    }
-
-    // the whole row's units per quarter octave
-    auto sum_up = [&](const auto *from) {
-        __syncthreads();
-        if (threadIdx.x < kOct)
-            amount[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < parts * kOct; i += kThreads)
-            if (from[i])
-                atomicAdd(&amount[i % kOct], (u64)from[i]);
-        __syncthreads();
-    };
-    // gathers the tokens of a quarter octave; false: too many
-    int gathered = -1;
-    auto gather = [&](int bin) {
-        if (bin == gathered)
-            return true;
-        __syncthreads();
-        if (threadIdx.x == 0)
-            sh.count = 0;
-        __syncthreads();
-        row.each(0, row.vectors(), [&](int i, uint32_t k) {
-            if (k > kNone && s.bin(s.octaves(k)) == bin) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList)
-                    list[at] = make_uint2(k, (uint32_t)i);
+            if (piece(k) == at) {
+                const int to = atomicAdd(&sh.count, 1);
+                if (to < kThreads)
+                    few[to] = order_of(k, i);
             }
         });
         __syncthreads();
-        n = min(sh.count, kList);
-        gathered = bin;
-        return sh.count <= kList;
-    };
-    int edge = kOct;  // tokens of heavier quarter octaves are kept, those of this one by the limit
-    if (set.top_k) {
-        sum_up(q.tokens(b));
-        find(sh, amount, kOct, false, (u64)set.top_k);
-        const int bin = (int)sh.bin;
-        const u64 before = sh.before;
-        if (bin < kOct) {
-            Limit to;
-            if (!gather(bin)) {
-                draw_slowly(sh, p, b, row, s, set);
-                return;
-            }
-            limit_at(sh, tokens, by_count, (u64)set.top_k - before, to);
-            limit = to;
-            edge = bin;
+        const int n = sh.count;
+        if (n > kThreads) {  // equal ones, or nearly
+            limit_at(sh, tokens, [&](uint32_t k) { return s.units_of(k); }, edge.stop, limit);
+        } else {
+            sort_few(few, n);
+            const u64 token = (int)threadIdx.x < n ? few[threadIdx.x] : 0;
+            const u64 units = (int)threadIdx.x < n ? s.units_of(key_in(token)) : 0;
+            u64 all;
+            const u64 sum = before + block_scan(sh, units, all);
+            if (sum >= edge.stop && sum - units < edge.stop)
+                sh.before = token;
+            __syncthreads();
+            limit = {key_in(sh.before), index_in(sh.before)};
         }
-    }
-    sum_up(q.units(b));
-    if (threadIdx.x < kOct)
-        units[threadIdx.x] = amount[threadIdx.x];
-    if (set.has_p) {
-        // of the edge's tokens those that top-k keeps
-        u64 mine = 0;
-        if (edge < kOct)
-            tokens([&](int, uint32_t k) { mine += s.units_of(k); });
-        const u64 in_edge = block_sum(sh, mine);
-        if (edge < kOct && threadIdx.x >= (unsigned)edge && threadIdx.x < kOct)
-            units[threadIdx.x] = threadIdx.x == (unsigned)edge ? in_edge : 0;
-        const u64 total = block_sum(sh, threadIdx.x < kOct ? units[threadIdx.x] : 0);
-        const u64 stop = set.reach(total);
-        find(sh, units, kOct, false, stop);
-        const int bin = (int)sh.bin;
-        const u64 before = sh.before;
-        if (bin < kOct) {
-            if (!gather(bin)) {
-                draw_slowly(sh, p, b, row, s, set);
-                return;
-            }
-            Limit to;
-            limit_at(sh, tokens, by_units, stop - before, to);
-            limit = to;
-            edge = bin;
-        }
-    }
-    const int far = s.bin(set.far);
-    if (far < edge) {
-        if (!gather(far)) {
-            draw_slowly(sh, p, b, row, s, set);
-            return;
-        }
-        edge = far;
     }
     auto kept = [&](int i, uint32_t k) {
         if (k <= kNone || !limit.keeps(i, k))
             return (u64)0;
-        const double y = s.octaves(k);
-        return y <= set.far ? s.units(y) : 0;
+        const double eighths = s.eighths(k);
+        return eighths <= edge.far ? s.units(eighths) : 0;
     };
     // what each part of the row keeps
+    for (int w = threadIdx.x >> 6; w < parts; w += kWaves) {
+        u64 sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOct; i += 64)
+            if (i + lane < edge.bin)
+                sum += q.units[((int64_t)b * parts + w) * kOct + i + lane];
+        sum = wave_sum(sum);
+        if (lane == 0)
+            amount[w] = sum;
+    }
     __syncthreads();
-    if (threadIdx.x < kGroups)
-        amount[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < parts * kOct; i += kThreads)
-        if (i % kOct < edge) {
-            const u64 x = q.units(b)[i];
-            if (x)
-                atomicAdd(&amount[i / kOct], x);
-        }
     const int part_vectors = q.steps * 64 * kPart;
-    if (edge < kOct)
-        tokens([&](int i, uint32_t k) {
-            const u64 x = kept(i, k);
-            if (x)
-                atomicAdd(&amount[(i + row.lead) / Row<TYPE>::kE / part_vectors], x);
-        });
+    const Row<TYPE> row(p, b);
+    tokens([&](int i, uint32_t k) {
+        const u64 x = kept(i, k);
+        if (x)
+            atomicAdd(&amount[(i + row.lead) / Row<TYPE>::kE / part_vectors], x);
+    });
     __syncthreads();
-    const u64 total = block_sum(sh, threadIdx.x < kGroups ? amount[threadIdx.x] : 0);
+    // every wavefront finds the part: at most 64 of them, one a lane
+    const u64 here = lane < parts ? amount[lane] : 0, upto = wave_scan(here), total = __shfl(upto, 63, 64);
     const u64 want = set.pass(total);
-    find(sh, amount, parts, false, want + 1);
-    const int part = (int)sh.bin;
-    const u64 before = sh.before;
-    draw_from(sh, p, b, row, part * part_vectors, min((part + 1) * part_vectors, row.vectors()), kept, want, before, total);
+    const int part = __ffsll((u64)__ballot(upto > want)) - 1;
+    draw_from(sh, p, b, row, part * part_vectors, min((part + 1) * part_vectors, row.vectors()), kept, want,
+              __shfl(upto - here, part, 64), total);
 }
 
 // Wavefronts that read 64 vectors a step, so many steps that a row has at most
@@ -824,9 +977,24 @@ Parts parts_of(int64_t rows, int64_t vocab, int type)
     q.waves = (int)((steps + q.steps * kPart - 1) / (q.steps * kPart)) * kPart;
     q.lanes = q.waves <= kGroups / 4 ? 16 : 64;
     q.groups = q.waves * (64 / q.lanes);
-    const int64_t lists = kRowList * 8 + 4, hists = q.parts() * kOct * 12;
-    q.row_bytes = ((lists > hists ? lists : hists) + 15) / 16 * 16;
     return q;
+}
+
+// Lays out the workspace; its bytes.
+int64_t place(Parts &q, int64_t rows, uint8_t *at)
+{
+    uint8_t *const start = at;
+    auto take = [&](auto *&p, int64_t n) {
+        p = (decltype(p + 0))at;
+        at += (n * (int64_t)sizeof(*p) + 15) / 16 * 16;
+    };
+    take(q.list, rows * kList);
+    take(q.units, rows * q.parts() * kOct);
+    take(q.sums, rows * kOct);
+    take(q.first, rows * q.parts());
+    take(q.greatest, rows * q.groups);
+    take(q.length, rows);
+    return at - start;
 }
 
 // Rows of fewer tokens than that are one workgroup's.
@@ -835,28 +1003,25 @@ bool shared(int64_t vocab) { return vocab >= 2048; }
 template <int TYPE>
 hipError_t launch_t(const SampleArgs &p, void *workspace, int64_t workspace_bytes, hipStream_t s)
 {
+    const dim3 rows((unsigned)p.rows);
     const int64_t need = sample_workspace_bytes(p.rows, p.vocab, TYPE);
+    if (!grid_fits(p.rows, kThreads))
+        return kGridTooLarge;
     if (need == 0 || workspace_bytes < need) {
-        if (!grid_fits(p.rows, kThreads))
-            return kGridTooLarge;
-        sample_kernel<TYPE><<<dim3((unsigned)p.rows), kThreads, 0, s>>>(p);
+        sample_kernel<TYPE><<<rows, kThreads, 0, s>>>(p);
         return hipGetLastError();
     }
     Parts q = parts_of(p.rows, p.vocab, TYPE);
-    q.found = (uint8_t *)workspace;
-    q.first = (uint2 *)(q.found + p.rows * q.row_bytes);
-    q.greatest = (uint32_t *)(q.first + (int64_t)p.rows * q.parts());
+    place(q, p.rows, (uint8_t *)workspace);
     const int64_t items = (int64_t)p.rows * q.parts();
-    if (!grid_fits(items, 64 * kPart) || !grid_fits(p.rows, kThreads))
+    if (!grid_fits(items, 64 * kPart))
         return kGridTooLarge;
-    greatest_kernel<TYPE><<<dim3((unsigned)items), 64 * kPart, 0, s>>>(p, q);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    weigh_kernel<TYPE><<<dim3((unsigned)items), 64 * kPart, 0, s>>>(p, q);
-    if ((e = hipGetLastError()) != hipSuccess)
-        return e;
-    draw_kernel<TYPE><<<dim3((unsigned)p.rows), kThreads, 0, s>>>(p, q);
+    const dim3 grid((unsigned)items);
+    greatest_kernel<TYPE><<<grid, 64 * kPart, 0, s>>>(p, q);
+    weigh_kernel<TYPE><<<grid, 64 * kPart, 0, s>>>(p, q);
+    if (p.top_p || p.min_p)
+        gather_kernel<TYPE><<<grid, 64 * kPart, 0, s>>>(p, q);
+    draw_kernel<TYPE><<<rows, kThreads, 0, s>>>(p, q);
     return hipGetLastError();
 }
 
@@ -866,8 +1031,8 @@ int64_t sample_workspace_bytes(int64_t rows, int64_t vocab, int type)
 {
     if (rows == 0 || !shared(vocab))
         return 0;
-    const Parts q = parts_of(rows, vocab, type);
-    return rows * (q.row_bytes + q.parts() * 8 + q.groups * 4);
+    Parts q = parts_of(rows, vocab, type);
+    return place(q, rows, nullptr);
 }
 
 hipError_t launch_sample(const SampleArgs &p, int type, void *workspace, int64_t workspace_bytes, hipStream_t s)
