@@ -11,7 +11,8 @@
 // What is kept is a limit in the order of the tokens (key descending, index
 // ascending): its last token's key and index.
 //
-// Four kernels:
+// Rows of up to 2^15 tokens are held in a workgroup's registers, in one kernel;
+// the others take four:
 //   greatest   the greatest logit of every group of a row's lanes;
 //   weigh      a row with a top_k of at most as many as there are groups: no
 //              token below the top_k-th greatest group can be kept, those from
@@ -22,7 +23,7 @@
 //   draw       one workgroup a row: ends the kept ones of the listed tokens; the
 //              sums over the others give the part of the row that the drawn token
 //              is in, which is read again.
-// Without a workspace, where a list is too short (a row of equal logits), and for
+// The one kernel takes the same steps.  Without a workspace, where a list is too short (a row of equal logits), and for
 // a greater top_k, one workgroup selects over the row itself, eight bits of key at
 // a time.
 //
@@ -133,6 +134,34 @@ struct Row {
             f(at, key_of(value(x[0])));
             shift(x, 0);
         }
+    }
+    // f(index, key) for those whose bits are set.
+    template <typename F>
+    __device__ __forceinline__ void each_set(int v, const u4 &x, uint32_t on, F f) const
+    {
+#pragma unroll 1
+        for (; on; on &= on - 1) {
+            const int e = __ffs(on) - 1, w = TYPE == 2 ? e : e >> 1;
+            const uint32_t lo = w & 1 ? x[1] : x[0], hi = w & 1 ? x[3] : x[2], word = w & 2 ? hi : lo;
+            f(v * kE + e - lead, key_of(value(TYPE == 2 ? word : word >> (16 * (e & 1)))));
+        }
+    }
+    // The greatest number of a vector; NaN is none.
+    __device__ __forceinline__ static float greatest(const u4 &x, float m)
+    {
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+            m = fmaxf(m, value(x, e));
+        return m;
+    }
+    // Bits of the numbers of at least `least`.
+    __device__ __forceinline__ static uint32_t at_least(const u4 &x, float least)
+    {
+        uint32_t on = 0;
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+            on |= (uint32_t)(value(x, e) >= least) << e;
+        return on;
     }
     // The same for the whole row, by a workgroup of kThreads.
     template <typename F>
@@ -539,6 +568,327 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs p)
     draw_row<TYPE>(sh, p, blockIdx.x);
 }
 
+// Where a row that was summed up ends what it keeps.
+struct Edge {
+    int bin;     // heavier eighths of octaves are kept; kOct: all are
+    u64 stop;    // units up to which the tokens of this one are, 0: all
+    double far;  // eighths of octaves within which tokens are kept
+};
+
+// Computed by every wavefront, of the row's sums.
+__device__ __forceinline__ Edge edge_of(const u64 *sums, const Settings &set)
+{
+    Edge x = {kOct, 0, set.far()};
+    if (set.has_p) {
+        constexpr int N = kOct / 64;
+        u64 a[N], total = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            total += a[i] = sums[N * (threadIdx.x & 63) + i];
+        const u64 stop = set.reach(wave_sum(total));
+        u64 before;
+        x.bin = wave_find(a, stop, before);
+        x.stop = stop - before;
+    }
+    if (x.far < x.bin) {
+        x.bin = (int)x.far;
+        x.stop = 0;
+    }
+    return x;
+}
+
+// The limit among the edge's tokens: a 256th of the eighth of an octave, then the
+// tokens in it in order.
+template <typename Tokens>
+__device__ __forceinline__ Limit end_edge(Shared &sh, u64 *few, Tokens tokens, const Edge &edge, const Scale &s)
+{
+    Limit limit = {kNone, 0};
+    __syncthreads();
+    if (threadIdx.x < 256)
+        sh.hist[threadIdx.x] = 0;
+    if (threadIdx.x == 0)
+        sh.count = 0;
+    __syncthreads();
+    if (!edge.stop)
+        return limit;
+    auto piece = [&](uint32_t k) { return min((int)((s.eighths(k) - edge.bin) * 256.0), 255); };
+    tokens([&](int, uint32_t k) { atomicAdd(&sh.hist[piece(k)], s.units_of(k)); });
+    __syncthreads();
+    u64 a[4], before;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a[i] = sh.hist[4 * (threadIdx.x & 63) + i];
+    const int at = wave_find(a, edge.stop, before);
+    tokens([&](int i, uint32_t k) {
+        if (piece(k) == at) {
+            const int to = atomicAdd(&sh.count, 1);
+            if (to < kThreads)
+                few[to] = order_of(k, i);
+        }
+    });
+    __syncthreads();
+    const int n = sh.count;
+    if (n > kThreads) {  // equal ones, or nearly
+        limit_at(sh, tokens, [&](uint32_t k) { return s.units_of(k); }, edge.stop, limit);
+        return limit;
+    }
+    sort_few(few, n);
+    const u64 token = (int)threadIdx.x < n ? few[threadIdx.x] : 0;
+    const u64 units = (int)threadIdx.x < n ? s.units_of(key_in(token)) : 0;
+    u64 all;
+    const u64 sum = before + block_scan(sh, units, all);
+    if (sum >= edge.stop && sum - units < edge.stop)
+        sh.before = token;
+    __syncthreads();
+    limit = {key_in(sh.before), index_in(sh.before)};
+    return limit;
+}
+
+// Draws from n <= kThreads tokens, among which all that are kept are: sorts them,
+// ends the kept ones, sorts these by index.
+__device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b, u64 *few, u64 *units, int n, const Scale &s,
+                                         const Settings &set)
+{
+    const int i = threadIdx.x;
+    int place = 0;
+    u64 mine = 0, total;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+        sort_few(few, n);
+        const u64 x = i < n ? few[i] : 0;
+        u64 sum;
+        if (pass == 0) {
+            double eighths = 0.0;
+            if (i < min(n, set.top_k)) {
+                place = index_in(x);
+                eighths = s.eighths(key_in(x));
+                mine = s.units(eighths);
+            }
+            sum = block_scan(sh, mine, total);
+            if ((set.has_p && sum - mine >= set.reach(total)) || eighths > set.far())
+                mine = 0;
+            units[i] = mine;
+            n = __syncthreads_count(mine > 0);  // the kept ones are the first
+            few[i] = mine ? order_of(~(uint32_t)place, i) : 0;
+            __syncthreads();
+        } else {
+            mine = i < n ? units[index_in(x)] : 0;
+            sum = block_scan(sh, mine, total);
+            const u64 want = set.pass(total);
+            if (sum > want && sum - mine <= want)
+                answer_units(p, b, (int)~key_in(x), mine, total);
+            return;
+        }
+    }
+}
+
+// Draws from listed tokens, of which top-k keeps at most kThreads.
+template <typename Tokens>
+__device__ __forceinline__ void draw_listed(Shared &sh, const SampleArgs &p, int b, Tokens tokens, int length, u64 *few,
+                                            u64 *units, const Scale &s, const Settings &set)
+{
+    Limit limit = {kNone, 0};
+    if (length > kThreads)
+        limit_at(sh, tokens, [](uint32_t) { return (u64)1; }, (u64)set.top_k, limit);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        sh.count = 0;
+    __syncthreads();
+    tokens([&](int i, uint32_t k) {
+        if (limit.keeps(i, k))
+            few[atomicAdd(&sh.count, 1)] = order_of(k, i);
+    });
+    __syncthreads();
+    draw_few(sh, p, b, few, units, sh.count, s, set);
+}
+
+// A row that a workgroup holds in registers, NV vectors a thread.
+template <int TYPE, int NV>
+__global__ __launch_bounds__(kThreads) void sample_held_kernel(const SampleArgs p)
+{
+    constexpr int E = Row<TYPE>::kE;
+    constexpr int kRoom = 4096;  // tokens listed
+    __shared__ Shared sh;
+    __shared__ u64 list[kRoom], few[kThreads], more[kThreads];
+    u64 *const sums = more;  // of one of which there is need
+    __shared__ uint32_t groups[kGroups];
+    __shared__ uint32_t low;
+    const int b = blockIdx.x, lane = threadIdx.x & 63;
+    const Row<TYPE> row(p, b);
+    const int n = row.vectors();
+    u4 held[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        held[i] = (u4){0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // NaN: no tokens
+        if ((int)threadIdx.x + i * kThreads < n)
+            held[i] = row.load(threadIdx.x + i * kThreads);
+    }
+    // f(vector, x) for the held vectors, in a loop
+    auto each_vector = [&](auto f) {
+        u4 x[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            x[i] = held[i];
+#pragma unroll 1
+        for (int v = threadIdx.x; v < n; v += kThreads) {
+            f(v, x[0]);
+#pragma unroll
+            for (int i = 1; i < NV; ++i)
+                x[i - 1] = x[i];
+        }
+    };
+    const Settings set(p, b);
+    fill_mid(sh.mid, p.frac);
+    for (int i = threadIdx.x; i < kOct; i += kThreads)
+        sums[i] = 0;
+    if (threadIdx.x == 0) {
+        sh.count = 0;
+        low = 0;
+    }
+    float most = -__builtin_inff();
+    each_vector([&](int, const u4 &x) { most = row.greatest(x, most); });
+    // groups of 16 lanes, or of four where more tokens are kept than they can tell apart
+    const int quad = set.top_k > 40;
+    uint32_t key = key_of(most);
+    key = max(key, (uint32_t)__shfl_xor(key, 1, 64));
+    key = max(key, (uint32_t)__shfl_xor(key, 2, 64));
+    uint32_t all = max(key, (uint32_t)__shfl_xor(key, 4, 64));
+    all = max(all, (uint32_t)__shfl_xor(all, 8, 64));
+    if (!quad)
+        key = all;
+    if ((threadIdx.x & (quad ? 3 : 15)) == 0)
+        groups[threadIdx.x >> (quad ? 2 : 4)] = key;
+    all = max(all, (uint32_t)__shfl_xor(all, 16, 64));
+    all = max(all, (uint32_t)__shfl_xor(all, 32, 64));
+    if (lane == 0)
+        sh.sums[threadIdx.x >> 6] = all;
+    __syncthreads();
+    const uint32_t top = (uint32_t)wave_max(lane < kWaves ? sh.sums[lane] : 0);
+    if (top <= kNone || set.greedy) {
+        // the first of the greatest: below p.vocab, as there is one
+        if (threadIdx.x == 0)
+            sh.bin = p.vocab;
+        __syncthreads();
+        each_vector([&](int v, const u4 &x) {
+            row.each_token(v, x, [&](int i, uint32_t k) {
+                if (k == top)
+                    atomicMin(&sh.bin, (uint32_t)i);
+            });
+        });
+        __syncthreads();
+        if (threadIdx.x == 0)
+            answer_first(p, b, order_of(top, (int)sh.bin));
+        return;
+    }
+    const bool lists = set.lists(p.vocab <= kRoom ? kThreads : kGroups);
+    if (!lists && !set.sums()) {
+        draw_row<TYPE>(sh, p, b);
+        return;
+    }
+    const Scale s = set.scale(top, p.frac, sh.mid);
+    auto add = [&](int v, const u4 &x, uint32_t on) {
+        if (!on)
+            return;
+        int to = atomicAdd(&sh.count, __popc(on));
+        row.each_set(v, x, on, [&](int index, uint32_t k) {
+            if (to < kRoom)
+                list[to] = order_of(k, index);
+            ++to;
+        });
+    };
+    if (lists) {
+        // the top_k-th greatest group: at least top_k tokens are as great
+        const int mine = threadIdx.x >> (quad ? 2 : 4), step = quad ? 4 : 16;
+        int rank = 0;
+#pragma unroll 4
+        for (int i = threadIdx.x & (step - 1); i < kThreads / step; i += step)
+            rank += groups[i] > key || (groups[i] == key && i < mine);
+        rank += __shfl_xor(rank, 1, 64);
+        rank += __shfl_xor(rank, 2, 64);
+        if (!quad) {
+            rank += __shfl_xor(rank, 4, 64);
+            rank += __shfl_xor(rank, 8, 64);
+        }
+        if (rank == set.top_k - 1)
+            low = key;
+        __syncthreads();
+        const float least = value_of(max(low, kNone + 1));
+        each_vector([&](int v, const u4 &x) { add(v, x, row.at_least(x, least)); });
+    }
+    auto eighths_of = [&](float a) { return a == (float)s.max ? 0.0 : (s.max - (double)a) * s.c; };
+    if (!lists)
+        each_vector([&](int, const u4 &x) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const double eighths = eighths_of(row.value(x, e));
+                if (eighths < kOct)  // no NaN, and no -infinity
+                    atomicAdd(&sums[(int)eighths], s.units(eighths, (int)eighths));
+            }
+        });
+    __syncthreads();
+    const Edge edge = lists ? Edge{kOct, 0, 0.0} : edge_of(sums, set);
+    if (!lists && edge.bin < kOct)
+        each_vector([&](int v, const u4 &x) {
+            uint32_t on = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const double eighths = eighths_of(row.value(x, e));
+                on |= (uint32_t)(eighths < kOct && (int)eighths == edge.bin) << e;
+            }
+            add(v, x, on);
+        });
+    __syncthreads();
+    const int length = sh.count;
+    if (length > kRoom) {
+        draw_row<TYPE>(sh, p, b);
+        return;
+    }
+    auto tokens = [&](auto f) {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < length; i += kThreads)
+            f(index_in(list[i]), key_in(list[i]));
+    };
+    if (lists) {
+        draw_listed(sh, p, b, tokens, length, few, more, s, set);
+        return;
+    }
+    const Limit limit = end_edge(sh, few, tokens, edge, s);
+    auto kept = [&](int i, uint32_t k) {
+        if (k <= kNone || !limit.keeps(i, k))
+            return (u64)0;
+        const double eighths = s.eighths(k);
+        return eighths <= edge.far ? s.units(eighths) : 0;
+    };
+    u64 mine = (int)threadIdx.x < edge.bin && threadIdx.x < kOct ? sums[threadIdx.x] : 0;
+    tokens([&](int i, uint32_t k) { mine += kept(i, k); });
+    const u64 total = block_sum(sh, mine), want = set.pass(total);
+    // step by step in the order of indices
+    u64 sum = 0;
+#pragma unroll 1
+    for (int v0 = 0; v0 < n; v0 += kThreads) {
+        const int v = v0 + threadIdx.x;
+        u64 here = 0, step;
+        if (v < n)
+            row.each_token(v, held[0], [&](int i, uint32_t k) { here += kept(i, k); });
+        u64 upto = sum + block_scan(sh, here, step);
+        if (upto > want && upto - here <= want) {
+            upto -= here;
+            row.each_token(v, held[0], [&](int i, uint32_t k) {
+                const u64 units = kept(i, k);
+                if (upto <= want && upto + units > want)
+                    answer_units(p, b, i, units, total);
+                upto += units;
+            });
+        }
+        sum += step;
+        if (sum > want)
+            return;
+#pragma unroll
+        for (int i = 1; i < NV; ++i)
+            held[i - 1] = held[i];
+    }
+}
+
 // How rows are shared between workgroups, and where what they find is kept.
 struct Parts {
     int steps;    // of 64 vectors, a wavefront
@@ -615,11 +965,10 @@ struct Found {
     __device__ __forceinline__ void add(const Row<TYPE> &row, int v, const u4 &x, uint32_t on)
     {
         int to = atomicAdd(&count, __popc(on));
-        row.each_token(v, x, [&](int index, uint32_t k) {
-            if ((on & 1) && to < kFound)
+        row.each_set(v, x, on, [&](int index, uint32_t k) {
+            if (to < kFound)
                 token[to] = order_of(k, index);
-            to += on & 1;
-            on >>= 1;
+            ++to;
         });
     }
     // To the row's list; more than there is room for make the list too long.
@@ -693,14 +1042,9 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
         if ((int)threadIdx.x < q.groups && rank == set.top_k - 1)
             low = mine;
         __syncthreads();
-        const uint32_t least = max(low, kNone + 1);
+        const float least = value_of(max(low, kNone + 1));
         each([&](int v) {
-            uint32_t on = 0;
-            if (v < n) {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    on |= (uint32_t)(key_of(row.value(x[0], e)) >= least) << e;
-            }
+            const uint32_t on = v < n ? row.at_least(x[0], least) : 0;
             if (on)
                 found.add(row, v, x[0], on);
         });
@@ -735,35 +1079,6 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
         if (sum)
             atomicAdd(&q.sums[(int64_t)b * kOct + i], sum);
     }
-}
-
-// Where a row that was summed up ends what it keeps.
-struct Edge {
-    int bin;     // heavier eighths of octaves are kept; kOct: all are
-    u64 stop;    // units up to which the tokens of this one are, 0: all
-    double far;  // eighths of octaves within which tokens are kept
-};
-
-// Computed by every wavefront, of the row's sums.
-__device__ __forceinline__ Edge edge_of(const u64 *sums, const Settings &set)
-{
-    Edge x = {kOct, 0, set.far()};
-    if (set.has_p) {
-        constexpr int N = kOct / 64;
-        u64 a[N], total = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            total += a[i] = sums[N * (threadIdx.x & 63) + i];
-        const u64 stop = set.reach(wave_sum(total));
-        u64 before;
-        x.bin = wave_find(a, stop, before);
-        x.stop = stop - before;
-    }
-    if (x.far < x.bin) {
-        x.bin = (int)x.far;
-        x.stop = 0;
-    }
-    return x;
 }
 
 template <int TYPE>
@@ -806,44 +1121,6 @@ __global__ __launch_bounds__(64 * kPart) void gather_kernel(const SampleArgs p, 
     found.list(q, b);
 }
 
-// Draws from n <= kThreads tokens, among which all that are kept are: sorts them,
-// ends the kept ones, sorts these by index.
-__device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b, u64 *few, u64 *units, int n, const Scale &s,
-                                         const Settings &set)
-{
-    const int i = threadIdx.x;
-    int place = 0;
-    u64 mine = 0, total;
-#pragma unroll 1
-    for (int pass = 0;; ++pass) {
-        sort_few(few, n);
-        const u64 x = i < n ? few[i] : 0;
-        u64 sum;
-        if (pass == 0) {
-            double eighths = 0.0;
-            if (i < min(n, set.top_k)) {
-                place = index_in(x);
-                eighths = s.eighths(key_in(x));
-                mine = s.units(eighths);
-            }
-            sum = block_scan(sh, mine, total);
-            if ((set.has_p && sum - mine >= set.reach(total)) || eighths > set.far())
-                mine = 0;
-            units[i] = mine;
-            n = __syncthreads_count(mine > 0);  // the kept ones are the first
-            few[i] = mine ? order_of(~(uint32_t)place, i) : 0;
-            __syncthreads();
-        } else {
-            mine = i < n ? units[index_in(x)] : 0;
-            sum = block_scan(sh, mine, total);
-            const u64 want = set.pass(total);
-            if (sum > want && sum - mine <= want)
-                answer_units(p, b, (int)~key_in(x), mine, total);
-            return;
-        }
-    }
-}
-
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs p, const Parts q)
 {
@@ -859,23 +1136,13 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs p, cons
         return;
     }
     const bool lists = set.lists(q.groups);
-    if ((!lists && !set.sums()) || length > (lists ? kThreads : kList)) {
+    if ((!lists && !set.sums()) || length > kList) {
         draw_row<TYPE>(sh, p, b);
         return;
     }
     const Scale s = set.scale(key_in(first), p.frac, sh.mid);
     const u64 *list = q.list + (int64_t)b * kList;
     fill_mid(sh.mid, p.frac);
-    if (lists) {
-        if (threadIdx.x < length)
-            few[threadIdx.x] = list[threadIdx.x];
-        __syncthreads();
-        draw_few(sh, p, b, few, amount, (int)length, s, set);
-        return;
-    }
-
-    const Edge edge = edge_of(q.sums + (int64_t)b * kOct, set);
-    Limit limit = {kNone, 0};
     u64 mine[kList / kThreads];
 #pragma unroll
     for (int i = 0; i < kList / kThreads; ++i)
@@ -893,44 +1160,12 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs p, cons
                 x[i - 1] = x[i];
         }
     };
-    if (threadIdx.x < 256)
-        sh.hist[threadIdx.x] = 0;
-    if (threadIdx.x == 0)
-        sh.count = 0;
-    __syncthreads();
-    if (edge.stop) {
-        // a 256th of the eighth of an octave, then its tokens in order
-        auto piece = [&](uint32_t k) { return min((int)((s.eighths(k) - edge.bin) * 256.0), 255); };
-        tokens([&](int, uint32_t k) { atomicAdd(&sh.hist[piece(k)], s.units_of(k)); });
-        __syncthreads();
-        u64 a[4], before;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            a[i] = sh.hist[4 * lane + i];
-        const int at = wave_find(a, edge.stop, before);
-        tokens([&](int i, uint32_t k) {
-            if (piece(k) == at) {
-                const int to = atomicAdd(&sh.count, 1);
-                if (to < kThreads)
-                    few[to] = order_of(k, i);
-            }
-        });
-        __syncthreads();
-        const int n = sh.count;
-        if (n > kThreads) {  // equal ones, or nearly
-            limit_at(sh, tokens, [&](uint32_t k) { return s.units_of(k); }, edge.stop, limit);
-        } else {
-            sort_few(few, n);
-            const u64 token = (int)threadIdx.x < n ? few[threadIdx.x] : 0;
-            const u64 units = (int)threadIdx.x < n ? s.units_of(key_in(token)) : 0;
-            u64 all;
-            const u64 sum = before + block_scan(sh, units, all);
-            if (sum >= edge.stop && sum - units < edge.stop)
-                sh.before = token;
-            __syncthreads();
-            limit = {key_in(sh.before), index_in(sh.before)};
-        }
+    if (lists) {
+        draw_listed(sh, p, b, tokens, (int)length, few, amount, s, set);
+        return;
     }
+    const Edge edge = edge_of(q.sums + (int64_t)b * kOct, set);
+    const Limit limit = end_edge(sh, few, tokens, edge, s);
     auto kept = [&](int i, uint32_t k) {
         if (k <= kNone || !limit.keeps(i, k))
             return (u64)0;
@@ -997,8 +1232,13 @@ int64_t place(Parts &q, int64_t rows, uint8_t *at)
     return at - start;
 }
 
-// Rows of fewer tokens than that are one workgroup's.
-bool shared(int64_t vocab) { return vocab >= 2048; }
+// Rows that a workgroup holds: up to four vectors of 16-bit logits a thread, eight
+// of fp32.
+constexpr int kHeld16 = 4, kHeld32 = 8;
+bool held(int64_t vocab, int type)
+{
+    return type == 2 ? vocab + 3 <= 4 * kHeld32 * kThreads : vocab + 7 <= 8 * kHeld16 * kThreads;
+}
 
 template <int TYPE>
 hipError_t launch_t(const SampleArgs &p, void *workspace, int64_t workspace_bytes, hipStream_t s)
@@ -1007,7 +1247,11 @@ hipError_t launch_t(const SampleArgs &p, void *workspace, int64_t workspace_byte
     const int64_t need = sample_workspace_bytes(p.rows, p.vocab, TYPE);
     if (!grid_fits(p.rows, kThreads))
         return kGridTooLarge;
-    if (need == 0 || workspace_bytes < need) {
+    if (need == 0) {
+        sample_held_kernel<TYPE, TYPE == 2 ? kHeld32 : kHeld16><<<rows, kThreads, 0, s>>>(p);
+        return hipGetLastError();
+    }
+    if (workspace_bytes < need) {
         sample_kernel<TYPE><<<rows, kThreads, 0, s>>>(p);
         return hipGetLastError();
     }
@@ -1029,7 +1273,7 @@ hipError_t launch_t(const SampleArgs &p, void *workspace, int64_t workspace_byte
 
 int64_t sample_workspace_bytes(int64_t rows, int64_t vocab, int type)
 {
-    if (rows == 0 || !shared(vocab))
+    if (rows == 0 || held(vocab, type))
         return 0;
     Parts q = parts_of(rows, vocab, type);
     return place(q, rows, nullptr);
