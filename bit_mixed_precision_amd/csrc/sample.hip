@@ -187,16 +187,16 @@ struct Row {
 
 // Weights of a row's tokens.
 struct Scale {
-    uint32_t top;       // greatest key
     double max, c;      // y = (max - x) c / 8: c counts eighths of octaves
     int frac;
     const double *mid;  // [kOct] weight of the middle of each eighth of an octave, in units
 
     // Eighths of octaves below the greatest.
-    __device__ __forceinline__ double eighths(uint32_t key) const
+    __device__ __forceinline__ double eighths(float x) const
     {
-        return key == top ? 0.0 : (max - (double)value_of(key)) * c;
+        return x == (float)max ? 0.0 : (max - (double)x) * c;  // not infinity - infinity
     }
+    __device__ __forceinline__ double eighths(uint32_t key) const { return eighths(value_of(key)); }
     // 2^-(q / 8) in units, to the nearest: from the middle of the eighth of an octave
     // `bin` = floor(q) on by the series, whose remainder is below 2^-50.
     __device__ __forceinline__ u64 units(double q, int bin) const
@@ -253,7 +253,7 @@ struct Settings {
     }
     __device__ __forceinline__ Scale scale(uint32_t top, int frac, const double *mid) const
     {
-        return {top, value_of(top), 8 * 1.4426950408889634074 / (double)temperature, frac, mid};
+        return {value_of(top), 8 * 1.4426950408889634074 / (double)temperature, frac, mid};
     }
     // Eighths of octaves within which min-p keeps tokens.
     __device__ __forceinline__ double far() const
@@ -815,12 +815,11 @@ __global__ __launch_bounds__(kThreads) void sample_held_kernel(const SampleArgs 
         const float least = value_of(max(low, kNone + 1));
         each_vector([&](int v, const u4 &x) { add(v, x, row.at_least(x, least)); });
     }
-    auto eighths_of = [&](float a) { return a == (float)s.max ? 0.0 : (s.max - (double)a) * s.c; };
     if (!lists)
         each_vector([&](int, const u4 &x) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const double eighths = eighths_of(row.value(x, e));
+                const double eighths = s.eighths(row.value(x, e));
                 if (eighths < kOct)  // no NaN, and no -infinity
                     atomicAdd(&sums[(int)eighths], s.units(eighths, (int)eighths));
             }
@@ -832,7 +831,7 @@ __global__ __launch_bounds__(kThreads) void sample_held_kernel(const SampleArgs 
             uint32_t on = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const double eighths = eighths_of(row.value(x, e));
+                const double eighths = s.eighths(row.value(x, e));
                 on |= (uint32_t)(eighths < kOct && (int)eighths == edge.bin) << e;
             }
             add(v, x, on);
@@ -903,6 +902,46 @@ struct Parts {
     u64 *units;          // [rows][waves / kPart][kOct]: the same of each part
 
     __host__ __device__ int parts() const { return waves / kPart; }
+};
+
+// A wavefront's vectors of its part of a row, four a lane on their way at a time.
+template <int TYPE>
+struct PartVectors {
+    const Row<TYPE> &row;
+    int first, steps, n;
+    u4 x[4];
+
+    __device__ __forceinline__ PartVectors(const Row<TYPE> &r, const Parts &q, int wave)
+        : row(r), first(wave * q.steps * 64 + (int)(threadIdx.x & 63)), steps(q.steps), n(r.vectors())
+    {
+        load(0);
+    }
+    __device__ __forceinline__ void load(int st)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (st + i < steps && first + (st + i) * 64 < n)
+                x[i] = row.load(first + (st + i) * 64);
+    }
+    // f(vector, x), once
+    template <typename F>
+    __device__ __forceinline__ void each(F f)
+    {
+        for (int st = 0;;) {
+#pragma unroll 1
+            for (int i = st; i < min(st + 4, steps); ++i) {
+                if (first + i * 64 < n)
+                    f(first + i * 64, x[0]);
+                x[0] = x[1];
+                x[1] = x[2];
+                x[2] = x[3];
+            }
+            st += 4;
+            if (st >= steps)
+                break;
+            load(st);
+        }
+    }
 };
 
 template <int TYPE>
@@ -1004,30 +1043,7 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
     if (set.greedy || (!lists && !set.sums()))
         return;
     const Row<TYPE> row(p, b);
-    const int n = row.vectors(), first = wave * q.steps * 64 + lane;
-    u4 x[4];
-    auto load = [&](int st) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (st + i < q.steps && first + (st + i) * 64 < n)
-                x[i] = row.load(first + (st + i) * 64);
-    };
-    auto each = [&](auto f) {
-        for (int st = 0;;) {
-#pragma unroll 1
-            for (int i = st; i < min(st + 4, q.steps); ++i) {
-                f(first + i * 64);
-                x[0] = x[1];
-                x[1] = x[2];
-                x[2] = x[3];
-            }
-            st += 4;
-            if (st >= q.steps)
-                break;
-            load(st);
-        }
-    };
-    load(0);
+    PartVectors<TYPE> vectors(row, q, wave);
     if (lists) {
         // the top_k-th greatest group: at least top_k tokens are as great
         const uint32_t mine = (int)threadIdx.x < q.groups ? q.greatest[(int64_t)b * q.groups + threadIdx.x] : 0u;
@@ -1043,10 +1059,10 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
             low = mine;
         __syncthreads();
         const float least = value_of(max(low, kNone + 1));
-        each([&](int v) {
-            const uint32_t on = v < n ? row.at_least(x[0], least) : 0;
+        vectors.each([&](int v, const u4 &x) {
+            const uint32_t on = row.at_least(x, least);
             if (on)
-                found.add(row, v, x[0], on);
+                found.add(row, v, x, on);
         });
         found.list(q, b);
         return;
@@ -1059,16 +1075,13 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
         units[i] = 0;
     fill_mid(mid, p.frac);
     __syncthreads();
-    each([&](int v) {
-        if (v < n) {
+    vectors.each([&](int, const u4 &x) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float a = row.value(x[0], e);
-                const double eighths = a == (float)s.max ? 0.0 : (s.max - (double)a) * s.c;
-                if (eighths < kOct) {  // no NaN, and no -infinity
-                    const int bin = (int)eighths;
-                    atomicAdd(&units[bin], s.units(eighths, bin));
-                }
+        for (int e = 0; e < E; ++e) {
+            const double eighths = s.eighths(row.value(x, e));
+            if (eighths < kOct) {  // no NaN, and no -infinity
+                const int bin = (int)eighths;
+                atomicAdd(&units[bin], s.units(eighths, bin));
             }
         }
     });
@@ -1092,7 +1105,7 @@ __global__ __launch_bounds__(64 * kPart) void gather_kernel(const SampleArgs p, 
     if (set.greedy || !set.sums() || !(set.has_p || set.min_p > 0.0f))
         return;
     const Row<TYPE> row(p, b);
-    const int n = row.vectors(), first = wave * q.steps * 64 + lane;
+    PartVectors<TYPE> vectors(row, q, wave);
     const u64 top = wave_max(lane < q.parts() ? q.first[(int64_t)b * q.parts() + lane] : 0);
     if (key_in(top) <= kNone)
         return;
@@ -1103,21 +1116,16 @@ __global__ __launch_bounds__(64 * kPart) void gather_kernel(const SampleArgs p, 
     if (threadIdx.x == 0)
         found.count = 0;
     __syncthreads();
-    for (int st = 0; st < q.steps; ++st) {
-        const int v = first + st * 64;
-        if (v >= n)
-            continue;
-        const u4 x = row.load(v);
+    vectors.each([&](int v, const u4 &x) {
         uint32_t on = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float a = row.value(x, e);
-            const double eighths = a == (float)s.max ? 0.0 : (s.max - (double)a) * s.c;
+            const double eighths = s.eighths(row.value(x, e));
             on |= (uint32_t)(eighths < kOct && (int)eighths == bin) << e;
         }
         if (on)
             found.add(row, v, x, on);
-    }
+    });
     found.list(q, b);
 }
 
