@@ -304,12 +304,14 @@ static int attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q
     a.lse = lse;
     a.tree_mask = mask;
     a.mask_words = (int)mask_words;
-    const bq::AttnKv4Plan plan = bq::attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, head_dim, max_len);
+    const bq::AttnKv4Plan plan = (tree ? bq::attn_tree_plan : bq::attn_kv4_plan)(batch, max_q_len, q_heads, kv_heads, head_dim,
+                                                                                max_len);
     a.row_tiles = (int)plan.row_tiles;
     a.nsplit = plan.part_rows > 0 && workspace && workspace_bytes >= plan.part_rows * (head_dim + 2) * 4 ? plan.nsplit : 1;
     a.part = (float *)workspace;
     a.part_ml = a.part + plan.part_rows * head_dim;
-    return bq::launch_status(bq::launch_attn_kv4(a, head_dim, plan.rt, dtype == BQ_BF16, (hipStream_t)stream));
+    return bq::launch_status((tree ? bq::launch_attn_tree : bq::launch_attn_kv4)(a, head_dim, plan.rt, dtype == BQ_BF16,
+                                                                                 (hipStream_t)stream));
 }
 
 int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
@@ -325,8 +327,9 @@ int bq_attn_kv4(const void *q, int64_t q_stride, int dtype, const int32_t *q_sta
 int64_t bq_attn_kv4_tree_workspace_bytes(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int head_dim,
                                          int64_t max_len)
 {
-    return max_q_len > BQ_TREE_MAX ? -BQ_ERR_SHAPE
-                                   : bq_attn_kv4_workspace_bytes(batch, max_q_len, q_heads, kv_heads, head_dim, max_len);
+    if (max_q_len > BQ_TREE_MAX || attn_shape(batch, max_q_len, q_heads, kv_heads, head_dim, max_len) != BQ_OK)
+        return -BQ_ERR_SHAPE;
+    return bq::attn_tree_plan(batch, max_q_len, q_heads, kv_heads, head_dim, max_len).part_rows * (head_dim + 2) * 4;
 }
 
 int bq_attn_kv4_tree(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,

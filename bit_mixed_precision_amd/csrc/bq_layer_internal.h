@@ -63,6 +63,10 @@ struct AttnKv4Plan {
 };
 AttnKv4Plan attn_kv4_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int D, int64_t max_len);
 hipError_t launch_attn_kv4(AttnKv4Args &p, int D, int rt, bool bf16, hipStream_t s);
+// The same for the nodes of trees (tree_mask set); rt > 2: rows that share
+// decoded codes.
+AttnKv4Plan attn_tree_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int D, int64_t max_len);
+hipError_t launch_attn_tree(AttnKv4Args &p, int D, int rt, bool bf16, hipStream_t s);
 
 // 4-bit weights with group scales times 16-bit activations.  A call whose
 // outputs are few splits K over workgroups through `ws` when it is given.

@@ -869,3 +869,184 @@ def test_step_on_other_streams(bq, dev):
     for o, w in zip(states, wants):
         for k in OUTS:
             assert torch.equal(o[k], w[k]), k
+
+
+# ---------------------------------------------- trees by way of shared operands
+
+def wide_run(bq, dev, q, cache, tab, lens, hkv, page, mask, *a, **kw):
+    """run_tree with a table so wide that rows times keys take the kernel whose
+    rows share decoded codes; no entry of the added ones is read."""
+    maxq = kw.get("maxq") or (a[1] if len(a) > 1 and a[1] else q.shape[0] // len(lens))
+    per = len(lens) * hkv * max(maxq * (q.shape[1] // hkv), 1)
+    blocks = -(-(1 << 26) // (per * page))
+    more = torch.full((tab.shape[0], max(blocks - tab.shape[1], 1)), 1 << 30, dtype=torch.int32)
+    return run_tree(bq, dev, q, cache, torch.cat([tab, more], 1), lens, hkv, page, mask, *a, **kw)
+
+
+SHARED = [
+    ([1], 70, 1, 1, 128, 16, 0),
+    ([700], 25, 16, 2, 128, 16, 0),
+    ([31, 32, 33, 40, 63, 64, 65, 127, 128, 129], 30, 3, 1, 128, 16, 0),
+    ([129, 40, 300], 33, 16, 2, 128, 32, 0),      # three tiles of 128 rows
+    ([257, 640], 31, 20, 4, 64, 64, 0),
+    ([1000, 65], 64, 14, 2, 128, 128, 100),
+    ([90, 70, 66], 65, 4, 2, 128, 16, 0),
+    ([300, 140], 130, 4, 2, 64, 32, 0),
+    ([200, 190], 33, 6, 2, 128, 16, 20),          # a window inside the tree
+    ([5000, 3, 64, 2999], 24, 4, 1, 64, 16, 0),
+    ([4000, 90], 17, 8, 1, 128, 16, 1500),
+    ([300], 1000, 2, 2, 64, 16, 0),               # fewer keys than nodes
+    ([700, 130], 1024, 1, 1, 128, 256, 0),
+    ([40, 45], 70, 1, 1, 64, 16, 1),
+    ([190], 19, 64, 1, 128, 64, 0),               # 1216 rows: a tile that is not full
+]
+
+
+@pytest.mark.parametrize("c", SHARED)
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("ws", ["auto", "none", "full"])
+def test_attn_kv4_tree_shared(bq, dev, monkeypatch, c, T, ws):
+    shared(monkeypatch)
+    test_attn_kv4_tree(bq, dev, c, T, ws)
+
+
+def shared(monkeypatch):
+    narrow = run_tree
+
+    def run(*a, **kw):
+        with monkeypatch.context() as m:
+            m.setitem(globals(), "run_tree", narrow)
+            return wide_run(*a, **kw)
+
+    monkeypatch.setitem(globals(), "run_tree", run)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("window", [0, 6, 50])
+@pytest.mark.parametrize("d,hq,hkv,nodes", [(64, 4, 1, 40), (128, 8, 1, 40), (128, 4, 2, 36), (64, 6, 2, 30)])
+def test_attn_kv4_tree_shared_any_bits(bq, dev, monkeypatch, T, window, d, hq, hkv, nodes):
+    shared(monkeypatch)
+    test_attn_kv4_tree_any_bits(bq, dev, T, window, d, hq, hkv, nodes)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("group", [1, 6])
+def test_attn_kv4_tree_shared_ragged(bq, dev, monkeypatch, T, group):
+    shared(monkeypatch)
+    test_attn_kv4_tree_ragged(bq, dev, T, group)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("k_off,v_mul,q_mul", [(0.0, 1e-4, 1.0), (4.0, 300.0, 3.0), (0.0, 4000.0, 0.01), (1.0, 1.0, 30.0)])
+def test_attn_kv4_tree_shared_ranges(bq, dev, monkeypatch, T, k_off, v_mul, q_mul):
+    shared(monkeypatch)
+    test_attn_kv4_tree_ranges(bq, dev, T, k_off, v_mul, q_mul, 33)
+
+
+def test_attn_kv4_tree_shared_growing_scales(bq, dev, monkeypatch):
+    shared(monkeypatch)
+    test_attn_kv4_tree_growing_scales(bq, dev)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1.0])
+@pytest.mark.parametrize("T", TYPES)
+def test_attn_kv4_tree_shared_scales(bq, dev, monkeypatch, T, scale):
+    shared(monkeypatch)
+    test_attn_kv4_tree_scales(bq, dev, T, scale, 20)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("hq,d,nodes", [(64, 64, 8), (16, 128, 8), (4, 128, 60), (2, 64, 64)])
+def test_attn_kv4_tree_shared_masked_places_may_be_anything(bq, dev, monkeypatch, T, hq, d, nodes):
+    shared(monkeypatch)
+    test_attn_kv4_tree_masked_places_may_be_anything(bq, dev, T, hq, d, nodes)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("batch,top,hq,hkv,d,nodes,window", [(40, 333, 16, 1, 64, 5, 0), (130, 290, 4, 1, 128, 20, 50),
+                                                             (9, 2400, 16, 2, 128, 12, 0), (65, 150, 40, 5, 64, 9, 0),
+                                                             (300, 90, 24, 1, 64, 3, 0), (3, 20000, 4, 1, 64, 17, 0)])
+def test_attn_kv4_tree_shared_many_workgroups(bq, dev, monkeypatch, T, batch, top, hq, hkv, d, nodes, window):
+    shared(monkeypatch)
+    test_attn_kv4_tree_many_workgroups(bq, dev, T, batch, top, hq, hkv, d, nodes, window)
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_kv4_tree_shared_bad_pages_and_lengths(bq, dev, T, d):
+    """Pages that are none, lengths below zero and past the table, in a table of
+    its full width."""
+    banner(f"tree attention shared bad pages {d} {T}")
+    hq, hkv, page, nodes, B, wide = 32, 1, 16, 6, 3, 128
+    g = gen(18)
+    cache = make_cache(g, 40, hkv, d, page, T)
+    tab = torch.randint(-3, 44, (B, wide), generator=g, dtype=torch.int32)
+    tab[0, :9] = torch.arange(9)
+    tab[1, 3], tab[1, 4] = 1 << 30, -(1 << 31)
+    # 64 sequences more without queries make the rows times keys
+    more = 200
+    tab = torch.cat([tab, torch.full((more, wide), 77, dtype=torch.int32)])
+    _, see, mask, _ = trees(g, [nodes] * B)
+    q = torch.randn(B * nodes, hq, d, generator=g).to(T)
+    starts = [min(nodes * i, B * nodes) for i in range(B + more + 1)]
+    see = see + [torch.zeros(0, 0, dtype=torch.bool)] * more
+    for lens in ([140, 1 << 30, 2048], [-7, 60, 1 << 20], [3, 0, 1]):
+        lens = lens + [100] * more
+        got = run_tree(bq, dev, q, cache, tab, lens, hkv, page, mask, starts, nodes)
+        check_tree(got, q, cache, tab, [min(n, wide * page) for n in lens], starts, see, what=str(lens[:3]))
+
+
+def test_attn_kv4_tree_shared_captured(bq, dev):
+    """A captured call replayed with other lengths, queries and masks, beside a
+    second one with a workspace of its own."""
+    banner("tree attention shared captured")
+    T, B, nodes, hq, hkv, d, page, wide = torch.bfloat16, 3, 40, 4, 1, 64, 16, 16384
+    g = gen(19)
+    cache = make_cache(g, 130, hkv, d, page, T)
+    tab = torch.full((B, wide), -1, dtype=torch.int32)
+    for b in range(B):
+        tab[b, :42] = torch.arange(42) + 42 * b
+    tab_d, cache_d = tab.to(dev), cache.flat().to(dev)
+    sets = []
+    for k in range(2):
+        need = bq.attn_kv4_tree_workspace_bytes(B, nodes, hq, hkv, d, wide * page)
+        assert need > 0
+        sets.append(dict(q=torch.zeros(B * nodes, hq, d, dtype=T, device=dev), lens=i32([0] * B, dev),
+                         mask=torch.zeros(B * nodes, 2, dtype=torch.int32, device=dev), out=torch.zeros(B * nodes, hq, d, dtype=T, device=dev),
+                         lse=torch.zeros(B * nodes, hq, device=dev), ws=torch.empty(need, dtype=torch.uint8, device=dev)))
+
+    def call(s):
+        bq.attn_kv4_tree(s["q"], cache_d, tab_d, s["lens"], page, hkv, s["mask"], d ** -0.5, None, None, 0, s["out"], s["lse"],
+                         workspace=s["ws"])
+
+    graphs = []
+    for s in sets:
+        call(s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(s)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, lens in enumerate([[600, 50, 41], [40, 640, 300], [0, 0, 670], [100, 100, 100]]):
+        given = []
+        for k, s in enumerate(sets):
+            mine = lens[k:] + lens[:k]
+            _, see, mask, _ = trees(g, [nodes] * B)
+            q = torch.randn(B * nodes, hq, d, generator=g).to(T)
+            s["q"].copy_(q)
+            s["lens"].copy_(i32(mine, dev))
+            s["mask"].copy_(mask)
+            s["out"].fill_(7)
+            given.append((q, mine, see))
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for s, (q, mine, see) in zip(sets, given):
+            check_tree((s["out"], s["lse"]), q, cache, tab, mine, [nodes * j for j in range(B + 1)], see, what=f"replay {i}")
+            eager = [x.clone() for x in (s["out"], s["lse"])]
+            call(s)
+            torch.cuda.synchronize()
+            assert torch.equal(eager[0], s["out"]) and torch.equal(eager[1], s["lse"])
