@@ -90,10 +90,14 @@ __global__ void tree_accept_kernel(const TreeArgs t, const int32_t *tokens, cons
         path[(int64_t)b * max_path + i] = i < steps ? taken[i] : -1;
 }
 
-// A wavefront moves the entries of one sequence, layer and kv head.  A lane
-// moves the same bytes of every token, entry after entry: entry j reads key
-// path[j] >= j, which no entry before it has written (they write keys before
-// j), so all reads are as of the start.
+// A wavefront moves the entries of one sequence, layer and kv head.  Entry j
+// reads key path[j] >= j and writes key j: what is read has not been written by
+// an entry before, so entries may be read ahead of the ones before them, and are,
+// kAhead at a time; where they lie is found for 64 at a time, an entry a lane.
+// Bound by latency: a token is 8 lines of the cache.  32 layers of 8 heads, 64
+// paths through trees of 64 nodes, D = 128: 16.0 us, one at a time 24.5, eight 17.5.
+constexpr int kAhead = 4;
+
 template <int D>
 __global__ __launch_bounds__(256) void kv4_compact_kernel(const TreeArgs t, const CompactArgs c, int64_t items)
 {
@@ -114,32 +118,58 @@ __global__ __launch_bounds__(256) void kv4_compact_kernel(const TreeArgs t, cons
     constexpr int kPieces = D / 2 / kU;           // units of a token
     const int P = 1 << c.page_shift;
     const int64_t head_bytes = (int64_t)P * (D + 8);
-    for (int j = 0; j < entries; ++j) {
-        const int node = path[j];
-        if (node <= j || node >= n.len)
-            continue;  // out of range, or where it is already
+    // a lane's bytes of a token: of K, of a V unit, of its parameters
+    const int k_at = 4 * lane, v_at = (D / 2 << c.page_shift) + lane * 4 * kU, p_at = (D << c.page_shift) + (lane & 1) * 4 * P;
+    for (int base = 0; base < entries; base += 64) {
+        const int j = base + lane, node = j < entries ? path[j] : -1;
+        int fp = -1, tp = -1;
         const int from = prefix + node, to = prefix + j;
-        if (to < 0)
-            continue;
-        const int fp = table[from >> c.page_shift], tp = table[to >> c.page_shift];
-        if ((uint32_t)fp >= (uint32_t)c.num_pages || (uint32_t)tp >= (uint32_t)c.num_pages)
-            continue;
-        const int ft = from & (P - 1), tt = to & (P - 1);
-        const uint8_t *src = cache + ((int64_t)fp * c.hkv + head) * head_bytes;
-        uint8_t *dst = cache + ((int64_t)tp * c.hkv + head) * head_bytes;
-        if (lane < D / 8)
-            *(uint32_t *)(dst + tt * (D / 2) + 4 * lane) = *(const uint32_t *)(src + ft * (D / 2) + 4 * lane);
-        if (lane < kPieces) {
-            const int sv = (D / 2 << c.page_shift) + (ft >> 2) * (2 * D) + (ft & 3) * kU + lane * 4 * kU;
-            const int dv = (D / 2 << c.page_shift) + (tt >> 2) * (2 * D) + (tt & 3) * kU + lane * 4 * kU;
-            if constexpr (kU == 2)
-                *(uint16_t *)(dst + dv) = *(const uint16_t *)(src + sv);
-            else
-                *(uint32_t *)(dst + dv) = *(const uint32_t *)(src + sv);
+        if (node > j && node < n.len && to >= 0) {  // else out of range, or where it is already
+            fp = table[from >> c.page_shift];
+            tp = table[to >> c.page_shift];
         }
-        if (lane < 2) {
-            const int at = (D << c.page_shift) + lane * 4 * P;
-            *(uint32_t *)(dst + at + 4 * tt) = *(const uint32_t *)(src + at + 4 * ft);
+        const int at = (from & (P - 1)) | (to & (P - 1)) << 16;  // a page has at most 256 tokens
+        unsigned long long left = __ballot((uint32_t)fp < (uint32_t)c.num_pages && (uint32_t)tp < (uint32_t)c.num_pages);
+        while (left) {
+            uint32_t k[kAhead], v[kAhead], par[kAhead];
+            uint8_t *dst[kAhead];
+            int tt[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int e = left ? __builtin_ctzll(left) : -1;  // uniform
+                left &= left - 1;
+                dst[i] = nullptr;
+                if (e < 0)
+                    continue;
+                const uint8_t *src = cache + ((int64_t)__builtin_amdgcn_readlane(fp, e) * c.hkv + head) * head_bytes;
+                dst[i] = cache + ((int64_t)__builtin_amdgcn_readlane(tp, e) * c.hkv + head) * head_bytes;
+                const int both = __builtin_amdgcn_readlane(at, e), ft = both & 0xffff;
+                tt[i] = both >> 16;
+                if (lane < D / 8)
+                    k[i] = *(const uint32_t *)(src + ft * (D / 2) + k_at);
+                if (lane < kPieces) {
+                    const uint8_t *u = src + v_at + (ft >> 2) * (2 * D) + (ft & 3) * kU;
+                    v[i] = kU == 2 ? *(const uint16_t *)u : *(const uint32_t *)u;
+                }
+                if (lane < 2)
+                    par[i] = *(const uint32_t *)(src + p_at + 4 * ft);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (!dst[i])
+                    break;
+                if (lane < D / 8)
+                    *(uint32_t *)(dst[i] + tt[i] * (D / 2) + k_at) = k[i];
+                if (lane < kPieces) {
+                    uint8_t *u = dst[i] + v_at + (tt[i] >> 2) * (2 * D) + (tt[i] & 3) * kU;
+                    if constexpr (kU == 2)
+                        *(uint16_t *)u = (uint16_t)v[i];
+                    else
+                        *(uint32_t *)u = v[i];
+                }
+                if (lane < 2)
+                    *(uint32_t *)(dst[i] + p_at + 4 * tt[i]) = par[i];
+            }
         }
     }
 }
