@@ -2,13 +2,14 @@
 
 Bounds: masks, positions, paths, tokens and moved bytes are whole numbers and
 equal.  A sampled token's choice lies at a border between two sums; the kernel
-holds each weight to 2^-(F + 1) of the greatest, F = 61 - ceil(log2 vocab), so
-a sum of up to vocab of them to vocab 2^-(F + 1), and two sums that are
-compared to vocab 2^-F of the greatest weight, which all kept ones together are
-not less than: an input whose nearest border is farther than that, relative to
-the kept sum, decides its token (that all inputs here are such ones is
-asserted).  Log probabilities: the logarithm's argument is exact to 2^-24, its
-rounding 2^-24 of itself: 2^-22 (1 + |lp|).
+holds weights as multiples of 2^-F of the greatest, F = min(46, 61 -
+ceil(log2 vocab)): each is off by 2^-(F + 1) for its rounding and by at most
+2^-50 (2^-(F + 4)) before it, so a sum of up to vocab of them by 1.125 vocab
+2^-(F + 1), and two sums that are compared by 1.125 vocab 2^-F of the greatest
+weight, which all kept ones together are not less than: an input whose nearest
+border is farther than that, relative to the kept sum, decides its token (that
+all inputs here are such ones is asserted).  Log probabilities: the logarithm's
+argument is exact to 2^-24, its rounding 2^-24 of itself: 2^-22 (1 + |lp|).
 Attention: the bounds of attn_kv4 (test_gpu_layer.py).
 """
 import math
@@ -190,7 +191,7 @@ def test_kv4_compact_bad_pages(bq, dev):
 # ---------------------------------------------------------------- sampling
 
 def border(vocab):
-    return vocab * 2.0 ** -(61 - math.ceil(math.log2(vocab)))
+    return 1.125 * vocab * 2.0 ** -min(46, 61 - math.ceil(math.log2(vocab)))
 
 
 def check_sample(got, x, u, t=None, k=None, p=None, m=None, exact=False):
@@ -377,6 +378,137 @@ def test_sample_settings_left_out(bq, dev):
     b = bq.sample(x.to(dev), u.to(dev), ones, zeros.int(), ones, zeros)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     check_sample(a, x, u)
+
+
+@pytest.mark.parametrize("vocab", [32759, 32760, 32761, 32762, 32764, 32765, 32766, 32768, 32769, 65536, 65537])
+@pytest.mark.parametrize("T", TYPES + [torch.float32])
+def test_sample_about_the_longest_held_row(bq, dev, T, vocab):
+    banner(f"sample {vocab} {T}")
+    g = gen(vocab)
+    rows = 4
+    room = torch.full((rows, vocab + 9), 99.0, dtype=T, device=dev)
+    for i, filters in enumerate(FILTERS):
+        x = torch.stack([logits_row(g, vocab, 6.0 * (i % 3), T) for i in range(rows)])
+        x[1, :20], x[1, -20:] = x[1, :20] + 4, x[1, -20:] + 4  # the ends count
+        args = sample_settings(g, rows, filters, vocab)
+        room[:, i: i + vocab].copy_(x)
+        check_sample(bq.sample(room[:, i: i + vocab], *(on(v, dev) for v in args)), x, *args)
+
+
+@pytest.mark.parametrize("T", TYPES + [torch.float32])
+@pytest.mark.parametrize("ws", ["auto", "none", "full"])
+@pytest.mark.parametrize("rows,vocab", [(24, 40007), (3, 262147)])
+def test_sample_long_rows(bq, dev, T, ws, rows, vocab):
+    """Rows past a workgroup's registers: other settings in each, off ones and
+    greedy ones, strides and rows off 16-byte boundaries, any workspace."""
+    banner(f"sample long rows {rows} x {vocab} {T} {ws}")
+    g = gen(78)
+    x = torch.stack([logits_row(g, vocab, 9.0 * (i % 4) / 3, T) for i in range(rows)])
+    u, t, k, p, m = sample_settings(g, rows, "kpm", vocab)
+    off = torch.rand(rows, 4, generator=g) < 0.4
+    t, k, p, m = t * ~off[:, 0], k * ~off[:, 1], torch.where(off[:, 2], torch.ones(rows), p), m * ~off[:, 3]
+    kw = {}
+    if ws == "none":
+        kw["workspace"] = torch.empty(16, dtype=torch.uint8, device=dev)
+    elif ws == "full":
+        kw["workspace"] = torch.full((bq.sample_workspace_bytes(rows, vocab, T),), 255, dtype=torch.uint8, device=dev)
+    for lead, tail in ((0, 0), (1, 2), (3, 10)):
+        room = torch.full((rows, lead + vocab + tail), 99.0, dtype=T, device=dev)
+        view = room[:, lead: lead + vocab]
+        view.copy_(x)
+        check_sample(bq.sample(view, *(on(v, dev) for v in (u, t, k, p, m)), **kw), x, u, t, k, p, m)
+
+
+@pytest.mark.parametrize("T", TYPES + [torch.float32])
+@pytest.mark.parametrize("vocab", [3001, 40000])
+def test_sample_top_k_of_any_size(bq, dev, T, vocab):
+    """Up to and past the numbers of groups, of threads and of listed tokens."""
+    banner(f"sample top-k {vocab} {T}")
+    g = gen(20)
+    k = [v for v in (1, 2, 63, 64, 65, 255, 256, 257, 1000, 1023, 1024, 1025, 2999, 3000, 3001, 6144, 6145, 20000, 39999) if v <= vocab]
+    x = torch.stack([logits_row(g, vocab, 3.0, T) for _ in k])
+    for filters in ("", "p", "m"):
+        u, t, _, p, m = sample_settings(g, len(k), filters, vocab)
+        args = (u, t, torch.tensor(k, dtype=torch.int32), p, m)
+        check_sample(bq.sample(x.to(dev), *(on(v, dev) for v in args)), x, *args)
+
+
+@pytest.mark.parametrize("T", TYPES + [torch.float32])
+@pytest.mark.parametrize("vocab", [30000, 50003])
+def test_sample_crowded(bq, dev, T, vocab):
+    """Tokens that crowd where the limit lies, in the whole row or in a run of it:
+    more than are listed.  A long tail of equal weights beside one token."""
+    banner(f"sample crowded {vocab} {T}")
+    g = gen(21)
+    rows = []
+    rows.append(torch.randn(vocab, generator=g) * 0.01)
+    rows.append(torch.randn(vocab, generator=g) * 2)
+    rows[-1][7000:10000] = 6 + torch.rand(3000, generator=g) * 0.02
+    rows.append(torch.randn(vocab, generator=g) * 2)
+    rows[-1][vocab - 6200:] = 5.0
+    rows.append(torch.full((vocab,), -9.0))
+    rows[-1][vocab // 2] = 3.0
+    rows.append(torch.rand(vocab, generator=g) * 1e-3)
+    rows.append(torch.linspace(-20, 0, vocab))
+    x = torch.stack(rows).to(T)
+    n = len(rows)
+    for filters in FILTERS:
+        for _ in range(3):
+            args = sample_settings(g, n, filters, vocab)
+            check_sample(bq.sample(x.to(dev), *(on(v, dev) for v in args)), x, *args)
+
+
+@pytest.mark.parametrize("T", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [3000, 70001])
+def test_sample_captured(bq, dev, T, vocab):
+    """Two captured calls with workspaces of their own, replayed side by side with
+    other logits and settings, equal the definition and the eager call."""
+    banner(f"sample captured {vocab} {T}")
+    g = gen(22)
+    rows = 6
+    sets, graphs = [], []
+    for i in range(2):
+        new = lambda T, *shape: torch.ones(*shape, dtype=T, device=dev)  # noqa: E731
+        s = dict(x=new(T, rows, vocab), u=new(torch.float32, rows) * 0.5, t=new(torch.float32, rows), k=new(torch.int32, rows),
+                 p=new(torch.float32, rows), m=new(torch.float32, rows), tokens=new(torch.int32, rows),
+                 logprobs=new(torch.float32, rows),
+                 ws=torch.empty(max(16, bq.sample_workspace_bytes(rows, vocab, T)), dtype=torch.uint8, device=dev))
+        sets.append(s)
+
+    def call(s):
+        return bq.sample(s["x"], s["u"], s["t"], s["k"], s["p"], s["m"], s["tokens"], s["logprobs"], s["ws"])
+
+    for s in sets:
+        call(s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(s)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for filters in ("kpm", "p", "k", "", "pm"):
+        given = []
+        for s in sets:
+            x = torch.stack([logits_row(g, vocab, 4.0, T) for _ in range(rows)])
+            u, t, k, p, m = sample_settings(g, rows, filters, vocab)
+            k = torch.zeros(rows, dtype=torch.int32) if k is None else k
+            p = torch.ones(rows) if p is None else p
+            m = torch.zeros(rows) if m is None else m
+            for name, v in zip(("x", "u", "t", "k", "p", "m"), (x, u, t, k, p, m)):
+                s[name].copy_(v)
+            s["tokens"].fill_(-7)
+            given.append((x, u, t, k, p, m))
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for s, args in zip(sets, given):
+            check_sample((s["tokens"], s["logprobs"]), *args)
+            first = s["tokens"].clone(), s["logprobs"].clone()
+            call(s)
+            torch.cuda.synchronize()
+            assert torch.equal(first[0], s["tokens"]) and torch.equal(first[1], s["logprobs"])
 
 
 # ---------------------------------------------------------------- attention over a tree
