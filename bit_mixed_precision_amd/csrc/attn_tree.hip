@@ -648,8 +648,22 @@ AttnKv4Plan attn_tree_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv
     // 2000 (2^25) 38.5 and 35.6, 1 of 128 nodes before 8000 (2^25) 39.7 and 48.8,
     // 8 x 64 of 8192 95 and 115.
     const int64_t rows = max_q_len * (q_heads / kv_heads);
-    if (D > 128 || rows <= 64 || (double)batch * kv_heads * rows * max_len < (D == 128 ? 3 << 24 : 1 << 25))
-        return attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, D, max_len);
+    if (D > 128 || rows <= 64 || (double)batch * kv_heads * rows * max_len < (D == 128 ? 3 << 24 : 1 << 25)) {
+        AttnKv4Plan a = attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, D, max_len);
+        // Where 16 rows a workgroup still leave CUs free: they let eight wavefronts
+        // have the keys, and no split is needed up to a length (8 kv heads; 1 tree
+        // of 8 x 4 rows, 200 keys 7.0 us against 9.7, 700 10.1 against 15.2, 1000
+        // 11.6 against 18.0, 1500 13.8 against 13.3 split; 4 of 32 x 4, 1500 17.7
+        // against 25.4, 2000 21.3 against 27.3).
+        const int64_t tiles = (rows + 15) / 16, items = batch * kv_heads * tiles;
+        if (D == 128 && a.rt == 2 && items <= 256 && max_len <= (items >= 128 ? 2048 : 1024)) {
+            a.rt = 1;
+            a.row_tiles = tiles;
+            a.nsplit = 1;
+            a.part_rows = 0;
+        }
+        return a;
+    }
     // 256 rows a workgroup, one a CU (16 x 64 nodes x 4 heads before 3000 keys 101
     // us, with 128 rows, two a CU, 108), or 128 where that leaves out a sixth of
     // the rows (130 x 4 rows before 8000 keys 158 us against 200; 275 x 4 161
