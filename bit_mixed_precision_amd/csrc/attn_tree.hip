@@ -18,14 +18,14 @@
 // Pieces of 16 bytes are permuted within their rows (by the row's number) so that
 // the 16 lanes of a cycle meet all banks.
 //
-// Per key and row the vector ALUs have 11.5 issue slots (the two-term fix-up 2,
-// maximum 0.5, exponent 1 + 4, both sums 2, weight and its rounding 2), the matrix
-// cores 4 D operations (an fp16 output's two-part weights: 6 D).  8 trees of 64
-// nodes x 4 heads a kv head before 8192 keys, D = 128, bf16: 117 us and 10 for the
-// join, of which the ALUs work for 60 %, LDS for 55 % and the matrix cores for
-// 28 % (550 TFLOP/s).  Four wavefronts a SIMD of 16 rows, which fit 128 registers,
-// are as fast at D = 128 as two of 32 rows with half the reads of LDS, and faster
-// at D = 64 (4 x 64 nodes of 8000 keys: 45 against 51 us).
+// Per key and row the vector ALUs have 10.5 issue slots (the two-term fix-up 2,
+// maximum 0.5, exponent 1 + 4, both sums 2, weight with its rounding 1), the matrix
+// cores 4 D operations (an fp16 output's two-part weights: 2 slots and 2 D more).
+// 8 trees of 64 nodes x 4 heads a kv head before 8192 keys, D = 128, bf16: 121 us
+// and 8.5 for the join, of which the ALUs work for 60 %, LDS for 55 % and the
+// matrix cores for 28 % (570 TFLOP/s).  Four wavefronts a SIMD of 16 rows, which
+// fit 128 registers, are as fast at D = 128 as two of 32 rows with half the reads
+// of LDS, and faster at D = 64 (4 x 64 nodes of 8000 keys: 45 against 51 us).
 #include "attn_kv4.h"
 
 namespace bq {

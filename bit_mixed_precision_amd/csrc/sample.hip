@@ -23,9 +23,14 @@
 //   draw       one workgroup a row: ends the kept ones of the listed tokens; the
 //              sums over the others give the part of the row that the drawn token
 //              is in, which is read again.
-// The one kernel takes the same steps.  Without a workspace, where a list is too short (a row of equal logits), and for
-// a greater top_k, one workgroup selects over the row itself, eight bits of key at
-// a time.
+// The one kernel takes the same steps.  Without a workspace, where a list is too
+// short (a row of equal logits), and for a greater top_k, one workgroup selects
+// over the row itself, eight bits of key at a time.
+//
+// 1 x 32000 fp16 in the one kernel 21.7 us (in the four 28.4); 64 x 131072 bf16 with
+// top-p: greatest 8.3, weigh 15.6 (25 operations in 64 bits a token), gather 13.7,
+// draw 26.8; 487 x 100003 fp32 with all settings: 43 (4.5 TB/s), 53, 17, 41.  One
+// workgroup a row, each over the whole of it: 139, 528 and 1083.
 //
 // Most of a draw's time is one workgroup's way through code and dependent loads:
 // code that runs once costs the instructions' way from memory, so loops are not
