@@ -1182,3 +1182,60 @@ def test_attn_kv4_tree_shared_captured(bq, dev):
             call(s)
             torch.cuda.synchronize()
             assert torch.equal(eager[0], s["out"]) and torch.equal(eager[1], s["lse"])
+
+
+# ---------------------------------------------------------------- past 32 bits
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_kv4_tree_past_32_bits(bq, dev, T, wide):
+    """Pages that lie past 4 GiB of the cache."""
+    banner(f"tree attention past 32 bits {wide} {T}")
+    hq, hkv, d, page, nodes, lens = 64, 8, 128, 16, 20, [333, 90]
+    g = gen(31)
+    cache = make_cache(g, 30, hkv, d, page, T)
+    flat = cache.flat()
+    off = (1 << 32) // flat.shape[1] + 1
+    big = torch.zeros(off + 30, flat.shape[1], dtype=torch.uint8, device=dev)
+    big[off:] = flat.to(dev)
+    tab = tables(g, lens, page, 30)
+    _, see, mask, _ = trees(g, [nodes] * 2)
+    q = torch.randn(2 * nodes, hq, d, generator=g).to(T)
+    got = (wide_run if wide else run_tree)(bq, dev, q, big, tab + off, lens, hkv, page, mask)
+    check_tree(got, q, cache, tab, lens, [0, nodes, 2 * nodes], see, what="past 32 bits")
+
+
+def test_kv4_compact_past_32_bits(bq, dev):
+    """Pages past 4 GiB of a layer, layers further than that apart."""
+    banner("compact past 32 bits")
+    hkv, d, page, nodes, lens = 8, 64, 16, 12, [50, 31]
+    g = gen(32)
+    layers = [make_cache(g, 9, hkv, d, page, torch.float16) for _ in range(2)]
+    size = layers[0].flat().shape[1]
+    off = (1 << 32) // size + 1
+    big = torch.zeros(2, off + 9, size, dtype=torch.uint8, device=dev)
+    for i, c in enumerate(layers):
+        big[i, off:] = c.flat().to(dev)
+    tab = tables(g, lens, page, 9)
+    path, count = [[0, 2, 5, 11, -1], [0, 1, 7, -1, -1]], [4, 3]
+    bq.kv4_compact(big, (tab + off).to(dev), i32(lens, dev), i32(path, dev), i32(count, dev), page, hkv, d, max_q_len=nodes)
+    for i, c in enumerate(layers):
+        for b, n in enumerate(lens):
+            decode.compact(c, tab[b], n, nodes, path[b][: count[b]])
+        assert torch.equal(big[i, off:].cpu(), c.flat())
+        assert not big[i, :off].any()
+
+
+@pytest.mark.parametrize("vocab", [1000, 40001])
+def test_sample_past_32_bits(bq, dev, vocab):
+    """Rows that lie past 4 GiB of the logits."""
+    banner(f"sample past 32 bits {vocab}")
+    g = gen(33)
+    rows, stride = 3, (1 << 31) + 1
+    x = torch.stack([logits_row(g, vocab, 4.0, torch.bfloat16) for _ in range(rows)])
+    room = torch.empty(stride * (rows - 1) + vocab, dtype=torch.bfloat16, device=dev)
+    view = room.as_strided((rows, vocab), (stride, 1))
+    view.copy_(x)
+    for filters in ("", "p", "kpm"):
+        args = sample_settings(g, rows, filters, vocab)
+        check_sample(bq.sample(view, *(on(v, dev) for v in args)), x, *args)
