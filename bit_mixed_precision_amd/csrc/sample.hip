@@ -16,7 +16,8 @@
 //   greatest   the greatest logit of every group of a row's lanes;
 //   weigh      a row with a top_k of at most as many as there are groups: no
 //              token below the top_k-th greatest group can be kept, those from
-//              it on, a few more than top_k, are listed.  Another row: the units
+//              it on, a few more than top_k, are listed, of the few lanes only
+//              whose greatest logit is one of them.  Another row: the units
 //              of each eighth of an octave of weight, per workgroup and row;
 //   gather     lists the tokens of the eighth of an octave in which such a row's limit
 //              lies;
@@ -28,9 +29,10 @@
 // over the row itself, eight bits of key at a time.
 //
 // 1 x 32000 fp16 in the one kernel 21.7 us (in the four 28.4); 64 x 131072 bf16 with
-// top-p: greatest 8.3, weigh 15.6 (25 operations in 64 bits a token), gather 13.7,
-// draw 26.8; 487 x 100003 fp32 with all settings: 43 (4.5 TB/s), 53, 17, 41.  One
-// workgroup a row, each over the whole of it: 139, 528 and 1083.
+// top-p: greatest 8.4, weigh 15.7 (25 operations in 64 bits a token), gather 13.8,
+// draw 25.5; 487 x 100003 fp32 with all settings: 45 (4.3 TB/s), 31 (all lanes'
+// vectors, and the limit by ranks of the groups: 53), 17, 39.  One workgroup a row,
+// each over the whole of it: 139, 528 and 1083.
 //
 // Most of a draw's time is one workgroup's way through code and dependent loads:
 // code that runs once costs the instructions' way from memory, so loops are not
@@ -355,18 +357,25 @@ __device__ __forceinline__ u64 block_sum(Shared &sh, u64 v)
 }
 
 // Sorts n <= kThreads different numbers in LDS, the greatest first, by counting
-// the greater ones of each.
+// the greater ones of each, by up to eight lanes a number.
 __device__ __forceinline__ void sort_few(u64 *x, int n)
 {
-    const u64 mine = (int)threadIdx.x < n ? x[threadIdx.x] : 0;
+    int shift = 0;
+    while (shift < 3 && n << (shift + 1) <= kThreads)
+        ++shift;
+    const int number = threadIdx.x >> shift, lanes = 1 << shift;
+    const u64 mine = number < n ? x[number] : 0;
     int rank = 0;
-    if ((int)threadIdx.x < n) {
+    if (number < n) {
 #pragma unroll 8
-        for (int i = 0; i < n; ++i)
+        for (int i = threadIdx.x & (lanes - 1); i < n; i += lanes)
             rank += x[i] > mine;
     }
+#pragma unroll 1
+    for (int off = 1; off < lanes; off <<= 1)
+        rank += __shfl_xor(rank, off, 64);
     __syncthreads();
-    if ((int)threadIdx.x < n)
+    if (number < n && (threadIdx.x & (lanes - 1)) == 0)
         x[rank] = mine;
     __syncthreads();
 }
@@ -900,6 +909,7 @@ struct Parts {
     int lanes;    // of a group: 16 or 64
     int groups;
     uint32_t *greatest;  // [rows][groups]
+    uint32_t *highest;   // [rows][64 waves]: the greatest logit's key of each lane's vectors
     u64 *first;          // [rows][waves / kPart]: greatest key and its first place (order_of)
     u64 *list;           // [rows][kList]: tokens (order_of)
     uint32_t *length;    // [rows]
@@ -919,7 +929,6 @@ struct PartVectors {
     __device__ __forceinline__ PartVectors(const Row<TYPE> &r, const Parts &q, int wave)
         : row(r), first(wave * q.steps * 64 + (int)(threadIdx.x & 63)), steps(q.steps), n(r.vectors())
     {
-        load(0);
     }
     __device__ __forceinline__ void load(int st)
     {
@@ -928,7 +937,7 @@ struct PartVectors {
             if (st + i < steps && first + (st + i) * 64 < n)
                 x[i] = row.load(first + (st + i) * 64);
     }
-    // f(vector, x), once
+    // f(vector, x), once, after load(0)
     template <typename F>
     __device__ __forceinline__ void each(F f)
     {
@@ -978,6 +987,7 @@ __global__ __launch_bounds__(64 * kPart) void greatest_kernel(const SampleArgs p
                     }
                 }
     }
+    q.highest[((int64_t)b * q.waves + wave) * 64 + lane] = key;
     uint32_t g = key;
 #pragma unroll 1
     for (int off = 1; off < q.lanes; off <<= 1)
@@ -1034,9 +1044,6 @@ template <int TYPE>
 __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, const Parts q)
 {
     constexpr int E = Row<TYPE>::kE;
-    static_assert(kGroups == 64 * kPart, "a thread a group");
-    __shared__ uint32_t groups[kGroups];
-    __shared__ uint32_t low;
     __shared__ Found found;
     u64 *const units = found.token;  // of one of which there is need
     static_assert(kOct <= kFound, "units share the list's place");
@@ -1050,28 +1057,39 @@ __global__ __launch_bounds__(64 * kPart) void weigh_kernel(const SampleArgs p, c
     const Row<TYPE> row(p, b);
     PartVectors<TYPE> vectors(row, q, wave);
     if (lists) {
-        // the top_k-th greatest group: at least top_k tokens are as great
-        const uint32_t mine = (int)threadIdx.x < q.groups ? q.greatest[(int64_t)b * q.groups + threadIdx.x] : 0u;
-        groups[threadIdx.x] = mine;
+        const uint32_t highest = q.highest[((int64_t)b * q.waves + wave) * 64 + lane];
+        // A limit that top_k groups' greatest reach, so that at least top_k tokens do:
+        // 19 bits of the top_k-th greatest (all that 16-bit logits have), by every
+        // wavefront for itself.
+        uint32_t group[kGroups / 64], low = 0;
+#pragma unroll
+        for (int i = 0; i < kGroups / 64; ++i)
+            group[i] = lane + 64 * i < q.groups ? q.greatest[(int64_t)b * q.groups + lane + 64 * i] : 0u;
         if (threadIdx.x == 0)
             found.count = 0;
         __syncthreads();
-        int rank = 0;
-#pragma unroll 8
-        for (int i = 0; i < q.groups; ++i)
-            rank += groups[i] > mine || (groups[i] == mine && i < (int)threadIdx.x);
-        if ((int)threadIdx.x < q.groups && rank == set.top_k - 1)
-            low = mine;
-        __syncthreads();
-        const float least = value_of(max(low, kNone + 1));
-        vectors.each([&](int v, const u4 &x) {
-            const uint32_t on = row.at_least(x, least);
-            if (on)
-                found.add(row, v, x, on);
-        });
+#pragma unroll 1
+        for (uint32_t bit = 1u << 31; bit >= 1u << 13; bit >>= 1) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kGroups / 64; ++i)
+                n += __popcll(__ballot(group[i] >= (low | bit)));
+            low |= n >= set.top_k ? bit : 0;
+        }
+        const uint32_t limit = max(low, kNone + 1);
+        const float least = value_of(limit);
+        if (highest >= limit) {  // of few lanes: what the others have is not read again
+            vectors.load(0);
+            vectors.each([&](int v, const u4 &x) {
+                const uint32_t on = row.at_least(x, least);
+                if (on)
+                    found.add(row, v, x, on);
+            });
+        }
         found.list(q, b);
         return;
     }
+    vectors.load(0);  // on their way meanwhile
     const u64 top = wave_max(lane < q.parts() ? q.first[(int64_t)b * q.parts() + lane] : 0);
     if (key_in(top) <= kNone)
         return;
@@ -1111,6 +1129,7 @@ __global__ __launch_bounds__(64 * kPart) void gather_kernel(const SampleArgs p, 
         return;
     const Row<TYPE> row(p, b);
     PartVectors<TYPE> vectors(row, q, wave);
+    vectors.load(0);
     const u64 top = wave_max(lane < q.parts() ? q.first[(int64_t)b * q.parts() + lane] : 0);
     if (key_in(top) <= kNone)
         return;
@@ -1241,6 +1260,7 @@ int64_t place(Parts &q, int64_t rows, uint8_t *at)
     take(q.sums, rows * kOct);
     take(q.first, rows * q.parts());
     take(q.greatest, rows * q.groups);
+    take(q.highest, rows * q.waves * 64);
     take(q.length, rows);
     return at - start;
 }
