@@ -560,6 +560,7 @@ __device__ __noinline__ void draw_row(Shared &sh, const SampleArgs &p, int b)
     u64 first = 0;
     row.each([&](int i, uint32_t k) { first = max(first, order_of(k, i)); });
     first = wave_max(first);
+    __syncthreads();  // a caller's wavefronts may still read sh
     if ((threadIdx.x & 63) == 0)
         sh.sums[threadIdx.x >> 6] = first;
     fill_mid(sh.mid, p.frac);
