@@ -65,14 +65,18 @@ __device__ __forceinline__ int k_piece(int r, int c)
 }
 __device__ __forceinline__ int v_piece(int r, int c) { return r * 128 + (c ^ (r >> 1 & 7)) * 16; }
 
-// What the keys of a step have beside their codes.
-struct Params {
+// What the keys of a step have beside their codes.  Two of them lie one behind
+// the other, read and written in 8 and 16 bytes.
+struct alignas(16) Params {
     uint32_t there[2], bad[2];  // a bit a key: in the cache; V's parameters are no numbers
     uint32_t k[kKeys];          // sk, mk
     float mv[kKeys];            // mv + 8 sv
     uint16_t sv[kKeys];
     int top;                    // the greatest |sv|, its bits
 };
+static_assert(sizeof(Params) % 16 == 0 && offsetof(Params, there) % 16 == 0 && offsetof(Params, bad) % 8 == 0 &&
+                  offsetof(Params, k) % 16 == 0 && offsetof(Params, mv) % 16 == 0 && offsetof(Params, sv) % 8 == 0,
+              "vectors of 8 and 16 bytes");
 
 // Sequence b's nodes and keys: all its rows have the same.
 __device__ __forceinline__ Rows tree_rows(const AttnKv4Args &p, int b)
@@ -191,7 +195,7 @@ __global__ __launch_bounds__(64 * W, 4) void attn_tree_kernel(const AttnKv4Args 
     constexpr bool kLow = !T::kBf16;
     constexpr int kBuf = kKeys * D * 2;               // bytes of a step's operands, K and V each: a power of two
     __shared__ __attribute__((aligned(16))) uint8_t lk[2 * kBuf], lv[2 * kBuf];
-    __shared__ __attribute__((aligned(16))) Params params[2];
+    __shared__ Params params[2];
     const int tid = threadIdx.x, lane = tid & 63, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int head = blockIdx.x % p.hkv, tile = blockIdx.x / p.hkv % p.row_tiles;
