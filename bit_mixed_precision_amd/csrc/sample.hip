@@ -40,6 +40,11 @@
 #include "bq_decode_internal.h"
 #include "dtype16.h"
 
+// A token's weight has the same bits wherever it is computed (a part's sum and the
+// row that is read again for the drawn token have to agree to the last unit): products
+// and sums are fused only where fma is written.
+#pragma clang fp contract(off)
+
 namespace bq {
 namespace {
 
