@@ -478,20 +478,21 @@ __device__ __forceinline__ void answer_first(const SampleArgs &p, int b, u64 fir
     const bool none = key_in(first) <= kNone;
     answer(p, b, none ? -1 : index_in(first), none ? -__builtin_inff() : 0.0f);
 }
-// With n of `total` units: by the smaller of the token and the others, so that
-// its rounding is one of the logarithm.
-__device__ __forceinline__ void answer_units(const SampleArgs &p, int b, int token, u64 n, u64 total)
+// A token q eighths of octaves below the greatest, of `total` kept units.  Its log
+// probability comes from q and not from its units, of which a light token that a
+// random number near 0 draws has only a few; in 64 bits, rounded once.
+__device__ __forceinline__ void answer_token(const SampleArgs &p, int b, int token, double q, u64 total)
 {
-    const bool most = n > total - n;
-    const float x = (float)((double)(most ? total - n : n) / (double)total);
-    answer(p, b, token, most ? log1pf(-x) : logf(x));
+    constexpr double l = 0.693147180559945309417 / 8;
+    const double all = (double)total * __hiloint2double((1023 - p.frac) << 20, 0);  // over the greatest, at least 1
+    answer(p, b, token, (float)(0.0 - (q * l + log(all))));
 }
 
 // Draws the token at which the kept units, in the order of indices, pass `want`,
 // among vectors [first, last), before which `sum` of them lie.
 template <int TYPE, typename Kept>
-__device__ __forceinline__ void draw_from(Shared &sh, const SampleArgs &p, int b, const Row<TYPE> &row, int first, int last,
-                                          Kept kept, u64 want, u64 sum, u64 total)
+__device__ __forceinline__ void draw_from(Shared &sh, const SampleArgs &p, int b, const Row<TYPE> &row, const Scale &s,
+                                          int first, int last, Kept kept, u64 want, u64 sum, u64 total)
 {
     for (int v0 = first; v0 < last; v0 += kThreads) {
         const int v = v0 + threadIdx.x;
@@ -507,7 +508,7 @@ __device__ __forceinline__ void draw_from(Shared &sh, const SampleArgs &p, int b
             row.each_token(v, x, [&](int i, uint32_t k) {
                 const u64 n = kept(i, k);
                 if (upto <= want && upto + n > want)
-                    answer_units(p, b, i, n, total);
+                    answer_token(p, b, i, s.eighths(k), total);
                 upto += n;
             });
         }
@@ -554,7 +555,7 @@ __device__ __forceinline__ void draw_slowly(Shared &sh, const SampleArgs &p, int
         const double q = s.eighths(k);
         return q <= far ? s.units(q) : 0;
     };
-    draw_from(sh, p, b, row, 0, row.vectors(), kept, set.pass(total), 0, total);
+    draw_from(sh, p, b, row, s, 0, row.vectors(), kept, set.pass(total), 0, total);
 }
 
 // A row without what other kernels found.
@@ -665,8 +666,8 @@ __device__ __forceinline__ Limit end_edge(Shared &sh, u64 *few, Tokens tokens, c
 }
 
 // Draws from n <= kThreads tokens, among which all that are kept are: sorts them,
-// ends the kept ones, sorts these by index.
-__device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b, u64 *few, u64 *units, int n, const Scale &s,
+// ends the kept ones, sorts these by index; `down` keeps their eighths of octaves.
+__device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b, u64 *few, u64 *down, int n, const Scale &s,
                                          const Settings &set)
 {
     const int i = threadIdx.x;
@@ -687,16 +688,17 @@ __device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b,
             sum = block_scan(sh, mine, total);
             if ((set.has_p && sum - mine >= set.reach(total)) || eighths > set.far())
                 mine = 0;
-            units[i] = mine;
+            down[i] = (u64)__double_as_longlong(eighths);
             n = __syncthreads_count(mine > 0);  // the kept ones are the first
             few[i] = mine ? order_of(~(uint32_t)place, i) : 0;
             __syncthreads();
         } else {
-            mine = i < n ? units[index_in(x)] : 0;
+            const double eighths = i < n ? __longlong_as_double((long long)down[index_in(x)]) : 0.0;
+            mine = i < n ? s.units(eighths) : 0;
             sum = block_scan(sh, mine, total);
             const u64 want = set.pass(total);
             if (sum > want && sum - mine <= want)
-                answer_units(p, b, (int)~key_in(x), mine, total);
+                answer_token(p, b, (int)~key_in(x), eighths, total);
             return;
         }
     }
@@ -705,7 +707,7 @@ __device__ __forceinline__ void draw_few(Shared &sh, const SampleArgs &p, int b,
 // Draws from listed tokens, of which top-k keeps at most kThreads.
 template <typename Tokens>
 __device__ __forceinline__ void draw_listed(Shared &sh, const SampleArgs &p, int b, Tokens tokens, int length, u64 *few,
-                                            u64 *units, const Scale &s, const Settings &set)
+                                            u64 *down, const Scale &s, const Settings &set)
 {
     Limit limit = {kNone, 0};
     if (length > kThreads)
@@ -719,7 +721,7 @@ __device__ __forceinline__ void draw_listed(Shared &sh, const SampleArgs &p, int
             few[atomicAdd(&sh.count, 1)] = order_of(k, i);
     });
     __syncthreads();
-    draw_few(sh, p, b, few, units, sh.count, s, set);
+    draw_few(sh, p, b, few, down, sh.count, s, set);
 }
 
 // A row that a workgroup holds in registers, NV vectors a thread.
@@ -895,7 +897,7 @@ __global__ __launch_bounds__(kThreads) void sample_held_kernel(const SampleArgs 
             row.each_token(v, held[0], [&](int i, uint32_t k) {
                 const u64 units = kept(i, k);
                 if (upto <= want && upto + units > want)
-                    answer_units(p, b, i, units, total);
+                    answer_token(p, b, i, s.eighths(k), total);
                 upto += units;
             });
         }
@@ -1234,7 +1236,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs p, cons
     const u64 here = lane < parts ? amount[lane] : 0, upto = wave_scan(here), total = __shfl(upto, 63, 64);
     const u64 want = set.pass(total);
     const int part = __ffsll((u64)__ballot(upto > want)) - 1;
-    draw_from(sh, p, b, row, part * part_vectors, min((part + 1) * part_vectors, row.vectors()), kept, want,
+    draw_from(sh, p, b, row, s, part * part_vectors, min((part + 1) * part_vectors, row.vectors()), kept, want,
               __shfl(upto - here, part, 64), total);
 }
 

@@ -114,9 +114,10 @@ int64_t bq_attn_kv4_tree_workspace_bytes(int64_t batch, int64_t max_q_len, int q
  *                none (one workgroup a row then does all of its work).  Calls
  *                that share one must not overlap.
  * Weights are held as multiples of 2^-F of the greatest one, F = min(46, 61 -
- * ceil(log2 vocab)), from a 64-bit exponential; their sums are exact, so that the
- * result does not depend on the order in which they are taken, nor on the
- * workspace.
+ * ceil(log2 vocab)), from a 64-bit exponential, and one that rounds to 0 is not
+ * drawn; their sums are exact, so that the result does not depend on the order in
+ * which they are taken, nor on the workspace.  In a log probability only the sum
+ * is of such multiples; w is the logit's own, however small.
  * 0 <= rows <= BQ_MAX_DIM, 1 <= vocab <= 2^24 (BQ_ERR_SHAPE); logits aligned to
  * their type.
  */

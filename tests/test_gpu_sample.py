@@ -75,3 +75,38 @@ def test_every_unit_of_a_row_is_found_again(bq, dev, T, rows, vocab):
             assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
             # 1 and NaN draw the last kept token whatever the sums are
             check_sample(got[0], x, u, t, k, p, m, exact=last != 1 - 2.0 ** -24)
+
+
+@pytest.mark.parametrize("T", TYPES + [torch.float32])
+@pytest.mark.parametrize("vocab", [50, 20011, 60013])
+@pytest.mark.parametrize("ws", ["auto", "none"])
+def test_log_probability_of_a_light_token(bq, dev, T, vocab, ws):
+    """A random number of 0 draws the first kept token, however little it weighs:
+    here e^-5 to e^-30.5 of the greatest, down to a few of the units that sums are
+    held in.  Its log probability is (x - max) / t less the logarithm of the kept
+    weights' sum, over the greatest.  The sum is off by less than 1.125 vocab
+    2^-(F + 1) of the greatest (F as in test_gpu_decode.py), which it is not less
+    than, and so is its logarithm; the other term, at most 31 here, by a few 2^-52
+    of itself, below 2^-40; the result is rounded to fp32, 2^-24 of itself."""
+    banner(f"sample: a light token {vocab} {T} {ws}")
+    down = [5.0, 12.0, 17.0, 20.25, 25.0, 28.0, 30.5]
+    x = torch.full((len(down), vocab), -1000.0)
+    x[:, vocab // 2], x[:, vocab // 2 + 1] = 0.0, -0.75
+    x[:, 3] = -torch.tensor(down)
+    x = x.to(T)
+    rows = len(down)
+    kw = {} if ws == "auto" else dict(workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+    frac = min(46, 61 - math.ceil(math.log2(vocab)))
+    u = torch.zeros(rows)
+    for t in (1.0, 0.5, 2.0):
+        xt = (x.float() * t).to(T)  # whole powers of two: the same weights
+        temp = torch.full((rows,), t)
+        for k in (None, 3, 45):
+            top_k = None if k is None else torch.full((rows,), k, dtype=torch.int32)
+            tokens, logp = bq.sample(xt.to(dev), u.to(dev), temp.to(dev), on(top_k, dev), **kw)
+            assert tokens.tolist() == [3] * rows
+            w = np.exp((xt.float().numpy().astype(np.longdouble) - xt.float().amax(1, True).numpy()) / np.longdouble(t))
+            kept = np.sort(w, 1)[:, -(k or vocab):].sum(1)
+            want = np.log(w[:, 3] / kept).astype(np.float64)
+            off = np.abs(logp.cpu().numpy().astype(np.float64) - want)
+            assert (off <= 2.0 ** -24 * np.abs(want) + 1.125 * vocab * 2.0 ** -(frac + 1) + 2.0 ** -40).all(), off
