@@ -123,9 +123,13 @@ def select_path(M: int, N: int, K: int, bits: int) -> str:
 # marshalling helpers
 # --------------------------------------------------------------------------
 
-def _check_tensor(t: torch.Tensor, name: str, dtype, shape=None, device=None):
+def _is_tensor(t, name: str):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _check_tensor(t: torch.Tensor, name: str, dtype, shape=None, device=None):
+    _is_tensor(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -780,6 +784,8 @@ def tree_mask(parents: torch.Tensor, seq_lens: Optional[torch.Tensor] = None, q_
     32 of word j / 32 of a row: the node sees node j, itself or an ancestor of
     its.  position = seq_len - q_len + depth with seq_lens int32 [batch], the
     keys in the cache with the nodes, else the depth."""
+    if mask is not None:
+        _is_tensor(mask, "mask")
     dev, batch, total, most, starts = _tree_nodes(parents, "parents", q_start, max_q_len)
     par = _dense(parents, "parents", torch.int32, None, dev)
     lens = None if seq_lens is None else _dense(seq_lens, "seq_lens", torch.int32, (batch,), dev)
@@ -878,14 +884,18 @@ def tree_accept(tokens: torch.Tensor, parents: torch.Tensor, sampled: torch.Tens
     was sampled at its parent, then -1; count int32 [batch]; next_token int32
     [batch], what was sampled at the path's last node).  max_path None: the most
     nodes of a tree."""
+    if path is not None:
+        _is_tensor(path, "path")
     dev, batch, total, most, starts = _tree_nodes(tokens, "tokens", q_start, max_q_len)
     tok = _dense(tokens, "tokens", torch.int32, None, dev)
     par = _dense(parents, "parents", torch.int32, tokens.shape, dev)
     if not isinstance(sampled, torch.Tensor):
         raise TypeError("sampled must be a torch.Tensor")
     drawn = _dense(sampled, "sampled", torch.int32, tokens.shape if sampled.dim() == tokens.dim() else (total,), dev)
+    if path is not None and path.dim() != 2:
+        raise ValueError("path must be 2-D [batch, max_path]")
     if max_path is None:
-        max_path = max(1, most) if path is None else path.shape[-1]
+        max_path = max(1, most) if path is None else path.shape[1]
     path, pp = _output(path, "path", torch.int32, (batch, max_path), dev)
     count, pc = _output(count, "count", torch.int32, (batch,), dev)
     next_token, pn = _output(next_token, "next_token", torch.int32, (batch,), dev)
@@ -902,7 +912,9 @@ def kv4_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.
     max_q_len each, or by q_start int32 [batch + 1] over total_q nodes.  cache
     [num_pages, page bytes], or [layers, num_pages, page bytes] for all layers
     in one call (its layers may lie apart) -> cache, changed in place."""
-    if not isinstance(cache, torch.Tensor) or cache.dim() not in (2, 3):
+    for t, name in ((cache, "cache"), (block_table, "block_table"), (path, "path")):
+        _is_tensor(t, name)
+    if cache.dim() not in (2, 3):
         raise ValueError("cache must be a tensor [num_pages, page bytes] or [layers, num_pages, page bytes]")
     dev = cache.device
     layers, stride = 1, 0

@@ -173,3 +173,21 @@ def test_python_arguments_are_checked(bq):
         bq.attn_kv4_tree(x, torch.zeros(2, 2 * 16 * 136, dtype=torch.uint8), i32, flat[:2], 16, 2, None)
     with pytest.raises(ValueError):
         bq.attn_kv4_tree(x, torch.zeros(2, 2 * 16 * 136, dtype=torch.uint8), i32, flat[:2], 16, 2, i32)
+
+
+@pytest.mark.parametrize("bad", [None, 3, [[0, 1]]])
+def test_what_is_no_tensor_is_a_type_error(bq, bad):
+    """Arguments whose dimensions are looked at first: no AttributeError."""
+    import torch
+
+    i32 = torch.zeros(2, 3, dtype=torch.int32)
+    flat = i32.view(-1)
+    given = dict(cache=torch.zeros(2, 2 * 16 * 136, dtype=torch.uint8), block_table=i32, seq_lens=flat[:2], path=i32, count=flat[:2])
+    for name in ("cache", "block_table", "path"):
+        with pytest.raises(TypeError, match=name):
+            bq.kv4_compact(**{**given, name: bad}, page_size=16, kv_heads=2, head_dim=128, max_q_len=3)
+    if bad is not None:  # None: made by the call
+        with pytest.raises(TypeError, match="mask"):
+            bq.tree_mask(i32, mask=bad)
+        with pytest.raises(TypeError, match="path"):
+            bq.tree_accept(i32, i32, i32, path=bad)
