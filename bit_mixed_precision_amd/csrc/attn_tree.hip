@@ -21,11 +21,21 @@
 // Per key and row the vector ALUs have 10.5 issue slots (the two-term fix-up 2,
 // maximum 0.5, exponent 1 + 4, both sums 2, weight with its rounding 1), the matrix
 // cores 4 D operations (an fp16 output's two-part weights: 2 slots and 2 D more).
-// 8 trees of 64 nodes x 4 heads a kv head before 8192 keys, D = 128, bf16: 121 us
-// and 8.5 for the join, of which the ALUs work for 60 %, LDS for 55 % and the
-// matrix cores for 28 % (570 TFLOP/s).  Four wavefronts a SIMD of 16 rows, which
-// fit 128 registers, are as fast at D = 128 as two of 32 rows with half the reads
-// of LDS, and faster at D = 64 (4 x 64 nodes of 8000 keys: 45 against 51 us).
+// 8 trees of 64 nodes x 4 heads a kv head before 8192 keys, D = 128, bf16: 124 us
+// and 8.6 for the join, of which the ALUs work for 63 %, LDS for 45 % and the
+// matrix cores for 27 % (554 TFLOP/s): no unit is at its limit, but all wavefronts
+// of a workgroup meet at a barrier every 64 keys.  Four wavefronts a SIMD of 16
+// rows, 128 registers each (at D = 128 with 1 to 4 more that are spilled),
+// are as fast at D = 128 as two of 32 rows with half the reads of LDS, and faster
+// at D = 64 (4 x 64 nodes of 8000 keys: 45 against 51 us).
+//
+// p sv enters the second product as one fp16 number where the output is bf16, as
+// two where it is fp16.  One is off by up to 2^-12 of itself, an eighth of what
+// rounding the output is: 16 trees of 32 nodes before up to 8192 keys, a tenth of
+// the outputs are the neighbouring bf16 number and the error against 64 bits is
+// 0.00167 of the output's norm, 0.00166 with fp32 products and the same rounding at
+// the end.  Two would take a fifth longer (107 us a call against 131; 8 x 64 of
+// 8192 116 against 140, D = 64 85 against 105).
 #include "attn_kv4.h"
 
 namespace bq {
@@ -101,7 +111,9 @@ __device__ __forceinline__ Rows tree_rows(const AttnKv4Args &p, int b)
 // units suffice (to 1.5 %), so that workgroups last equally long also where
 // lengths differ (16 trees of 32 nodes before 2 to 8192 keys, D = 128: 109 us,
 // with as many parts for each sequence 126; 3 of 61 before up to 30001 122
-// against 154).
+// against 154).  A call with no more units than sequences is not split: it lasts
+// as long as its longest sequence (40 trees of 64 nodes x 4 heads, one before 30000
+// keys and the others before 300: 1256 us).
 struct Unit {
     int b;         // sequence, -1: none
     int first, n;  // its units
@@ -645,12 +657,16 @@ hipError_t launch_w(const AttnKv4Args &p, int rt, hipStream_t s)
 
 AttnKv4Plan attn_tree_plan(int64_t batch, int64_t max_q_len, int q_heads, int kv_heads, int D, int64_t max_len)
 {
+    // max_len is the block table's width, as the lengths are device memory: a table
+    // that is wider than its sequences costs the short caches' forms (1 tree of 8 x 4
+    // rows, 700 keys 10.1 us, in a table for 32768 14.6; 64 x 4 rows 10.7 and 24.3).
     // Rows times keys from which the operands' way through LDS and the parts of
     // 16 W rows pay: 1 tree of 64 nodes x 4 heads before 8000 keys of 8 kv heads
     // (2^24) 42.6 us against attn_kv4.hip's 37.5, 30000 73.8 and 77.9, 3 x 61 of
     // 8000 67.0 and 81.1, of 30001 173 and 253; D = 64: 8 of 700 31.3 and 22.0, of
     // 2000 (2^25) 38.5 and 35.6, 1 of 128 nodes before 8000 (2^25) 39.7 and 48.8,
-    // 8 x 64 of 8192 95 and 115.
+    // 8 x 64 of 8192 95 and 115.  D = 256 has no such form: attn_kv4.hip
+    // decodes all codes for every 16 rows (8 x 64 of 8192 288 us).
     const int64_t rows = max_q_len * (q_heads / kv_heads);
     if (D > 128 || rows <= 64 || (double)batch * kv_heads * rows * max_len < (D == 128 ? 3 << 24 : 1 << 25)) {
         AttnKv4Plan a = attn_kv4_plan(batch, max_q_len, q_heads, kv_heads, D, max_len);

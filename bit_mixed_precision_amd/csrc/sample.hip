@@ -11,28 +11,33 @@
 // What is kept is a limit in the order of the tokens (key descending, index
 // ascending): its last token's key and index.
 //
-// Rows of up to 2^15 tokens are held in a workgroup's registers, in one kernel;
-// the others take four:
+// Rows of up to 32761 16-bit or 32765 fp32 logits (2^15, less what an unaligned
+// row has in its first and last vector) are held in a workgroup's registers, in one
+// kernel; the others take four:
 //   greatest   the greatest logit of every group of a row's lanes;
-//   weigh      a row with a top_k of at most as many as there are groups: no
+//   weigh      a row with a top_k of at most as many as there are groups (48 to
+//              256, by the row's length, the type and the number of rows): no
 //              token below the top_k-th greatest group can be kept, those from
 //              it on, a few more than top_k, are listed, of the few lanes only
-//              whose greatest logit is one of them.  Another row: the units
+//              whose greatest logit is one of them.  A row without top_k: the units
 //              of each eighth of an octave of weight, per workgroup and row;
 //   gather     lists the tokens of the eighth of an octave in which such a row's limit
 //              lies;
 //   draw       one workgroup a row: ends the kept ones of the listed tokens; the
 //              sums over the others give the part of the row that the drawn token
 //              is in, which is read again.
-// The one kernel takes the same steps.  Without a workspace, where a list is too
-// short (a row of equal logits), and for a greater top_k, one workgroup selects
-// over the row itself, eight bits of key at a time.
+// The one kernel takes the same steps, a top_k of up to 256 (of any number up to
+// 1024 in a row of up to 4096 tokens) by groups.  Without a workspace, where a list
+// is too short (a row of equal logits), and for a greater top_k, one workgroup
+// selects over the row itself, eight bits of key at a time.
 //
-// 1 x 32000 fp16 in the one kernel 21.7 us (in the four 28.4); 64 x 131072 bf16 with
-// top-p: greatest 8.4, weigh 15.7 (25 operations in 64 bits a token), gather 13.8,
-// draw 25.5; 487 x 100003 fp32 with all settings: 45 (4.3 TB/s), 31 (all lanes'
-// vectors, and the limit by ranks of the groups: 53), 17, 39.  One workgroup a row,
-// each over the whole of it: 139, 528 and 1083.
+// 1 x 32000 fp16 in the one kernel 21.9 us (in the four 28.4), with top-k 40 17.9,
+// with top-p or min-p alone 36 to 47; 64 x 131072 bf16 with top-p: greatest 8.6, weigh
+// 16.0 (25 operations in 64 bits a token), gather 13.9, draw 25.6; 487 x 100003 fp32
+// with all settings: 45 (4.3 TB/s), 31 (all lanes' vectors, and the limit by ranks of
+// the groups: 53), 17, 39.  One workgroup a row, each over the whole of it: 139, 528
+// and 1083, and so, past the groups, for one top_k more: 1 x 32768 fp16 has 68 groups,
+// top_k 40 21.4 us, 70 87.5; 64 x 131072 bf16 88, 70 35.5, 100 276.
 //
 // Most of a draw's time is one workgroup's way through code and dependent loads:
 // code that runs once costs the instructions' way from memory, so loops are not

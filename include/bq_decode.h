@@ -67,7 +67,9 @@ int bq_tree_mask(const int32_t *parents, const int32_t *q_start, const int32_t *
  *              row is node j; bits at or past q_len count as 0, and so does a
  *              node before the start of the cache (q_len > seq_len)
  * The other arguments, and what is said of them, are those of bq_attn_kv4;
- * a row that sees no key gives zeros (lse -infinity).
+ * a row that sees no key gives zeros (lse -infinity).  Which kernel a call takes
+ * and how it is split go by max_blocks * page_size, not by seq_lens, which the host
+ * does not read: a table no wider than its sequences is the faster one.
  * 1 <= mask_words <= BQ_TREE_MAX / 32 (BQ_ERR_SHAPE).
  */
 int bq_attn_kv4_tree(const void *q, int64_t q_stride, int dtype, const int32_t *q_start, const int32_t *seq_lens,
@@ -113,6 +115,8 @@ int64_t bq_attn_kv4_tree_workspace_bytes(int64_t batch, int64_t max_q_len, int q
  *                with 0 bytes, or fewer than bq_sample_workspace_bytes, for
  *                none (one workgroup a row then does all of its work).  Calls
  *                that share one must not overlap.
+ * A row with top_k is fastest up to some 48 to 256, by the sizes; a greater top_k
+ * costs several times as much.
  * Weights are held as multiples of 2^-F of the greatest one, F = min(46, 61 -
  * ceil(log2 vocab)), from a 64-bit exponential, and one that rounds to 0 is not
  * drawn; their sums are exact, so that the result does not depend on the order in
