@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from decode_cases import gen, logits_row
+from decode_cases import gen, logits_row, sample_wants
 from gpu_util import banner, need_gpu
 from test_gpu_decode import TYPES, check_sample, on, sample_settings
 
@@ -110,3 +110,55 @@ def test_log_probability_of_a_light_token(bq, dev, T, vocab, ws):
             want = np.log(w[:, 3] / kept).astype(np.float64)
             off = np.abs(logp.cpu().numpy().astype(np.float64) - want)
             assert (off <= 2.0 ** -24 * np.abs(want) + 1.125 * vocab * 2.0 ** -(frac + 1) + 2.0 ** -40).all(), off
+
+
+@pytest.mark.parametrize("T", TYPES + [torch.float32])
+@pytest.mark.parametrize("vocab", [1 << 24, (1 << 24) - 5])
+def test_longest_rows(bq, dev, T, vocab):
+    """Rows of 2^24 tokens, the most there may be: 3000 of them finite, the first
+    and the last among these (the others weigh nothing, so that sums are of 3000
+    terms and the bound is theirs, in units of 2^-37); then all equal, whose sums
+    are exact."""
+    banner(f"sample: longest rows {vocab} {T}")
+    g = gen(44)
+    rows, n = 2, 3000
+    at = torch.randperm(vocab - 2, generator=g)[: n - 2] + 1
+    at = torch.cat([torch.tensor([0]), at.sort()[0], torch.tensor([vocab - 1])])
+    few = torch.stack([logits_row(g, n, 5.0, T) for _ in range(rows)])
+    few[:, 0], few[:, -1] = 4.0, 4.5
+    x = torch.full((rows, vocab), -math.inf, dtype=T, device=dev)
+    x[:, at.to(dev)] = few.to(dev)
+    for filters in ("", "p", "m", "kp", "kpm"):
+        args = sample_settings(g, rows, filters, n)
+        want, lp, margin = sample_wants(few, *args)
+        assert (margin > 1.125 * n * 2.0 ** -37).all(), "an input at a border"
+        tokens, logp = bq.sample(x, *(on(v, dev) for v in args))
+        assert tokens.tolist() == at[torch.from_numpy(want).long()].tolist(), filters
+        assert (np.abs(logp.cpu().numpy() - lp) <= 2.0 ** -24 * np.abs(lp) + 1.125 * n * 2.0 ** -38 + 2.0 ** -40).all()
+    x.fill_(-1.5)
+    u = torch.tensor([0.7181, 1 - 2.0 ** -24])
+    tokens, logp = bq.sample(x, u.to(dev))
+    assert tokens.tolist() == [math.floor(float(v) * vocab) for v in u]
+    assert np.allclose(logp.cpu().numpy(), -math.log(vocab), rtol=2.0 ** -24)
+    tokens, _ = bq.sample(x, u.to(dev), None, None, torch.tensor([0.25, 0.5], device=dev))
+    assert tokens.tolist() == [math.floor(float(v) * math.ceil(p * vocab)) for v, p in zip(u, (0.25, 0.5))]
+
+
+@pytest.mark.parametrize("T", [torch.float16, torch.float32])
+def test_more_long_rows_than_workgroups_at_once(bq, dev, T):
+    """3000 rows of 33001 tokens, each with other settings: every row as one
+    workgroup over the whole of it has it, some against the definition."""
+    banner(f"sample: many long rows {T}")
+    g = gen(45)
+    rows, vocab = 3000, 33001
+    x = torch.randn(rows, vocab, generator=g).to(T)
+    u, t, k, p, m = sample_settings(g, rows, "kpm", vocab)
+    off = torch.rand(rows, 4, generator=g) < 0.4
+    t, k, p, m = t * ~off[:, 0], k * ~off[:, 1], torch.where(off[:, 2], torch.ones(rows), p), m * ~off[:, 3]
+    moved = [v.to(dev) for v in (u, t, k, p, m)]
+    y = x.to(dev)
+    a = bq.sample(y, *moved)
+    b = bq.sample(y, *moved, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    some = slice(0, rows, 100)
+    check_sample((a[0][some], a[1][some]), x[some], *(v[some] for v in (u, t, k, p, m)))

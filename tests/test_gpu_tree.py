@@ -8,7 +8,7 @@ from decode_cases import gen, trees
 from gpu_util import banner, need_gpu
 from oracle import decode, layer
 from test_gpu_decode import TYPES, i32
-from test_gpu_layer import make_cache, tables
+from test_gpu_layer import half_step, make_cache, tables, within
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,45 @@ def test_attn_kv4_tree_repeats_itself(bq, dev, T, d, nodes, wide):
         torch.cuda.synchronize()
         first = first or [x.clone() for x in got]
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("nodes", [3, 300])
+def test_attn_kv4_tree_without_pages(bq, dev, T, nodes):
+    """A table of no columns over a cache of no pages: no row sees a key."""
+    banner(f"tree attention without pages {nodes} {T}")
+    hq, hkv, d, page, B = 8, 2, 128, 16, 2
+    _, _, mask, _ = trees(gen(53), [nodes] * B)
+    q = torch.randn(B * nodes, hq, d, generator=gen(54)).to(T).to(dev)
+    cache = torch.empty(0, bq.kv4_page_bytes(hkv, d, page), dtype=torch.uint8, device=dev)
+    tab = torch.empty(B, 0, dtype=torch.int32, device=dev)
+    out, lse = bq.attn_kv4_tree(q, cache, tab, i32([nodes, 900], dev), page, hkv, mask.to(dev), return_lse=True)
+    assert not out.any() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("T", TYPES)
+@pytest.mark.parametrize("wide", [1, 4096])
+def test_attn_kv4_tree_more_nodes_than_are_computed(bq, dev, T, wide):
+    """2000 nodes behind one prefix, the first 1024 of them computed: their rows
+    are those of a tree whose other nodes no row sees, the others' stay."""
+    banner(f"tree attention 1024 of 2000 nodes {wide} {T}")
+    g = gen(55)
+    hq, hkv, d, page, nodes, prefix = 2, 2, 64, 16, 2000, 77
+    n = prefix + nodes
+    cache = make_cache(g, -(-n // page), hkv, d, page, T)
+    tab = torch.cat([tables(g, [n], page, -(-n // page)), torch.full((1, wide), -1, dtype=torch.int32)], 1)
+    _, see, mask, _ = trees(g, [1024])
+    words = torch.full((nodes, 32), -1, dtype=torch.int32)
+    words[:1024] = mask
+    q = torch.randn(nodes, hq, d, generator=g).to(T)
+    out = torch.full(q.shape, 7.0, dtype=T, device=dev)
+    lse = torch.full(q.shape[:2], 7.0, device=dev)
+    bq.attn_kv4_tree(q.to(dev), cache.flat().to(dev), tab.to(dev), i32([n], dev), page, hkv, words.to(dev), None, i32([0, nodes], dev),
+                     1024, 0, out, lse)
+    whole = torch.zeros(nodes, nodes, dtype=torch.bool)
+    whole[:1024, :1024] = see[0]
+    want, _, size, delta = decode.attention_tree(q, cache, tab, [n], [0, nodes], [whole], d ** -0.5)
+    r = (2.0 ** -20 if T == torch.float16 else 2.0 ** -10 + 2.0 ** -20) + n * 2.0 ** -24
+    tol = half_step(T) * want.abs() + (2 * delta[..., None] + r) * size * (1 + 2.0 ** -6) + 2.0 ** -25
+    within(out[:1024], want[:1024], tol[:1024], "first nodes")
+    assert (out[1024:] == 7).all() and (lse[1024:] == 7).all()
